@@ -518,6 +518,123 @@ int nvfp4_mx_gemm(const nvfp4_tensor* a, const nvfp4_tensor* b, void* c, int64_t
  */
 int nvfp4_mfma_sustain(int64_t blocks, int64_t iters, int32_t operands, float* out, void* stream);
 
+/*
+ * nvfp4_bf16_grouped_gemm -- nvfp4_bf16_gemm for a linear layer of E experts,
+ * its tokens sorted by expert: the three passes with one weight per expert,
+ * bf16 operands, fp32 accumulation.  Expert e owns rows ends[e - 1] ..
+ * ends[e] - 1 of X and dY (0 before the first); an expert may own none.
+ *   FPROP: a = X  (T x K), b = W (E x N x K)
+ *          c[t, n] = sum_k x[t,k] * w[e(t),n,k]                (T x N)
+ *   DGRAD: a = dY (T x N), b = W (E x N x K)
+ *          c[t, k] = sum_n dy[t,n] * w[e(t),n,k]               (T x K)
+ *   WGRAD: a = dY (T x N), b = X (T x K)
+ *          c[e, n, k] = sum_{t of e} dy[t,n] * x[t,k]          (E x N x K)
+ * Rows from ends[E - 1] on belong to no expert: they enter no sum, and
+ * FPROP and DGRAD write zeros for them.  WGRAD writes zeros for an expert
+ * without rows.
+ *   ends      device int32, E values, read by the kernel (the host does not
+ *             see the routing).  They should not decrease nor pass T; a
+ *             value outside [0, T] counts as the nearest bound and one below
+ *             an earlier value as that value, so no row out of range is
+ *             touched.
+ *   a, lda    as for nvfp4_bf16_gemm.
+ *   b         W: expert e at b + e * stride_b elements (a multiple of 8), its
+ *             rows ldb apart; WGRAD: X, stride_b ignored.
+ *   E, T, N, K  >= 0 and below 2^31; N and K multiples of 8; T any.
+ *   c, ldc, c_dtype  as for nvfp4_gemm; WGRAD: expert e at c + e * stride_c
+ *             elements (a multiple of 4), its rows ldc apart; otherwise
+ *             stride_c is ignored.
+ * Returns NVFP4_OK or a negative status; nothing is enqueued on failure.
+ */
+int nvfp4_bf16_grouped_gemm(int32_t pass, const void* a, int64_t lda, const void* b, int64_t ldb,
+                            int64_t stride_b, const int32_t* ends, int64_t E, int64_t T, int64_t N,
+                            int64_t K, void* c, int64_t ldc, int64_t stride_c, int32_t c_dtype,
+                            void* stream);
+
+/* One tensor of an AdamW step (device pointers; n elements each, contiguous). */
+typedef struct nvfp4_adamw_tensor {
+    void* p;          /* parameters, fp32 or bf16, updated */
+    const void* g;    /* gradients, fp32 or bf16 */
+    void* m;          /* first moment: fp32, or E4M3 codes */
+    void* v;          /* second moment: fp32, or E4M3 codes of its square root */
+    float* m_scale;   /* 8-bit states: one scale per 128 elements (ceil(n / 128) values) */
+    float* v_scale;
+    uint16_t* copy;   /* bf16 copy of the updated fp32 parameters, or NULL */
+    int64_t n;
+} nvfp4_adamw_tensor;
+
+/*
+ * nvfp4_adamw -- one step of AdamW over `count` tensors, in place:
+ *   g' = g * grad_scale
+ *   m  = beta1 m + (1 - beta1) g'
+ *   v  = beta2 v + (1 - beta2) g'^2
+ *   p  = p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32 (the factors of the step are rounded once from double).
+ *   tensors     HOST array; it is read before the call returns.  The tensors
+ *               of one step must not overlap.
+ *   p_dtype, g_dtype  NVFP4_OUT_FP32 or NVFP4_OUT_BF16, for every tensor
+ *               (bf16 parameters are rounded to nearest even; a copy needs
+ *               fp32 parameters, NVFP4_ERR_MODE otherwise).
+ *   state_bits  32: m and v are fp32.
+ *               8: m and r = sqrt(v) are OCP E4M3 codes times their block's
+ *               scale, blocks of 128 consecutive elements of the tensor.  The
+ *               scale is the smallest power of two (not below 2^-126) for
+ *               which no value of the block passes 448; codes are rounded to
+ *               nearest even, and a nonzero r to at least 2^-9 of the scale.
+ *               The update uses m and v before they are rounded to 8 bits.
+ *               All-zero codes with any finite scale are the initial state.
+ *   step        >= 1, the number of this step (the bias corrections).
+ *   beta1, beta2 in [0, 1), eps >= 0, lr and weight_decay finite
+ *               (NVFP4_ERR_MODE otherwise).
+ *   grad_scale  optional device float that every gradient is multiplied by
+ *               (clipping, loss scaling).  If it is not finite the step
+ *               writes nothing.
+ * A gradient that is not finite makes its own element NaN (in 8 bits its
+ * block's scale too grows to its largest).  Pointers need the alignment of
+ * their type; with 16 bytes for fp32, 8 for bf16 and 4 for codes the wide
+ * accesses are used.  A captured call replays the scalars it was captured
+ * with.  Returns NVFP4_OK or a negative status; nothing is enqueued on
+ * failure.
+ */
+int nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t p_dtype, int32_t g_dtype,
+                int32_t state_bits, int64_t step, double lr, double beta1, double beta2, double eps,
+                double weight_decay, const float* grad_scale, void* stream);
+
+/*
+ * nvfp4_i8_quantize -- symmetric 8-bit integer quantisation of the rows of a
+ * bf16 matrix (the tokens of an activation, the output channels of a weight):
+ *   scale[r] = max_k |x[r, k]| / 127
+ *   code[r, k] = 127 x[r, k] / max_k |x[r, k]| rounded to nearest even
+ * A row of zeros has scale 0 and codes 0.
+ *   x         device bf16, rows x ld_x elements; 16-byte aligned, ld_x >= cols
+ *             and a multiple of 8.
+ *   cols      >= 0 and a multiple of 16.
+ *   codes     device int8, rows x ld_codes; 16-byte aligned, ld_codes >= cols
+ *             and a multiple of 16.
+ *   scales    device float, rows values.
+ * Returns NVFP4_OK or a negative status; nothing is enqueued on failure.
+ */
+int nvfp4_i8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x, int8_t* codes,
+                      int64_t ld_codes, float* scales, void* stream);
+
+/*
+ * nvfp4_i8_gemm -- the product of two int8 matrices with a scale for each row
+ * of both (tokens of a, output channels of b):
+ *   c[m, n] = a_scales[m] * b_scales[n] * sum_k a[m, k] * b[n, k]
+ * The sum is exact in int32; it is converted to fp32 and multiplied by the
+ * two scales in that order, then rounded once more for a bf16 output.
+ *   a, b      device int8, M x lda and N x ldb; 16-byte aligned, lda and ldb
+ *             multiples of 16 and at least K.
+ *   K         a multiple of 16 below 2^17 (so that no sum leaves int32).
+ *   M, N      any, below 2^31.
+ *   c, ldc, c_dtype  as for nvfp4_gemm.
+ * Returns NVFP4_OK or a negative status; nothing is enqueued on failure.
+ */
+int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int8_t* b, int64_t ldb,
+                  const float* b_scales, int64_t M, int64_t N, int64_t K, void* c, int64_t ldc,
+                  int32_t c_dtype, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* nvfp4_status_string(int32_t status);
 

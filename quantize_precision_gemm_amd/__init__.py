@@ -23,6 +23,7 @@ __all__ = [
     "nvfp4_rht_sign_mask", "nvfp4_amax", "nvfp4_bf16_gemm", "nvfp4_mx_quantize",
     "nvfp4_mx_gemm", "nvfp4_rht_quantize_sized", "nvfp4_rht_signs64", "nvfp4_quantize_rht_rows", "BLOCK_MX32", "MX_ROWS", "MX_COLS", "MX_COLS_RHT", "nvfp4_gemm_fp8blk", "nvfp4_gemm_amax", "nvfp4_gemm_split", "nvfp4_gemm_split_workspace", "nvfp4_gemm_split_noalloc",
     "nvfp4_mfma_sustain", "MFMA_SUSTAIN_DECODED", "MFMA_SUSTAIN_RANDOM", "MFMA_SUSTAIN_FP4",
+    "nvfp4_bf16_grouped_gemm", "AdamWGroup", "nvfp4_adamw", "I8Tensor", "nvfp4_i8_quantize", "nvfp4_i8_gemm",
     "LAYOUT_ROW_MAJOR", "LAYOUT_INTERLEAVED", "interleave_codes", "deinterleave_codes",
     "lib_path", "load_library",
 ]
@@ -67,6 +68,12 @@ class _Desc(ctypes.Structure):
         ("ld_codes_t", ctypes.c_int64), ("ld_scales_t", ctypes.c_int64),
         ("block", ctypes.c_int32), ("layout", ctypes.c_int32),
     ]
+
+
+class _AdamWTensor(ctypes.Structure):
+    """Mirror of struct nvfp4_adamw_tensor."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("p", "g", "m", "v", "m_scale", "v_scale", "copy")] + \
+        [("n", ctypes.c_int64)]
 
 
 def load_library():
@@ -117,6 +124,16 @@ def load_library():
         L.nvfp4_rht_sign_mask.restype = u32
         L.nvfp4_mfma_sustain.argtypes = [i64, i64, i32, P, P]
         L.nvfp4_mfma_sustain.restype = ctypes.c_int
+        L.nvfp4_bf16_grouped_gemm.argtypes = [i32, P, i64, P, i64, i64, P, i64, i64, i64, i64, P, i64, i64,
+                                              i32, P]
+        L.nvfp4_bf16_grouped_gemm.restype = ctypes.c_int
+        f64 = ctypes.c_double
+        L.nvfp4_adamw.argtypes = [P, i64, i32, i32, i32, i64, f64, f64, f64, f64, f64, P, P]
+        L.nvfp4_adamw.restype = ctypes.c_int
+        L.nvfp4_i8_quantize.argtypes = [P, i64, i64, i64, P, i64, P, P]
+        L.nvfp4_i8_quantize.restype = ctypes.c_int
+        L.nvfp4_i8_gemm.argtypes = [P, i64, P, P, i64, P, i64, i64, i64, P, i64, i32, P]
+        L.nvfp4_i8_gemm.restype = ctypes.c_int
         L.nvfp4_status_string.argtypes = [i32]
         L.nvfp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -644,6 +661,268 @@ def nvfp4_bf16_gemm(pass_, a, b, out_dtype=torch.bfloat16, out=None, stream=None
     st = load_library().nvfp4_bf16_gemm(pass_, _ptr(a), ld(a), _ptr(b), ld(b), M, N, K,
                                         _ptr(out), ld(out), dt, _stream(stream))
     _check(st, "nvfp4_bf16_gemm")
+    return out
+
+
+def _out_code(dtype, what="output"):
+    if dtype == torch.float32:
+        return OUT_FP32
+    if dtype == torch.bfloat16:
+        return OUT_BF16
+    raise TypeError(f"{what}: dtype {dtype}, expected float32 or bfloat16")
+
+
+def _pitch(x, multiple=8):
+    """Row pitch of a matrix; the stride of one row or none means nothing."""
+    return x.stride(0) if x.shape[0] > 1 and x.shape[1] > 0 else _round_up(x.shape[1], multiple)
+
+
+def _for_stream(t, stream):
+    """A tensor made here for work on `stream` keeps its memory until that work is done."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _check_bf16_experts(w, what):
+    if not (isinstance(w, torch.Tensor) and w.is_cuda and w.dtype == torch.bfloat16 and w.dim() == 3):
+        raise TypeError(f"{what}: expected a 3-D bfloat16 CUDA tensor (experts, rows, columns)")
+    if w.numel() > 0 and w.stride(2) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+
+
+def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=None, stream=None):
+    """GEMM of a linear layer of E experts kept in bf16, its rows sorted by
+    expert (see nvfp4_bf16_grouped_gemm in nvfp4.h).
+
+    FPROP: a = X (T x K), b = W (E x N x K) -> T x N
+    DGRAD: a = dY (T x N), b = W (E x N x K) -> T x K
+    WGRAD: a = dY (T x N), b = X (T x K) -> E x N x K
+    ends: int32 device tensor (E): one past the last row of each expert.
+    """
+    _check_bf16(a)
+    dev = a.device
+    if not isinstance(ends, torch.Tensor) or ends.dtype != torch.int32 or ends.dim() != 1 or \
+            not _same_device(ends.device, dev) or not ends.is_contiguous():
+        raise ValueError("ends: expected a contiguous 1-D int32 tensor on the operands' device")
+    E, T = ends.shape[0], a.shape[0]
+    if pass_ == WGRAD:
+        _check_bf16(b)
+        if b.shape[0] != T:
+            raise ValueError(f"b: {b.shape[0]} rows, a has {T}")
+        N, K = a.shape[1], b.shape[1]
+        shape = (E, N, K)
+        ldb, stride_b = _pitch(b), 0
+    elif pass_ in (FPROP, DGRAD):
+        _check_bf16_experts(b, "b")
+        if b.shape[0] != E:
+            raise ValueError(f"b: {b.shape[0]} experts, ends has {E}")
+        N, K = b.shape[1], b.shape[2]
+        if a.shape[1] != (K if pass_ == FPROP else N):
+            raise ValueError(f"a: {a.shape[1]} columns do not fit b's {tuple(b.shape)}")
+        shape = (T, N if pass_ == FPROP else K)
+        # the strides of a dimension of one element or none mean nothing
+        ldb = b.stride(1) if N > 1 and K > 0 else _round_up(K, 8)
+        stride_b = b.stride(0) if E > 1 and b.numel() > 0 else N * ldb
+    else:
+        raise ValueError(f"unknown pass {pass_}")
+    if not _same_device(b.device, dev):
+        raise ValueError(f"b: on {b.device}, expected {dev}")
+    if out is None:
+        if N % 8 or K % 8:
+            raise ValueError("N and K must be multiples of 8")
+        out = _for_stream(torch.empty(shape, dtype=out_dtype, device=dev), stream)
+    stride_c = 0
+    if pass_ == WGRAD:
+        if not isinstance(out, torch.Tensor) or tuple(out.shape) != shape or not _same_device(out.device, dev):
+            raise ValueError(f"out: expected a tensor of shape {shape} on {dev}")
+        if out.numel() > 0 and out.stride(2) != 1:
+            raise TypeError("output must have a contiguous last dimension")
+        ldc = out.stride(1) if N > 1 and K > 0 else _round_up(K, 4)
+        stride_c = out.stride(0) if E > 1 and out.numel() > 0 else N * ldc
+        if ldc < K or stride_c < (N - 1) * ldc + K and out.numel() > 0:
+            raise ValueError("out: rows or experts overlap")
+    else:
+        _check_gemm_out(out, shape, dev)
+        ldc = _pitch(out, 4)
+    st = load_library().nvfp4_bf16_grouped_gemm(pass_, _ptr(a), _pitch(a), _ptr(b), ldb, stride_b, _ptr(ends), E, T, N,
+                                                K, _ptr(out), ldc, stride_c, _out_code(out.dtype), _stream(stream))
+    _check(st, "nvfp4_bf16_grouped_gemm")
+    return out
+
+
+class AdamWGroup:
+    """The tensors of one AdamW step and where their states lie, made once.
+
+    params   contiguous float32 or bfloat16 tensors, updated in place (any shapes)
+    grads    float32 or bfloat16 tensors of the same sizes; the buffers that every
+             step reads
+    m, v     float32 tensors of the same sizes (32-bit states), or float8_e4m3fn
+             ones (8-bit states: v holds the root of the second moment)
+    m_scales, v_scales  float32, ceil(n / 128) values per tensor (8-bit states only)
+    copies   bfloat16 copies of float32 params written by the step, or None; an
+             entry may be None
+
+    The group holds references to its tensors; all of one kind have one dtype.
+    """
+
+    BLOCK = 128  # elements that share the scale of an 8-bit state
+
+    def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, copies=None):
+        k = len(params)
+        self.params, self.grads, self.m, self.v = list(params), list(grads), list(m), list(v)
+        eight = m_scales is not None or v_scales is not None
+        if eight and (m_scales is None or v_scales is None):
+            raise ValueError("8-bit states need both m_scales and v_scales")
+        self.m_scales = list(m_scales) if eight else [None] * k
+        self.v_scales = list(v_scales) if eight else [None] * k
+        self.copies = list(copies) if copies is not None else [None] * k
+        self.bits = 8 if eight else 32
+        lists = (self.params, self.grads, self.m, self.v, self.m_scales, self.v_scales, self.copies)
+        if any(len(x) != k for x in lists):
+            raise ValueError("the lists of an AdamW group have one entry per tensor")
+        state = torch.float8_e4m3fn if eight else torch.float32
+        self.p_dtype = _out_code(self.params[0].dtype, "params") if k else OUT_FP32
+        self.g_dtype = _out_code(self.grads[0].dtype, "grads") if k else OUT_FP32
+        self.device = self.params[0].device if k else None
+        self._table = (_AdamWTensor * max(k, 1))()
+        for i in range(k):
+            n = self.params[i].numel()
+            blocks = -(-n // self.BLOCK)
+            wanted = (("params", self.params[i], self.params[0].dtype, n), ("grads", self.grads[i], self.grads[0].dtype, n),
+                      ("m", self.m[i], state, n), ("v", self.v[i], state, n),
+                      ("m_scales", self.m_scales[i], torch.float32, blocks),
+                      ("v_scales", self.v_scales[i], torch.float32, blocks),
+                      ("copies", self.copies[i], torch.bfloat16, n))
+            for what, t, dtype, count in wanted:
+                if t is None and (what == "copies" or not eight and what.endswith("_scales")):
+                    continue
+                self._check_tensor(f"{what}[{i}]", t, dtype, count)
+            if self.copies[i] is not None and self.p_dtype != OUT_FP32:
+                raise ValueError("copies are made of float32 params")
+            row = self._table[i]
+            for field, (_, t, _, _) in zip(("p", "g", "m", "v", "m_scale", "v_scale", "copy"), wanted):
+                setattr(row, field, None if t is None else t.data_ptr())
+            row.n = n
+        self.count = k
+
+    def _check_tensor(self, what, t, dtype, count):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{what}: expected a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+        if t.device != self.device:
+            raise ValueError(f"{what}: on {t.device}, expected {self.device}")
+        if t.numel() != count:
+            raise ValueError(f"{what}: {t.numel()} elements, expected {count}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: must be contiguous")
+
+    @classmethod
+    def with_states(cls, params, grads, bits=32, copies=None):
+        """A group with new states of 0 (bits: 32 or 8)."""
+        if bits not in (8, 32):
+            raise ValueError(f"states of {bits} bits")
+        if bits == 32:
+            def zeros():
+                return [torch.zeros(p.numel(), dtype=torch.float32, device=p.device) for p in params]
+            return cls(params, grads, zeros(), zeros(), copies=copies)
+
+        def codes():
+            return [torch.zeros(p.numel(), dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn)
+                    for p in params]
+
+        def scales():
+            return [torch.zeros(-(-p.numel() // cls.BLOCK), dtype=torch.float32, device=p.device) for p in params]
+        return cls(params, grads, codes(), codes(), scales(), scales(), copies)
+
+
+def nvfp4_adamw(group, step, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, grad_scale=None, stream=None):
+    """One AdamW step over an AdamWGroup, in place (see nvfp4_adamw in nvfp4.h).
+
+    step counts from 1; grad_scale: optional one-element float32 device tensor
+    that every gradient is multiplied by (not finite: the step writes nothing).
+    """
+    if not isinstance(group, AdamWGroup):
+        raise TypeError("group: expected an AdamWGroup")
+    if grad_scale is not None:
+        if not isinstance(grad_scale, torch.Tensor) or grad_scale.dtype != torch.float32 or grad_scale.numel() != 1:
+            raise TypeError("grad_scale: expected a one-element float32 tensor")
+        if group.device is not None and not _same_device(grad_scale.device, group.device):
+            raise ValueError(f"grad_scale: on {grad_scale.device}, expected {group.device}")
+    if group.count == 0:
+        return
+    st = load_library().nvfp4_adamw(group._table, group.count, group.p_dtype, group.g_dtype, group.bits, step, lr,
+                                    beta1, beta2, eps, weight_decay, _ptr(grad_scale), _stream(stream))
+    _check(st, "nvfp4_adamw")
+
+
+class I8Tensor:
+    """An int8 matrix with one scale per row: codes int8 [rows, cols] (rows
+    a multiple of 16 bytes apart), scales float32 [rows]; the value of an
+    element is code * scale."""
+
+    def __init__(self, codes, scales):
+        self.codes, self.scales = codes, scales
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+
+def _check_i8(t, what):
+    if not isinstance(t, I8Tensor):
+        raise TypeError(f"{what}: expected an I8Tensor")
+    c, s = t.codes, t.scales
+    if not (isinstance(c, torch.Tensor) and c.is_cuda and c.dtype == torch.int8 and c.dim() == 2):
+        raise TypeError(f"{what}.codes: expected a 2-D int8 CUDA tensor")
+    if c.numel() > 0 and c.stride(1) != 1:
+        raise ValueError(f"{what}.codes: the last dimension must be contiguous")
+    if not isinstance(s, torch.Tensor) or s.dtype != torch.float32 or s.dim() != 1 or not s.is_contiguous():
+        raise TypeError(f"{what}.scales: expected a contiguous 1-D float32 tensor")
+    if s.shape[0] != c.shape[0]:
+        raise ValueError(f"{what}.scales: {s.shape[0]} values for {c.shape[0]} rows")
+    if s.device != c.device:
+        raise ValueError(f"{what}.scales: on {s.device}, expected {c.device}")
+
+
+def nvfp4_i8_quantize(x, out=None, stream=None):
+    """Rows of a bf16 matrix as int8 codes with one scale per row (see
+    nvfp4_i8_quantize in nvfp4.h): an I8Tensor."""
+    _check_bf16(x)
+    rows, cols = x.shape
+    if out is None:
+        out = I8Tensor(_for_stream(torch.empty((rows, cols), dtype=torch.int8, device=x.device), stream),
+                       _for_stream(torch.empty(rows, dtype=torch.float32, device=x.device), stream))
+    _check_i8(out, "out")
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError(f"out: shape {tuple(out.shape)}, expected {(rows, cols)}")
+    if not _same_device(out.codes.device, x.device):
+        raise ValueError(f"out: on {out.codes.device}, expected {x.device}")
+    st = load_library().nvfp4_i8_quantize(_ptr(x), rows, cols, _pitch(x), _ptr(out.codes), _pitch(out.codes, 16),
+                                          _ptr(out.scales), _stream(stream))
+    _check(st, "nvfp4_i8_quantize")
+    return out
+
+
+def nvfp4_i8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
+    """a (M x K) times b (N x K) transposed, both I8Tensors (see nvfp4_i8_gemm
+    in nvfp4.h): M x N, float32 or bfloat16."""
+    _check_i8(a, "a")
+    _check_i8(b, "b")
+    (M, K), N = a.shape, b.shape[0]
+    dev = a.codes.device
+    if b.shape[1] != K:
+        raise ValueError(f"b: {b.shape[1]} columns, a has {K}")
+    if not _same_device(b.codes.device, dev):
+        raise ValueError(f"b: on {b.codes.device}, expected {dev}")
+    if out is None:
+        out = _for_stream(_new_gemm_out((M, N), out_dtype, dev), stream)
+    _check_gemm_out(out, (M, N), dev)
+    st = load_library().nvfp4_i8_gemm(_ptr(a.codes), _pitch(a.codes, 16), _ptr(a.scales), _ptr(b.codes),
+                                      _pitch(b.codes, 16), _ptr(b.scales), M, N, K, _ptr(out), _pitch(out, 4),
+                                      _out_code(out.dtype), _stream(stream))
+    _check(st, "nvfp4_i8_gemm")
     return out
 
 

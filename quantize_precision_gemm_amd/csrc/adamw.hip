@@ -1,0 +1,246 @@
+// adamw.hip -- one AdamW step over many tensors on gfx950, with the two
+// moments held in fp32 or in 8 bits.
+//
+// With the gradient g (times the optional device factor grad_scale):
+//   m = beta1 m + (1 - beta1) g          v = beta2 v + (1 - beta2) g^2
+//   p = p (1 - lr decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+// all in fp32, every operation rounded once (the factors that depend on the
+// step alone are rounded from double on the host).
+//
+// 8-bit states: m and r = sqrt(v) are OCP E4M3 values times one fp32 power of
+// two per block of 128 elements, the smallest for which no value passes 448;
+// the root needs half the exponent range of v.  A root that is not zero is
+// held as at least the smallest E4M3 value (2^-9 of its scale), so that an
+// element with a first moment is never divided by eps alone.  The update uses
+// m and r before they are rounded to 8 bits.
+//
+// Every element is read and written once: the step is bound by HBM traffic
+// (30 bytes an element with fp32 states, fp32 gradients and a bf16 copy,
+// 18.1 with 8-bit states).
+#include "internal.hpp"
+#include "nvfp4_device.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = kThreads * 4;  // elements of one workgroup
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16x2_rne(float a, float b)
+{
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
+}
+
+// 4 elements from element i; those past n read as zero.
+__device__ __forceinline__ void load4(float (&y)[4], const void* base, int64_t i, int64_t n, bool vec, float)
+{
+    const float* p = static_cast<const float*>(base) + i;
+    if (vec && i + 4 <= n) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = i + k < n ? p[k] : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void load4(float (&y)[4], const void* base, int64_t i, int64_t n, bool vec, uint16_t)
+{
+    const uint16_t* p = static_cast<const uint16_t*>(base) + i;
+    if (vec && i + 4 <= n) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        y[0] = __uint_as_float(v.x << 16), y[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        y[2] = __uint_as_float(v.y << 16), y[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = i + k < n ? bf16_to_f32(p[k]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void store4(const float (&y)[4], void* base, int64_t i, int64_t n, bool vec, float)
+{
+    float* p = static_cast<float*>(base) + i;
+    if (vec && i + 4 <= n) {
+        *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < n) p[k] = y[k];
+    }
+}
+
+__device__ __forceinline__ void store4(const float (&y)[4], void* base, int64_t i, int64_t n, bool vec, uint16_t)
+{
+    uint16_t* p = static_cast<uint16_t*>(base) + i;
+    const uint32_t w[2] = {bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3])};
+    if (vec && i + 4 <= n) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < n) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+    }
+}
+
+// 4 E4M3 codes from element i (past n: zero).
+__device__ __forceinline__ uint32_t load_codes(const void* base, int64_t i, int64_t n, bool vec)
+{
+    const uint8_t* p = static_cast<const uint8_t*>(base) + i;
+    if (vec && i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p);
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (i + k < n) w |= (uint32_t)p[k] << (8 * k);
+    return w;
+}
+
+__device__ __forceinline__ void store_codes(uint32_t w, void* base, int64_t i, int64_t n, bool vec)
+{
+    uint8_t* p = static_cast<uint8_t*>(base) + i;
+    if (vec && i + 4 <= n) {
+        *reinterpret_cast<uint32_t*>(p) = w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < n) p[k] = (uint8_t)(w >> (8 * k));
+    }
+}
+
+__device__ __forceinline__ void decode4(float (&y)[4], uint32_t w, float scale)
+{
+    y[0] = __builtin_amdgcn_cvt_f32_fp8((int)w, 0) * scale;
+    y[1] = __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * scale;
+    y[2] = __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * scale;
+    y[3] = __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * scale;
+}
+
+// Max over the 32 lanes that hold one block of 128 elements.
+__device__ __forceinline__ uint32_t block_max(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));   // lanes ^ 1
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));   // lanes ^ 2
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));  // mirror in 8
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));  // mirror in 16
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max((uint32_t)r[0], (uint32_t)r[1]);
+}
+
+// The 4 values as E4M3 codes and their block's scale: 2^j, j the smallest for
+// which max |y| <= 448 * 2^j (not below 2^-126; a mantissa above 1.75 takes
+// the next power).  Magnitudes compare as integers, so a NaN counts as the
+// largest and the scale stays finite; what passes 448 is held as NaN.
+template <bool kRoot>
+__device__ __forceinline__ uint32_t encode4(const float (&y)[4], float& scale)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max(top, __float_as_uint(y[k]) & 0x7FFFFFFFu);
+    top = block_max(top);
+    int e = (int)((top + 0x1FFFFFu) >> 23) - 8;
+    e = min(max(e, 1), 246);
+    scale = __uint_as_float((uint32_t)e << 23);
+    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+    float q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float t = y[k] * inv;
+        if (kRoot) t = t > 0.0f ? __builtin_fmaxf(t, 0x1p-9f) : t;
+        q[k] = __builtin_fabsf(t) <= 448.0f ? t : __uint_as_float(0x7FC00000u);
+    }
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+    return (uint32_t)w;
+}
+
+}  // namespace
+
+// One workgroup updates one chunk of 1024 elements of one tensor; the tensor
+// is found from the first chunk of each, held in the kernel's arguments.
+template <class P, class G, bool k8>
+__global__ __launch_bounds__(kThreads) void k_adamw(AdamWArgs a)
+{
+    float gs = 1.0f;
+    if (a.grad_scale) {
+        gs = *a.grad_scale;
+        if ((__float_as_uint(gs) & 0x7F800000u) == 0x7F800000u) return;  // not finite: the step is left out
+    }
+    const int lane = threadIdx.x & 63;
+    const uint32_t mine = a.first[min(lane, a.count)];
+    const int at = __builtin_amdgcn_readfirstlane(
+        (int)__popcll(__ballot(lane < a.count && mine <= blockIdx.x)) - 1);
+    const AdamWTensor t = a.t[at];
+    const int64_t n = t.n;
+    const bool vec = t.vec != 0;
+    const int64_t i = (int64_t)(blockIdx.x - a.first[at]) * kChunk + 4 * threadIdx.x;
+
+    float p[4], g[4], m[4], v[4], r[4];
+    load4(p, t.p, i, n, vec, P());
+    load4(g, t.g, i, n, vec, G());
+    const int64_t nb = (n + 127) >> 7, b = i >> 7;
+    if constexpr (k8) {
+        const uint32_t cm = load_codes(t.m, i, n, vec), cv = load_codes(t.v, i, n, vec);
+        const float sm = b < nb ? t.m_scale[b] : 0.0f, sv = b < nb ? t.v_scale[b] : 0.0f;
+        decode4(m, cm, sm);
+        decode4(r, cv, sv);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = r[k] * r[k];
+    } else {
+        load4(m, t.m, i, n, vec, float());
+        load4(v, t.v, i, n, vec, float());
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float gk = g[k] * gs;
+        m[k] = a.beta1 * m[k] + a.rest1 * gk;
+        v[k] = a.beta2 * v[k] + a.rest2 * (gk * gk);
+        r[k] = sqrtf(v[k]);
+        p[k] = p[k] * a.keep - a.rate * (m[k] / (r[k] * a.root_corr + a.eps));
+    }
+    store4(p, t.p, i, n, vec, P());
+    if (t.copy) store4(p, t.copy, i, n, vec, uint16_t());
+    if constexpr (k8) {
+        float sm, sv;
+        const uint32_t cm = encode4<false>(m, sm), cv = encode4<true>(r, sv);
+        store_codes(cm, t.m, i, n, vec);
+        store_codes(cv, t.v, i, n, vec);
+        if ((lane & 31) == 0 && b < nb) {
+            t.m_scale[b] = sm;
+            t.v_scale[b] = sv;
+        }
+    } else {
+        store4(m, t.m, i, n, vec, float());
+        store4(v, t.v, i, n, vec, float());
+    }
+}
+
+namespace {
+
+template <class P, class G>
+void launch_bits(const AdamWArgs& a, uint32_t chunks, bool eight, hipStream_t s)
+{
+    if (eight)
+        hipLaunchKernelGGL((k_adamw<P, G, true>), dim3(chunks), dim3(kThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((k_adamw<P, G, false>), dim3(chunks), dim3(kThreads), 0, s, a);
+}
+
+}  // namespace
+
+int64_t adamw_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
+
+void launch_adamw(const AdamWArgs& a, bool p_bf16, bool g_bf16, bool eight, hipStream_t s)
+{
+    const uint32_t chunks = a.first[a.count];
+    if (chunks == 0) return;
+    if (p_bf16 && g_bf16) launch_bits<uint16_t, uint16_t>(a, chunks, eight, s);
+    else if (p_bf16) launch_bits<uint16_t, float>(a, chunks, eight, s);
+    else if (g_bf16) launch_bits<float, uint16_t>(a, chunks, eight, s);
+    else launch_bits<float, float>(a, chunks, eight, s);
+}
+
+}  // namespace nvfp4

@@ -3,6 +3,7 @@
 // enqueued; a failed check returns a negative status and launches nothing.
 #include <stdint.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "nvfp4.h"
@@ -632,6 +633,150 @@ int nvfp4_mfma_sustain(int64_t blocks, int64_t iters, int32_t operands, float* o
     if (operands < 0 || operands > 2) return NVFP4_ERR_MODE;
     if (!aligned(out, 4)) return NVFP4_ERR_ALIGN;
     nvfp4::launch_mfma_sustain(blocks, iters, operands, out, static_cast<hipStream_t>(stream));
+    return launch_status();
+}
+
+}  // extern "C"
+
+namespace {
+
+// nvfp4_adamw: one launch takes up to kAdamWTensors tensors.
+bool adamw_vec(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight)
+{
+    return aligned(t.p, p_bf16 ? 8 : 16) && aligned(t.g, g_bf16 ? 8 : 16) && aligned(t.m, eight ? 4 : 16) &&
+           aligned(t.v, eight ? 4 : 16) && aligned(t.copy, 8);
+}
+
+int check_adamw(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight)
+{
+    if (t.n < 0) return NVFP4_ERR_SHAPE;
+    if (t.n > 0 && (!t.p || !t.g || !t.m || !t.v)) return NVFP4_ERR_NULL;
+    if (t.n > 0 && eight && (!t.m_scale || !t.v_scale)) return NVFP4_ERR_NULL;
+    if (t.copy && p_bf16) return NVFP4_ERR_MODE;
+    if (!aligned(t.p, p_bf16 ? 2 : 4) || !aligned(t.g, g_bf16 ? 2 : 4) || !aligned(t.copy, 2))
+        return NVFP4_ERR_ALIGN;
+    if (!eight && (!aligned(t.m, 4) || !aligned(t.v, 4))) return NVFP4_ERR_ALIGN;
+    if (eight && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))) return NVFP4_ERR_ALIGN;
+    if (nvfp4::adamw_chunks(t.n) >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+    return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t p_dtype, int32_t g_dtype,
+                int32_t state_bits, int64_t step, double lr, double beta1, double beta2, double eps,
+                double weight_decay, const float* grad_scale, void* stream)
+{
+    const auto known = [](int32_t d) { return d == NVFP4_OUT_BF16 || d == NVFP4_OUT_FP32; };
+    if (!known(p_dtype) || !known(g_dtype) || (state_bits != 8 && state_bits != 32)) return NVFP4_ERR_MODE;
+    if (count < 0 || step < 1) return NVFP4_ERR_SHAPE;
+    if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0 && eps >= 0.0) || !std::isfinite(lr) ||
+        !std::isfinite(eps) || !std::isfinite(weight_decay))
+        return NVFP4_ERR_MODE;
+    if (!tensors && count > 0) return NVFP4_ERR_NULL;
+    if (!aligned(grad_scale, 4)) return NVFP4_ERR_ALIGN;
+    const bool p_bf16 = p_dtype == NVFP4_OUT_BF16, g_bf16 = g_dtype == NVFP4_OUT_BF16, eight = state_bits == 8;
+    for (int64_t i = 0; i < count; ++i) {
+        const int st = check_adamw(tensors[i], p_bf16, g_bf16, eight);
+        if (st != NVFP4_OK) return st;
+    }
+
+    nvfp4::AdamWArgs a{};
+    a.beta1 = (float)beta1;
+    a.rest1 = (float)(1.0 - beta1);
+    a.beta2 = (float)beta2;
+    a.rest2 = (float)(1.0 - beta2);
+    a.keep = (float)(1.0 - lr * weight_decay);
+    a.rate = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
+    a.root_corr = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+    a.eps = (float)eps;
+    a.grad_scale = grad_scale;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const nvfp4_adamw_tensor& t = tensors[i];
+        if (t.n == 0) continue;
+        const int64_t c = nvfp4::adamw_chunks(t.n);
+        if (a.count == nvfp4::kAdamWTensors || chunks + c >= (int64_t(1) << 31)) {
+            nvfp4::launch_adamw(a, p_bf16, g_bf16, eight, s);
+            a.count = 0;
+            chunks = 0;
+        }
+        a.t[a.count] = nvfp4::AdamWTensor{t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.n,
+                                          adamw_vec(t, p_bf16, g_bf16, eight)};
+        a.first[a.count] = (uint32_t)chunks;
+        chunks += c;
+        a.first[++a.count] = (uint32_t)chunks;
+    }
+    if (a.count > 0) nvfp4::launch_adamw(a, p_bf16, g_bf16, eight, s);
+    return launch_status();
+}
+
+int nvfp4_i8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x, int8_t* codes, int64_t ld_codes,
+                      float* scales, void* stream)
+{
+    if (rows < 0 || cols < 0 || cols % 16 != 0 || rows >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+    if (rows > 0 && (!scales || (cols > 0 && (!x || !codes)))) return NVFP4_ERR_NULL;
+    if (ld_x < cols || ld_codes < cols) return NVFP4_ERR_SHAPE;
+    if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(codes, 16) || ld_codes % 16 != 0 || !aligned(scales, 4))
+        return NVFP4_ERR_ALIGN;
+    nvfp4::launch_i8_quant(static_cast<const uint16_t*>(x), rows, cols, ld_x, codes, ld_codes, scales,
+                           static_cast<hipStream_t>(stream));
+    return launch_status();
+}
+
+int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int8_t* b, int64_t ldb,
+                  const float* b_scales, int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, int32_t c_dtype,
+                  void* stream)
+{
+    if (c_dtype != NVFP4_OUT_BF16 && c_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_MODE;
+    if (M < 0 || N < 0 || K < 0 || K % 16 != 0 || K >= (int64_t(1) << 17)) return NVFP4_ERR_SHAPE;
+    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+    if (M > 0 && N > 0 && (!c || !a_scales || !b_scales || (K > 0 && (!a || !b)))) return NVFP4_ERR_NULL;
+    if (!aligned(a, 16) || !aligned(b, 16) || lda % 16 != 0 || ldb % 16 != 0) return NVFP4_ERR_ALIGN;
+    if (!aligned(a_scales, 4) || !aligned(b_scales, 4)) return NVFP4_ERR_ALIGN;
+    if (!aligned(c, c_dtype == NVFP4_OUT_FP32 ? 16 : 8) || ldc % 4 != 0) return NVFP4_ERR_ALIGN;
+    if (lda < K || ldb < K || ldc < N) return NVFP4_ERR_SHAPE;
+    if ((M + 15) / 16 * ((N + 15) / 16) >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+    nvfp4::launch_i8_gemm(a, lda, a_scales, b, ldb, b_scales, M, N, K, c, ldc, c_dtype == NVFP4_OUT_FP32,
+                          static_cast<hipStream_t>(stream));
+    return launch_status();
+}
+
+int nvfp4_bf16_grouped_gemm(int32_t pass, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t stride_b,
+                            const int32_t* ends, int64_t E, int64_t T, int64_t N, int64_t K, void* c, int64_t ldc,
+                            int64_t stride_c, int32_t c_dtype, void* stream)
+{
+    if (pass != NVFP4_FPROP && pass != NVFP4_DGRAD && pass != NVFP4_WGRAD) return NVFP4_ERR_MODE;
+    if (c_dtype != NVFP4_OUT_BF16 && c_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_MODE;
+    if (E < 0 || T < 0 || N < 0 || K < 0 || N % 8 || K % 8) return NVFP4_ERR_SHAPE;
+    const int64_t lim = int64_t(1) << 31;
+    if (E >= lim || T >= lim || N >= lim || K >= lim) return NVFP4_ERR_SHAPE;
+    const bool wgrad = pass == NVFP4_WGRAD;
+    const int64_t a_cols = pass == NVFP4_FPROP ? K : N;
+    const int64_t c_cols = pass == NVFP4_FPROP ? N : K;
+    const int64_t b_rows = wgrad ? T : E * N, c_rows = wgrad ? E * N : T;
+    if ((T > 0 && a_cols > 0 && !a) || (b_rows > 0 && K > 0 && !b) || (c_rows > 0 && c_cols > 0 && !c) ||
+        (E > 0 && !ends))
+        return NVFP4_ERR_NULL;
+    if (!aligned(a, 16) || !aligned(b, 16) || lda % 8 || ldb % 8 || !aligned(ends, 4)) return NVFP4_ERR_ALIGN;
+    if (!aligned(c, c_dtype == NVFP4_OUT_FP32 ? 16 : 8) || ldc % 4 != 0) return NVFP4_ERR_ALIGN;
+    if (lda < a_cols || ldb < K || ldc < c_cols) return NVFP4_ERR_SHAPE;
+    if (wgrad) {
+        if (stride_c % 4 != 0) return NVFP4_ERR_ALIGN;
+        if (stride_c < (N > 0 ? (N - 1) * ldc + c_cols : 0)) return NVFP4_ERR_SHAPE;
+    } else {
+        if (stride_b % 8 != 0) return NVFP4_ERR_ALIGN;
+        if (stride_b < (N > 0 ? (N - 1) * ldb + K : 0)) return NVFP4_ERR_SHAPE;
+    }
+    // the smallest tile a launch may take is 16 x 16
+    const int64_t tiles = (wgrad ? E * ((N + 15) / 16) : T / 16 + E + 1) * ((c_cols + 15) / 16);
+    if (tiles >= lim) return NVFP4_ERR_SHAPE;
+    const nvfp4::GroupedArgs g{static_cast<const uint16_t*>(a), lda, static_cast<const uint16_t*>(b), ldb, stride_b,
+                               ends, E, T, N, K, c, ldc, stride_c};
+    nvfp4::launch_grouped(pass, g, c_dtype == NVFP4_OUT_FP32, static_cast<hipStream_t>(stream));
     return launch_status();
 }
 

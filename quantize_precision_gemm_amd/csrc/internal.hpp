@@ -115,6 +115,59 @@ void launch_bf16_gemm(const uint16_t* a, int64_t lda, bool a_t, const uint16_t* 
                       bool b_t, int64_t M, int64_t N, int64_t K, void* c, int64_t ldc,
                       bool out_fp32, hipStream_t s);
 
+// ---- AdamW ----
+constexpr int kAdamWTensors = 48;  // tensors of one launch (they travel in its arguments)
+
+struct AdamWTensor {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* m_scale;  // 8-bit states: one fp32 power of two per 128 elements
+    float* v_scale;
+    uint16_t* copy;  // bf16 copy of p, or null
+    int64_t n;
+    int64_t vec;     // every pointer suits accesses of 4 elements
+};
+
+struct AdamWArgs {
+    AdamWTensor t[kAdamWTensors];
+    uint32_t first[kAdamWTensors + 1];  // first workgroup of each tensor; [count]: all of them
+    int count;
+    float beta1, rest1, beta2, rest2;   // rest: 1 - beta
+    float keep, rate, root_corr, eps;   // 1 - lr decay, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+    const float* grad_scale;            // or null
+};
+
+int64_t adamw_chunks(int64_t n);  // workgroups for a tensor of n elements
+void launch_adamw(const AdamWArgs& a, bool p_bf16, bool g_bf16, bool eight, hipStream_t s);
+
+// ---- 8-bit integers ----
+void launch_i8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int8_t* codes, int64_t ld_codes,
+                     float* scales, hipStream_t s);
+
+// C[m, n] = sa[m] sb[n] sum_k a[m, k] b[n, k], the sum exact in int32 (K a
+// multiple of 16, K > 0).
+void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb, const float* sb,
+                    int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, hipStream_t s);
+
+// ---- products grouped by expert ----
+// Rows of expert e: [ends[e - 1], ends[e]) (0 before the first), the ends
+// taken as clamped to [0, T] and to their running maximum, so that every row
+// that a kernel touches lies inside the operands whatever the buffer holds.
+struct GroupedArgs {
+    const uint16_t* a;   // T rows
+    int64_t lda;
+    const uint16_t* b;   // the experts' weights, or (wgrad) T rows
+    int64_t ldb, b_expert;
+    const int32_t* ends;
+    int64_t E, T, N, K;  // layer outputs N, inputs K
+    void* c;
+    int64_t ldc, c_expert;
+};
+
+void launch_grouped(int pass, const GroupedArgs& g, bool out_fp32, hipStream_t s);
+
 // Register-only stream of matrix instructions: `blocks` workgroups of 512
 // threads, `iters` rounds of 64 instructions per wave; operands 0 = fp16
 // 32x32x16 on exact E2M1 x E4M3 fp16 values, 1 = the same on random fp16,

@@ -740,6 +740,7 @@ int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int
     if (!aligned(c, c_dtype == NVFP4_OUT_FP32 ? 16 : 8) || ldc % 4 != 0) return NVFP4_ERR_ALIGN;
     if (lda < K || ldb < K || ldc < N) return NVFP4_ERR_SHAPE;
     if ((M + 15) / 16 * ((N + 15) / 16) >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+    if (lda >= (int64_t(1) << 23) || ldb >= (int64_t(1) << 23)) return NVFP4_ERR_SHAPE;  // 32-bit offsets in a tile
     nvfp4::launch_i8_gemm(a, lda, a_scales, b, ldb, b_scales, M, N, K, c, ldc, c_dtype == NVFP4_OUT_FP32,
                           static_cast<hipStream_t>(stream));
     return launch_status();
@@ -771,6 +772,9 @@ int nvfp4_bf16_grouped_gemm(int32_t pass, const void* a, int64_t lda, const void
         if (stride_b % 8 != 0) return NVFP4_ERR_ALIGN;
         if (stride_b < (N > 0 ? (N - 1) * ldb + K : 0)) return NVFP4_ERR_SHAPE;
     }
+    // a tile's 256 rows (or 64 k rows) are addressed with 32-bit offsets
+    const int64_t span = int64_t(1) << 22;
+    if (lda >= span || ldb >= span) return NVFP4_ERR_SHAPE;
     // the smallest tile a launch may take is 16 x 16
     const int64_t tiles = (wgrad ? E * ((N + 15) / 16) : T / 16 + E + 1) * ((c_cols + 15) / 16);
     if (tiles >= lim) return NVFP4_ERR_SHAPE;

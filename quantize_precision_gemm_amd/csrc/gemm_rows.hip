@@ -34,6 +34,8 @@ __device__ __forceinline__ uint32_t bf16x2_rne(float a, float b)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
 
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+
 __device__ __forceinline__ f32x4_t mma(uint4 a, uint4 b, f32x4_t c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
@@ -61,27 +63,52 @@ struct Slice {
     int64_t tile;          // this workgroup's tile of them
 };
 
-// Tile `tile` of the experts' row tiles of `rows` rows each, counted expert
-// by expert, the rows behind the last expert as one more; false past them
-// all.  Each wave scans the ends, 64 at a time.
-__device__ __forceinline__ bool find_slice(const int32_t* __restrict__ ends, int64_t E, int64_t T, int rows, int64_t tile,
-                                           Slice& s)
+// Rows [begin, end) of the experts e0 + lane, in order and range whatever the
+// ends hold; the rows behind the last expert count as expert E's.  prev: the
+// end before e0's rows, and then the last lane's.
+__device__ __forceinline__ void lane_rows(const int32_t* __restrict__ ends, int64_t E, int64_t T, int64_t e0, int& prev,
+                                          int& begin, int& end)
 {
     const int lane = threadIdx.x & 63;
-    int prev = 0;        // end of the experts before this chunk
-    int64_t before = 0;  // tiles of those
-    for (int64_t e0 = 0; e0 <= E; e0 += 64) {
-        const int64_t e = e0 + lane;
-        int end = e < E ? min(max(ends[e], 0), (int)T) : (int)T;
-        end = max(end, prev);
+    const int64_t e = e0 + lane;
+    end = e < E ? min(max(ends[e], 0), (int)T) : (int)T;
+    end = max(end, prev);
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int u = __shfl_up(end, o, 64);
-            if (lane >= o) end = max(end, u);
-        }
-        int begin = __shfl_up(end, 1, 64);
-        if (lane == 0) begin = prev;
-        int tiles = e <= E ? (end - begin + rows - 1) / rows : 0;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(end, o, 64);
+        if (lane >= o) end = max(end, u);
+    }
+    begin = __shfl_up(end, 1, 64);
+    if (lane == 0) begin = prev;
+    prev = __shfl(end, 63, 64);
+}
+
+// Row tiles of `rows` rows over all experts, each expert's own.
+__device__ __forceinline__ int64_t count_tiles(const int32_t* __restrict__ ends, int64_t E, int64_t T, int rows)
+{
+    int prev = 0, begin, end;
+    int64_t total = 0;
+    for (int64_t e0 = 0; e0 <= E; e0 += 64) {
+        lane_rows(ends, E, T, e0, prev, begin, end);
+        int tiles = (end - begin + rows - 1) / rows;
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) tiles += __shfl_xor(tiles, o, 64);
+        total += tiles;
+    }
+    return total;
+}
+
+// Tile `tile` of all, each row tile counting `cols` times, expert by expert;
+// false past them all.  Each wave scans the ends, 64 at a time.
+__device__ __forceinline__ bool find_slice(const int32_t* __restrict__ ends, int64_t E, int64_t T, int rows, int cols,
+                                           int64_t tile, Slice& s)
+{
+    const int lane = threadIdx.x & 63;
+    int prev = 0, begin, end;
+    int64_t before = 0;  // tiles of the experts before this chunk
+    for (int64_t e0 = 0; e0 <= E; e0 += 64) {
+        lane_rows(ends, E, T, e0, prev, begin, end);
+        int tiles = (end - begin + rows - 1) / rows * cols;
         const int own = tiles;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -92,13 +119,12 @@ __device__ __forceinline__ bool find_slice(const int32_t* __restrict__ ends, int
         if (past) {
             const int l = __builtin_ctzll(past);
             s.e = e0 + l;
-            s.begin = __shfl(begin, l, 64);
-            s.end = __shfl(end, l, 64);
-            s.tile = tile - (before + __shfl(tiles - own, l, 64));
+            s.begin = __builtin_amdgcn_readlane(begin, l);
+            s.end = __builtin_amdgcn_readlane(end, l);
+            s.tile = tile - (before + __builtin_amdgcn_readlane(tiles - own, l));
             return true;
         }
-        prev = __shfl(end, 63, 64);
-        before += __shfl(tiles, 63, 64);
+        before += __builtin_amdgcn_readlane(tiles, 63);
     }
     return false;
 }
@@ -205,9 +231,350 @@ __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t 
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows: a workgroup of 8 waves computes 256 x 256 outputs in steps of
+// 128 bytes of K (64 bf16, 128 int8).
+//
+// Two LDS buffers of 64 KB each hold a step's A and B tile in halves of 128
+// rows (16 KB).  The halves come straight from memory by LDS DMA, 16 bytes a
+// lane, and the DMA writes LDS in lane order; so the places are permuted by
+// choosing what each lane reads:
+//   rows x K  (N): 128 rows of 128 bytes, piece c of row r at place
+//     c ^ (r / 2) % 8: the 16 rows of a fragment read, 128 bytes apart, then
+//     cover all banks;
+//   K x rows  (T): 64 k rows of 256 bytes, 32-byte block b of k row r at
+//     b ^ (r % 4 + 4 (r / 8 % 2)): the 4 k rows that a 16-lane group of a
+//     transposing read touches, 256 bytes apart, then lie in 4 bank groups.
+// Pieces past the operand's K are read from a page of zeros, rows past its
+// end from its last row (their products are not stored).
+//
+// Wave (wm, wn) of 2 x 4 owns rows 64 wm .. +63 of each A half and columns
+// 32 wn .. +31 of each B half: four quadrants of 4 x 2 MFMA tiles.  A step
+// has four phases, each of a memory part and 16 MFMAs, between barriers:
+//   phase  reads from LDS         multiplies   starts the DMA of
+//     0    A0 (8 x 16 B a lane)   A0 B0        B0 of step t + 2
+//     1    B1 (4)                 A0 B1        A0
+//     2    A1 (8)                 A1 B1        B1
+//     3    B0 of step t + 1 (4)   A1 B0        A1
+// Waves 4-7 run one barrier behind waves 0-3 (the other wave of each SIMD),
+// so one wave's memory part lies beside the other's MFMAs.  A half is
+// refilled in the phase after its read, when every wave's reads of it have
+// come back (each waits for its own before the barrier that ends its memory
+// part); it is next read 6 phases later, and every memory part ends with a
+// wait for all but the last 12 DMA instructions, which are those of the last
+// 6 phases.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 256;
+constexpr int kHalfBytes = 128 * 128;
+constexpr int kBufBytes = 4 * kHalfBytes;
+
+__device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
+
+// 16 bytes a lane from `src` to LDS byte `lds` + 16 * lane.
+__device__ __forceinline__ void dma16(const uint8_t* src, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+}
+
+template <int kLeft>
+__device__ __forceinline__ void wait_dma()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ void barrier()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Where one thread's DMA pieces of an operand tile come from: instruction j
+// of half h at p + off[2 h + j] (N) or p + off[h] + 32 j k rows (T).
+template <bool kT>
+struct Source {
+    const uint8_t* p;
+    uint32_t off[kT ? 2 : 4];
+    int steps[kT ? 2 : 1];  // steps in which the thread's piece lies inside K
+    int64_t ld;
+
+    // the tile's first row r0; K in bytes (N) or k rows (T)
+    __device__ __forceinline__ Source(const View& v, int64_t r0, int64_t K) : ld(v.ld)
+    {
+        const int tid = threadIdx.x;
+        if constexpr (!kT) {
+            const int c = (tid & 7) ^ ((tid >> 4) & 7);
+            const int64_t left = K - 16 * c;
+            steps[0] = left > 0 ? (int)((left + 127) >> 7) : 0;
+            const int last = (int)min(v.rows - 1 - r0, (int64_t)255);
+            p = v.p + r0 * ld;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) off[i] = (uint32_t)min(64 * i + (tid >> 3), last) * (uint32_t)ld + 16 * c;
+        } else {
+            const int kr = tid >> 4;
+            const int block = ((tid & 15) >> 1) ^ ((kr & 3) | (((kr >> 3) & 1) << 2));
+            const int last = (int)min(v.rows - 8 - r0, (int64_t)248);
+            p = v.p + 2 * r0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t left = K - kr - 32 * j;
+                steps[j] = left > 0 ? (int)((left + 63) >> 6) : 0;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                off[h] = (uint32_t)kr * (uint32_t)ld + 2 * min(128 * h + 16 * block + 8 * (tid & 1), last);
+        }
+    }
+
+    // half `h` of step t into LDS at `lds`
+    __device__ __forceinline__ void fetch(int h, int t, uint32_t lds) const
+    {
+        const uint32_t at = lds + wave_id() * 1024;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint8_t* step = p + (kT ? ((int64_t)t * 64 + 32 * j) * ld : (int64_t)t * 128);
+            const uint8_t* src = t < steps[kT ? j : 0] ? step + off[kT ? h : 2 * h + j] : kZeros;
+            dma16(src, at + 8192 * j);
+        }
+    }
+};
+
+// A lane's fragments of 16-row tiles of one half: kTiles tiles from tile
+// `first`, both 64-byte sub-steps.
+template <bool kT, int kTiles>
+struct Fragments {
+    int at[2];  // N: the sub-steps' offsets; T: the lane's k row and column, and its block permutation
+
+    __device__ __forceinline__ explicit Fragments(int first)
+    {
+        const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+        if constexpr (!kT) {
+            at[0] = (16 * first + r) * 128 + ((g ^ (r >> 1)) << 4);
+            at[1] = at[0] ^ 64;
+        } else {
+            at[0] = (8 * g + (r >> 2)) * 256 + 8 * (r & 3);
+            at[1] = (first ^ ((r >> 2) | ((g & 1) << 2))) << 5;
+        }
+    }
+
+    __device__ __forceinline__ void read(uint4 (&f)[kTiles][2], const uint8_t* half) const
+    {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if constexpr (!kT) {
+                    f[i][s] = *reinterpret_cast<const uint4*>(half + at[s] + 2048 * i);
+                } else {  // `first` is a multiple of kTiles, so tile first + i is first ^ i
+                    typedef short short4_t __attribute__((ext_vector_type(4)));
+                    typedef __attribute__((address_space(3))) short4_t lds_short4;
+                    const uint8_t* a = half + at[0] + (at[1] ^ (i << 5)) + 8192 * s;
+                    const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (lds_short4*)(__attribute__((address_space(3))) uint8_t*)a);
+                    const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (lds_short4*)(__attribute__((address_space(3))) uint8_t*)(a + 1024));
+                    const uint2 l = __builtin_bit_cast(uint2, lo), u = __builtin_bit_cast(uint2, hi);
+                    f[i][s] = make_uint4(l.x, l.y, u.x, u.y);
+                }
+            }
+    }
+};
+
+// The 256 x 256 products of A rows m0 .. and B rows n0 ..; K in bytes of a
+// row, or with kTA (then kTB too, or B alone) the k rows: see Source.
+// acc[half of A][half of B][tile of A][tile of B].
+template <class Acc, bool kTA, bool kTB>
+__device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m0, int64_t n0, int64_t Ka, int64_t Kb,
+                                         int steps, uint8_t* lds, Acc (&acc)[2][2][4][2])
+{
+    const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
+    const Source<kTA> sa(A, m0, Ka);
+    const Source<kTB> sb(B, n0, Kb);
+    const Fragments<kTA, 4> fa(4 * wm);
+    const Fragments<kTB, 2> fb(2 * wn);
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    // A's halves of both buffers, then B's: every place is within a 16-bit
+    // offset of its operand's first
+    constexpr int kA0 = 0, kA1 = kHalfBytes, kB0 = kBufBytes, kB1 = kBufBytes + kHalfBytes, kNext = 2 * kHalfBytes;
+
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        sb.fetch(0, t, base + t * kNext + kB0);
+        sa.fetch(0, t, base + t * kNext + kA0);
+        sb.fetch(1, t, base + t * kNext + kB1);
+        sa.fetch(1, t, base + t * kNext + kA1);
+    }
+    uint4 a[4][2], b[2][2][2];
+    wait_dma<12>();
+    barrier();
+    fb.read(b[0], lds + kB0);
+    wait_lds();
+    barrier();
+    if (wm == 1) barrier();
+
+    auto multiply = [&](Acc(&c)[4][2], const uint4(&bf)[2][2]) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) c[i][j] = mma(bf[j][s], a[i][s], c[i][j]);
+        __builtin_amdgcn_s_setprio(0);
+    };
+    auto between = [&]() {  // the memory part ends
+        wait_dma<12>();
+        wait_lds();
+        barrier();
+    };
+    // one step from buffer `buf`; b0 holds its B half 0, b1 takes its half 1 and then the next step's half 0
+    auto step = [&](int t, int buf, uint4(&b0)[2][2], uint4(&b1)[2][2]) {
+        const uint8_t* cur = lds + buf * kNext;
+        const uint8_t* nxt = lds + (buf ^ 1) * kNext;
+        const uint32_t fill = base + buf * kNext;
+        fa.read(a, cur + kA0);
+        sb.fetch(0, t + 2, fill + kB0);
+        between();
+        multiply(acc[0][0], b0);
+        barrier();
+        fb.read(b1, cur + kB1);
+        sa.fetch(0, t + 2, fill + kA0);
+        between();
+        multiply(acc[0][1], b1);
+        barrier();
+        fa.read(a, cur + kA1);
+        sb.fetch(1, t + 2, fill + kB1);
+        between();
+        multiply(acc[1][1], b1);
+        barrier();
+        fb.read(b1, nxt + kB0);
+        sa.fetch(1, t + 2, fill + kA1);
+        between();
+        multiply(acc[1][0], b0);
+        barrier();
+    };
+    for (int t = 0; t < steps; t += 2) {
+        step(t, 0, b[0], b[1]);
+        if (t + 1 < steps) step(t + 1, 1, b[1], b[0]);
+    }
+    if (wm == 0) barrier();
+    wait_dma<0>();  // nothing is on its way into LDS any more
+}
+
+// The tile's outputs: out(m, n, v) with 4 neighbouring columns n .. n + 3, or
+// (bf16, kWide) rows of 8.
+template <class Acc, class Out>
+__device__ __forceinline__ void big_store(const Acc (&acc)[2][2][4][2], int64_t m0, int64_t n0, int64_t M, int64_t N,
+                                          const Out& out)
+{
+    const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave >> 2, wn = wave & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + 128 * h + 64 * wm + 16 * i + (lane & 15);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t n = n0 + 128 * k + 32 * wn + 16 * j + 4 * (lane >> 4);
+                    if (m < M && n < N) out(m, n, acc[h][k][i][j]);
+                }
+        }
+}
+
+// Tile `in` of a product of tm x tn tiles, walked in groups of 8 tile rows,
+// column by column, so that tiles that run together share panels.
+__device__ __forceinline__ void grouped_order(int in, int tm, int tn, int& m, int& n)
+{
+    const int group = in / (8 * tn), first = 8 * group, rows = min(8, tm - first), at = in - group * 8 * tn;
+    m = first + at % rows;
+    n = at / rows;
+}
+
+// Workgroups are dealt to the 8 XCDs in turn; number `hw` of `total` pieces
+// of work such that each XCD gets neighbouring ones.  False: none left.
+__device__ __forceinline__ bool xcd_order(int64_t hw, int64_t total, int64_t& at)
+{
+    const int64_t each = (total + 7) / 8;
+    at = hw % 8 * each + hw / 8;
+    return hw / 8 < each && at < total;
+}
+
 constexpr int kThinM = 2, kThinN = 2;
 
 }  // namespace
+
+template <int kPass, bool kF32>
+__global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBufBytes];
+    const int64_t cols = kPass == 0 ? g.N : g.K;
+    const int tn = (int)((cols + kTile - 1) / kTile);
+    View A, B;
+    int64_t m0, n0, Ka, Kb, row0 = 0, c_at = 0, at;
+    int steps, im, in_;
+    if constexpr (kPass == 2) {
+        const int tm = (int)((g.N + kTile - 1) / kTile);
+        if (!xcd_order(blockIdx.x, g.E * tm * tn, at)) return;
+        const int64_t e = at / (tm * tn);
+        grouped_order((int)(at % (tm * tn)), tm, tn, im, in_);
+        int64_t begin, end;
+        expert_rows(g.ends, e, g.T, begin, end);
+        A = View{reinterpret_cast<const uint8_t*>(g.a + begin * g.lda), 2 * g.lda, g.N};
+        B = View{reinterpret_cast<const uint8_t*>(g.b + begin * g.ldb), 2 * g.ldb, g.K};
+        Ka = Kb = end - begin;
+        steps = (int)((end - begin + 63) / 64);
+        c_at = e * g.c_expert;
+    } else {
+        if (!xcd_order(blockIdx.x, (int64_t)tn * count_tiles(g.ends, g.E, g.T, kTile), at)) return;
+        Slice s;
+        if (!find_slice(g.ends, g.E, g.T, kTile, tn, at, s)) return;
+        grouped_order((int)s.tile, (int)((s.end - s.begin + kTile - 1) / kTile), tn, im, in_);
+        const bool none = s.e >= g.E;  // rows of no expert: zeros
+        A = View{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
+        B = View{reinterpret_cast<const uint8_t*>(g.b + (none ? 0 : s.e) * g.b_expert), 2 * g.ldb, cols};
+        const int64_t K = none ? 0 : kPass == 0 ? g.K : g.N;
+        Ka = 2 * K;
+        Kb = kPass == 0 ? 2 * K : K;
+        steps = (int)((K + 63) / 64);
+        row0 = s.begin;
+    }
+    m0 = (int64_t)kTile * im;
+    n0 = (int64_t)kTile * in_;
+    f32x4_t acc[2][2][4][2] = {};
+    if (steps > 0) big_tile<f32x4_t, kPass == 2, kPass != 0>(A, B, m0, n0, Ka, Kb, steps, lds, acc);
+    big_store(acc, m0, n0, A.rows, cols, [&](int64_t m, int64_t n, const f32x4_t& v) {
+        const float y[4] = {v[0], v[1], v[2], v[3]};
+        store_cols<kF32>(g.c, c_at + (row0 + m) * g.ldc + n, n, cols, y);
+    });
+}
+
+template <bool kF32>
+__global__ __launch_bounds__(512, 2) void k_i8_big(const int8_t* __restrict__ a, int64_t lda, const float* __restrict__ sa,
+                                                   const int8_t* __restrict__ b, int64_t ldb, const float* __restrict__ sb,
+                                                   int64_t M, int64_t N, int64_t K, void* __restrict__ c, int64_t ldc)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBufBytes];
+    const int tm = (int)((M + kTile - 1) / kTile), tn = (int)((N + kTile - 1) / kTile);
+    int64_t at;
+    if (!xcd_order(blockIdx.x, (int64_t)tm * tn, at)) return;
+    int im, in_;
+    grouped_order((int)at, tm, tn, im, in_);
+    const View A{reinterpret_cast<const uint8_t*>(a), lda, M}, B{reinterpret_cast<const uint8_t*>(b), ldb, N};
+    const int64_t m0 = (int64_t)kTile * im, n0 = (int64_t)kTile * in_;
+    i32x4_t acc[2][2][4][2] = {};
+    if (K > 0) big_tile<i32x4_t, false, false>(A, B, m0, n0, K, K, (int)((K + 127) / 128), lds, acc);
+    big_store(acc, m0, n0, M, N, [&](int64_t m, int64_t n, const i32x4_t& v) {
+        const float s = sa[m];
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = ((float)v[j] * s) * sb[min(n + j, N - 1)];
+        store_cols<kF32>(c, m * ldc + n, n, N, y);
+    });
+}
 
 template <int kPass, bool kF32>
 __global__ __launch_bounds__(256) void k_grouped_thin(GroupedArgs g)
@@ -232,7 +599,7 @@ __global__ __launch_bounds__(256) void k_grouped_thin(GroupedArgs g)
         c_at = e * g.c_expert;
     } else {
         Slice s;
-        if (!find_slice(g.ends, g.E, g.T, 16 * kThinM, blockIdx.x / tn, s)) return;
+        if (!find_slice(g.ends, g.E, g.T, 16 * kThinM, 1, blockIdx.x / tn, s)) return;
         A = View{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
         const int64_t e = s.e < g.E ? s.e : 0;
         B = View{reinterpret_cast<const uint8_t*>(g.b + e * g.b_expert), 2 * g.ldb, cols};
@@ -271,6 +638,15 @@ void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t*
                     int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, hipStream_t s)
 {
     if (M == 0 || N == 0) return;
+    if (M > 64) {
+        const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
+        const dim3 big((uint32_t)((tiles + 7) / 8 * 8));
+        if (out_fp32)
+            hipLaunchKernelGGL(k_i8_big<true>, big, dim3(512), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
+        else
+            hipLaunchKernelGGL(k_i8_big<false>, big, dim3(512), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
+        return;
+    }
     const int64_t grid = (M + 16 * kThinM - 1) / (16 * kThinM) * ((N + 16 * kThinN - 1) / (16 * kThinN));
     if (out_fp32)
         hipLaunchKernelGGL(k_i8_thin<true>, dim3((uint32_t)grid), dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
@@ -279,6 +655,18 @@ void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t*
 }
 
 namespace {
+
+template <int kPass>
+void launch_grouped_big(const GroupedArgs& g, bool out_fp32, hipStream_t s)
+{
+    const int64_t cols = ((kPass == 0 ? g.N : g.K) + kTile - 1) / kTile;
+    const int64_t rows = kPass == 2 ? g.E * ((g.N + kTile - 1) / kTile) : g.T / kTile + g.E + 1;
+    const dim3 grid((uint32_t)((rows * cols + 7) / 8 * 8));
+    if (out_fp32)
+        hipLaunchKernelGGL((k_grouped_big<kPass, true>), grid, dim3(512), 0, s, g);
+    else
+        hipLaunchKernelGGL((k_grouped_big<kPass, false>), grid, dim3(512), 0, s, g);
+}
 
 template <int kPass>
 void launch_grouped_thin(const GroupedArgs& g, bool out_fp32, hipStream_t s)
@@ -299,6 +687,12 @@ void launch_grouped(int pass, const GroupedArgs& g, bool out_fp32, hipStream_t s
 {
     const int64_t rows = pass == 2 ? g.E * g.N : g.T, cols = pass == 0 ? g.N : g.K;
     if (rows == 0 || cols == 0) return;  // (an empty contraction still writes zeros)
+    if (g.T > 32 * g.E) {
+        if (pass == 0) launch_grouped_big<0>(g, out_fp32, s);
+        else if (pass == 1) launch_grouped_big<1>(g, out_fp32, s);
+        else launch_grouped_big<2>(g, out_fp32, s);
+        return;
+    }
     if (pass == 0) launch_grouped_thin<0>(g, out_fp32, s);
     else if (pass == 1) launch_grouped_thin<1>(g, out_fp32, s);
     else launch_grouped_thin<2>(g, out_fp32, s);

@@ -26,6 +26,8 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t bf16x2_rne(float a, float b)
@@ -45,6 +47,18 @@ __device__ __forceinline__ f32x4_t mma(uint4 a, uint4 b, f32x4_t c)
 __device__ __forceinline__ i32x4_t mma(uint4 a, uint4 b, i32x4_t c)
 {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c,
+                                                 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16_t mma(uint4 a, uint4 b, f32x16_t c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                   c, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x16_t mma(uint4 a, uint4 b, i32x16_t c)
+{
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c,
                                                  0, 0, 0);
 }
 
@@ -80,7 +94,7 @@ __device__ __forceinline__ void lane_rows(const int32_t* __restrict__ ends, int6
     }
     begin = __shfl_up(end, 1, 64);
     if (lane == 0) begin = prev;
-    prev = __shfl(end, 63, 64);
+    prev = __builtin_amdgcn_readlane(end, 63);
 }
 
 // Row tiles of `rows` rows over all experts, each expert's own.
@@ -93,7 +107,7 @@ __device__ __forceinline__ int64_t count_tiles(const int32_t* __restrict__ ends,
         int tiles = (end - begin + rows - 1) / rows;
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1) tiles += __shfl_xor(tiles, o, 64);
-        total += tiles;
+        total += __builtin_amdgcn_readfirstlane(tiles);
     }
     return total;
 }
@@ -136,7 +150,7 @@ __device__ __forceinline__ void expert_rows(const int32_t* __restrict__ ends, in
     const int lane = threadIdx.x & 63;
     int b = 0;  // the largest end before e
     for (int64_t i = lane; i < e; i += 64) b = max(b, ends[i]);
-    b = (int)wave_max_u32((uint32_t)max(b, 0));
+    b = __builtin_amdgcn_readfirstlane((int)wave_max_u32((uint32_t)max(b, 0)));
     b = min(b, (int)T);
     begin = b;
     end = max(b, min(max(ends[e], 0), (int)T));
@@ -249,8 +263,8 @@ __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t 
 // end from its last row (their products are not stored).
 //
 // Wave (wm, wn) of 2 x 4 owns rows 64 wm .. +63 of each A half and columns
-// 32 wn .. +31 of each B half: four quadrants of 4 x 2 MFMA tiles.  A step
-// has four phases, each of a memory part and 16 MFMAs, between barriers:
+// 32 wn .. +31 of each B half: four quadrants of two 32 x 32 MFMA tiles.  A
+// step has four phases, each of a memory part and 8 MFMAs, between barriers:
 //   phase  reads from LDS         multiplies   starts the DMA of
 //     0    A0 (8 x 16 B a lane)   A0 B0        B0 of step t + 2
 //     1    B1 (4)                 A0 B1        A0
@@ -276,6 +290,13 @@ __device__ __forceinline__ void dma16(const uint8_t* src, uint32_t lds)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
 }
 
+// The same from `base` (one for the wave) + off.
+__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory", "m0");
+}
+
 template <int kLeft>
 __device__ __forceinline__ void wait_dma()
 {
@@ -297,17 +318,15 @@ template <bool kT>
 struct Source {
     const uint8_t* p;
     uint32_t off[kT ? 2 : 4];
-    int steps[kT ? 2 : 1];  // steps in which the thread's piece lies inside K
-    int64_t ld;
+    int whole;              // steps that lie wholly inside K
+    int64_t K, ld;
 
     // the tile's first row r0; K in bytes (N) or k rows (T)
-    __device__ __forceinline__ Source(const View& v, int64_t r0, int64_t K) : ld(v.ld)
+    __device__ __forceinline__ Source(const View& v, int64_t r0, int64_t K_) : whole((int)(K_ >> (kT ? 6 : 7))), K(K_), ld(v.ld)
     {
         const int tid = threadIdx.x;
         if constexpr (!kT) {
             const int c = (tid & 7) ^ ((tid >> 4) & 7);
-            const int64_t left = K - 16 * c;
-            steps[0] = left > 0 ? (int)((left + 127) >> 7) : 0;
             const int last = (int)min(v.rows - 1 - r0, (int64_t)255);
             p = v.p + r0 * ld;
 #pragma unroll
@@ -318,11 +337,6 @@ struct Source {
             const int last = (int)min(v.rows - 8 - r0, (int64_t)248);
             p = v.p + 2 * r0;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int64_t left = K - kr - 32 * j;
-                steps[j] = left > 0 ? (int)((left + 63) >> 6) : 0;
-            }
-#pragma unroll
             for (int h = 0; h < 2; ++h)
                 off[h] = (uint32_t)kr * (uint32_t)ld + 2 * min(128 * h + 16 * block + 8 * (tid & 1), last);
         }
@@ -332,45 +346,55 @@ struct Source {
     __device__ __forceinline__ void fetch(int h, int t, uint32_t lds) const
     {
         const uint32_t at = lds + wave_id() * 1024;
+        const uint8_t* step = p + (kT ? (int64_t)t * 64 * ld : (int64_t)t * 128);
+        if (t < whole) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint8_t* step = p + (kT ? ((int64_t)t * 64 + 32 * j) * ld : (int64_t)t * 128);
-            const uint8_t* src = t < steps[kT ? j : 0] ? step + off[kT ? h : 2 * h + j] : kZeros;
-            dma16(src, at + 8192 * j);
+            for (int j = 0; j < 2; ++j) dma16(kT ? step + 32 * j * ld : step, off[kT ? h : 2 * h + j], at + 8192 * j);
+        } else {  // the last step's pieces past K, and the steps behind it: zeros
+            const int tid = threadIdx.x;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t k = kT ? (int64_t)t * 64 + 32 * j + (tid >> 4)
+                                     : (int64_t)t * 128 + 16 * ((tid & 7) ^ ((tid >> 4) & 7));
+                const uint8_t* src = (kT ? step + 32 * j * ld : step) + off[kT ? h : 2 * h + j];
+                dma16(k < K ? src : kZeros, at + 8192 * j);
+            }
         }
     }
 };
 
-// A lane's fragments of 16-row tiles of one half: kTiles tiles from tile
-// `first`, both 64-byte sub-steps.
+// A lane's fragments of 32-row tiles of one half: kTiles tiles from tile
+// `first` (a multiple of kTiles), the four 32-byte sub-steps of each.
 template <bool kT, int kTiles>
 struct Fragments {
-    int at[2];  // N: the sub-steps' offsets; T: the lane's k row and column, and its block permutation
+    int at, block;  // N: the lane's row, its piece in sub-step 0; T: its k row and column, its block in tile 0
 
     __device__ __forceinline__ explicit Fragments(int first)
     {
-        const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+        const int lane = threadIdx.x & 63;
         if constexpr (!kT) {
-            at[0] = (16 * first + r) * 128 + ((g ^ (r >> 1)) << 4);
-            at[1] = at[0] ^ 64;
+            const int r = lane & 31;
+            at = (32 * first + r) * 128;
+            block = ((lane >> 5) ^ (r >> 1 & 7)) << 4;
         } else {
-            at[0] = (8 * g + (r >> 2)) * 256 + 8 * (r & 3);
-            at[1] = (first ^ ((r >> 2) | ((g & 1) << 2))) << 5;
+            const int r = lane & 15, g = lane >> 4;
+            at = (8 * (g >> 1) + (r >> 2)) * 256 + 8 * (r & 3);
+            block = ((2 * first + (g & 1)) ^ ((r >> 2) | ((g >> 1) << 2))) << 5;
         }
     }
 
-    __device__ __forceinline__ void read(uint4 (&f)[kTiles][2], const uint8_t* half) const
+    __device__ __forceinline__ void read(uint4 (&f)[kTiles][4], const uint8_t* half) const
     {
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int i = 0; i < kTiles; ++i) {
                 if constexpr (!kT) {
-                    f[i][s] = *reinterpret_cast<const uint4*>(half + at[s] + 2048 * i);
-                } else {  // `first` is a multiple of kTiles, so tile first + i is first ^ i
+                    f[i][s] = *reinterpret_cast<const uint4*>(half + at + (block ^ (s << 5)) + 4096 * i);
+                } else {
                     typedef short short4_t __attribute__((ext_vector_type(4)));
                     typedef __attribute__((address_space(3))) short4_t lds_short4;
-                    const uint8_t* a = half + at[0] + (at[1] ^ (i << 5)) + 8192 * s;
+                    const uint8_t* a = half + at + (block ^ (i << 6)) + 4096 * s;
                     const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                         (lds_short4*)(__attribute__((address_space(3))) uint8_t*)a);
                     const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -384,16 +408,16 @@ struct Fragments {
 
 // The 256 x 256 products of A rows m0 .. and B rows n0 ..; K in bytes of a
 // row, or with kTA (then kTB too, or B alone) the k rows: see Source.
-// acc[half of A][half of B][tile of A][tile of B].
+// acc[half of A][half of B][tile of A].
 template <class Acc, bool kTA, bool kTB>
 __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m0, int64_t n0, int64_t Ka, int64_t Kb,
-                                         int steps, uint8_t* lds, Acc (&acc)[2][2][4][2])
+                                         int steps, uint8_t* lds, Acc (&acc)[2][2][2])
 {
     const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
     const Source<kTA> sa(A, m0, Ka);
     const Source<kTB> sb(B, n0, Kb);
-    const Fragments<kTA, 4> fa(4 * wm);
-    const Fragments<kTB, 2> fb(2 * wn);
+    const Fragments<kTA, 2> fa(2 * wm);
+    const Fragments<kTB, 1> fb(wn);
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     // A's halves of both buffers, then B's: every place is within a 16-bit
     // offset of its operand's first
@@ -406,7 +430,7 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
         sb.fetch(1, t, base + t * kNext + kB1);
         sa.fetch(1, t, base + t * kNext + kA1);
     }
-    uint4 a[4][2], b[2][2][2];
+    uint4 a[2][4], b[2][1][4];
     wait_dma<12>();
     barrier();
     fb.read(b[0], lds + kB0);
@@ -414,14 +438,12 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
     barrier();
     if (wm == 1) barrier();
 
-    auto multiply = [&](Acc(&c)[4][2], const uint4(&bf)[2][2]) {
+    auto multiply = [&](Acc(&c)[2], const uint4(&bf)[1][4]) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) c[i][j] = mma(bf[j][s], a[i][s], c[i][j]);
+            for (int i = 0; i < 2; ++i) c[i] = mma(bf[0][s], a[i][s], c[i]);
         __builtin_amdgcn_s_setprio(0);
     };
     auto between = [&]() {  // the memory part ends
@@ -430,7 +452,7 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
         barrier();
     };
     // one step from buffer `buf`; b0 holds its B half 0, b1 takes its half 1 and then the next step's half 0
-    auto step = [&](int t, int buf, uint4(&b0)[2][2], uint4(&b1)[2][2]) {
+    auto step = [&](int t, int buf, uint4(&b0)[1][4], uint4(&b1)[1][4]) {
         const uint8_t* cur = lds + buf * kNext;
         const uint8_t* nxt = lds + (buf ^ 1) * kNext;
         const uint32_t fill = base + buf * kNext;
@@ -463,26 +485,52 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
     wait_dma<0>();  // nothing is on its way into LDS any more
 }
 
-// The tile's outputs: out(m, n, v) with 4 neighbouring columns n .. n + 3, or
-// (bf16, kWide) rows of 8.
+// The tile's outputs: out(m, n, v) with the 8 neighbouring columns n .. n + 7
+// of a row m (columns from N on are not to be stored).  A lane holds 4 of
+// every 8; the halves of the wave exchange theirs.
 template <class Acc, class Out>
-__device__ __forceinline__ void big_store(const Acc (&acc)[2][2][4][2], int64_t m0, int64_t n0, int64_t M, int64_t N,
+__device__ __forceinline__ void big_store(const Acc (&acc)[2][2][2], int64_t m0, int64_t n0, int64_t M, int64_t N,
                                           const Out& out)
 {
+    typedef typename std::conditional<std::is_same<Acc, f32x16_t>::value, float, int>::type Val;
     const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave >> 2, wn = wave & 3;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + 128 * h + 64 * wm + 16 * i + (lane & 15);
+        for (int i = 0; i < 2; ++i) {
+            const int64_t m = m0 + 128 * h + 64 * wm + 32 * i + (lane & 31);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int64_t n = n0 + 128 * k + 32 * wn + 16 * j + 4 * (lane >> 4);
-                    if (m < M && n < N) out(m, n, acc[h][k][i][j]);
+                for (int q = 0; q < 4; q += 2) {
+                    const int64_t n = n0 + 128 * k + 32 * wn + 8 * (q + (lane >> 5));
+                    Val v[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const auto r = __builtin_amdgcn_permlane32_swap(
+                            __builtin_bit_cast(uint32_t, (Val)acc[h][k][i][4 * q + j]),
+                            __builtin_bit_cast(uint32_t, (Val)acc[h][k][i][4 * q + 4 + j]), false, false);
+                        v[j] = __builtin_bit_cast(Val, (uint32_t)r[0]);
+                        v[4 + j] = __builtin_bit_cast(Val, (uint32_t)r[1]);
+                    }
+                    if (m < M && n < N) out(m, n, v);
                 }
         }
+}
+
+// 8 neighbouring columns of an output row, as 16-byte stores where the place
+// allows them (wide).
+template <bool kF32>
+__device__ __forceinline__ void store_row8(void* c, int64_t at, int64_t n, int64_t N, bool wide, const float (&y)[8])
+{
+    if (!kF32 && wide && n + 8 <= N) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c) + at) =
+            make_uint4(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7]));
+        return;
+    }
+    const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+    store_cols<kF32>(c, at, n, N, lo);
+    if (n + 4 < N) store_cols<kF32>(c, at + 4, n + 4, N, hi);
 }
 
 // Tile `in` of a product of tm x tn tiles, walked in groups of 8 tile rows,
@@ -544,11 +592,11 @@ __global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
     }
     m0 = (int64_t)kTile * im;
     n0 = (int64_t)kTile * in_;
-    f32x4_t acc[2][2][4][2] = {};
-    if (steps > 0) big_tile<f32x4_t, kPass == 2, kPass != 0>(A, B, m0, n0, Ka, Kb, steps, lds, acc);
-    big_store(acc, m0, n0, A.rows, cols, [&](int64_t m, int64_t n, const f32x4_t& v) {
-        const float y[4] = {v[0], v[1], v[2], v[3]};
-        store_cols<kF32>(g.c, c_at + (row0 + m) * g.ldc + n, n, cols, y);
+    f32x16_t acc[2][2][2] = {};
+    if (steps > 0) big_tile<f32x16_t, kPass == 2, kPass != 0>(A, B, m0, n0, Ka, Kb, steps, lds, acc);
+    const bool wide = (reinterpret_cast<uintptr_t>(g.c) & 15) == 0 && ((g.ldc | c_at) & 7) == 0;
+    big_store(acc, m0, n0, A.rows, cols, [&](int64_t m, int64_t n, const float (&y)[8]) {
+        store_row8<kF32>(g.c, c_at + (row0 + m) * g.ldc + n, n, cols, wide, y);
     });
 }
 
@@ -565,14 +613,15 @@ __global__ __launch_bounds__(512, 2) void k_i8_big(const int8_t* __restrict__ a,
     grouped_order((int)at, tm, tn, im, in_);
     const View A{reinterpret_cast<const uint8_t*>(a), lda, M}, B{reinterpret_cast<const uint8_t*>(b), ldb, N};
     const int64_t m0 = (int64_t)kTile * im, n0 = (int64_t)kTile * in_;
-    i32x4_t acc[2][2][4][2] = {};
-    if (K > 0) big_tile<i32x4_t, false, false>(A, B, m0, n0, K, K, (int)((K + 127) / 128), lds, acc);
-    big_store(acc, m0, n0, M, N, [&](int64_t m, int64_t n, const i32x4_t& v) {
+    i32x16_t acc[2][2][2] = {};
+    if (K > 0) big_tile<i32x16_t, false, false>(A, B, m0, n0, K, K, (int)((K + 127) / 128), lds, acc);
+    const bool wide = (reinterpret_cast<uintptr_t>(c) & 15) == 0 && (ldc & 7) == 0;
+    big_store(acc, m0, n0, M, N, [&](int64_t m, int64_t n, const int (&v)[8]) {
         const float s = sa[m];
-        float y[4];
+        float y[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = ((float)v[j] * s) * sb[min(n + j, N - 1)];
-        store_cols<kF32>(c, m * ldc + n, n, N, y);
+        for (int j = 0; j < 8; ++j) y[j] = ((float)v[j] * s) * sb[min(n + j, N - 1)];
+        store_row8<kF32>(c, m * ldc + n, n, N, wide, y);
     });
 }
 

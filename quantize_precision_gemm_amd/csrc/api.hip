@@ -3,6 +3,7 @@
 // enqueued; a failed check returns a negative status and launches nothing.
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -742,7 +743,7 @@ int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int
     if ((M + 15) / 16 * ((N + 15) / 16) >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
     if (lda >= (int64_t(1) << 23) || ldb >= (int64_t(1) << 23)) return NVFP4_ERR_SHAPE;  // 32-bit offsets in a tile
     nvfp4::launch_i8_gemm(a, lda, a_scales, b, ldb, b_scales, M, N, K, c, ldc, c_dtype == NVFP4_OUT_FP32,
-                          static_cast<hipStream_t>(stream));
+                          std::max(device_cus(), 1), static_cast<hipStream_t>(stream));
     return launch_status();
 }
 
@@ -779,7 +780,7 @@ int nvfp4_bf16_grouped_gemm(int32_t pass, const void* a, int64_t lda, const void
     const int64_t tiles = (wgrad ? E * ((N + 15) / 16) : T / 16 + E + 1) * ((c_cols + 15) / 16);
     if (tiles >= lim) return NVFP4_ERR_SHAPE;
     const nvfp4::GroupedArgs g{static_cast<const uint16_t*>(a), lda, static_cast<const uint16_t*>(b), ldb, stride_b,
-                               ends, E, T, N, K, c, ldc, stride_c};
+                               ends, E, T, N, K, c, ldc, stride_c, std::max(device_cus(), 1)};
     nvfp4::launch_grouped(pass, g, c_dtype == NVFP4_OUT_FP32, static_cast<hipStream_t>(stream));
     return launch_status();
 }

@@ -38,6 +38,18 @@ __device__ __forceinline__ uint32_t bf16x2_rne(float a, float b)
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
 
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v)
+{
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+}
+
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p)
+{
+    return reinterpret_cast<const uint8_t*>(uniform((int64_t)reinterpret_cast<uintptr_t>(p)));
+}
+
 __device__ __forceinline__ f32x4_t mma(uint4 a, uint4 b, f32x4_t c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
@@ -287,14 +299,14 @@ __device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
 // 16 bytes a lane from `src` to LDS byte `lds` + 16 * lane.
 __device__ __forceinline__ void dma16(const uint8_t* src, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
 }
 
 // The same from `base` (one for the wave) + off.
 __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory", "m0");
+                 : "memory");
 }
 
 template <int kLeft>
@@ -318,24 +330,36 @@ template <bool kT>
 struct Source {
     const uint8_t* p;
     uint32_t off[kT ? 2 : 4];
-    int whole;              // steps that lie wholly inside K
-    int64_t K, ld;
+    int whole[2];           // steps of each half that lie wholly inside K
+    int64_t K[2], ld;       // K: 0 for a half of which nothing is used
 
-    // the tile's first row r0; K in bytes (N) or k rows (T)
-    __device__ __forceinline__ Source(const View& v, int64_t r0, int64_t K_) : whole((int)(K_ >> (kT ? 6 : 7))), K(K_), ld(v.ld)
+    // the tile's first row r0; K in bytes (N) or k rows (T); second: whether
+    // half 1 is used.  kPairs (N): half h holds the rows 32 h .. 32 h + 31 of
+    // every 64, so that a wave's two 32-column pieces are neighbours.
+    template <bool kPairs = false>
+    __device__ __forceinline__ void set(const View& v, int64_t r0, int64_t K_, bool second)
     {
         const int tid = threadIdx.x;
+        ld = uniform(v.ld);
+        K[0] = uniform(K_);
+        K[1] = second ? K[0] : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) whole[h] = (int)(K[h] >> (kT ? 6 : 7));
         if constexpr (!kT) {
             const int c = (tid & 7) ^ ((tid >> 4) & 7);
             const int last = (int)min(v.rows - 1 - r0, (int64_t)255);
-            p = v.p + r0 * ld;
+            p = uniform(v.p + r0 * ld);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) off[i] = (uint32_t)min(64 * i + (tid >> 3), last) * (uint32_t)ld + 16 * c;
+            for (int i = 0; i < 4; ++i) {
+                const int r = 64 * i + (tid >> 3);  // half r / 128
+                const int row = kPairs ? (r >> 5 & 3) * 64 + (r >> 7) * 32 + (r & 31) : r;
+                off[i] = (uint32_t)min(row, last) * (uint32_t)ld + 16 * c;
+            }
         } else {
             const int kr = tid >> 4;
             const int block = ((tid & 15) >> 1) ^ ((kr & 3) | (((kr >> 3) & 1) << 2));
             const int last = (int)min(v.rows - 8 - r0, (int64_t)248);
-            p = v.p + 2 * r0;
+            p = uniform(v.p + 2 * r0);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 off[h] = (uint32_t)kr * (uint32_t)ld + 2 * min(128 * h + 16 * block + 8 * (tid & 1), last);
@@ -347,7 +371,7 @@ struct Source {
     {
         const uint32_t at = lds + wave_id() * 1024;
         const uint8_t* step = p + (kT ? (int64_t)t * 64 * ld : (int64_t)t * 128);
-        if (t < whole) {
+        if (t < whole[h]) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) dma16(kT ? step + 32 * j * ld : step, off[kT ? h : 2 * h + j], at + 8192 * j);
         } else {  // the last step's pieces past K, and the steps behind it: zeros
@@ -357,7 +381,7 @@ struct Source {
                 const int64_t k = kT ? (int64_t)t * 64 + 32 * j + (tid >> 4)
                                      : (int64_t)t * 128 + 16 * ((tid & 7) ^ ((tid >> 4) & 7));
                 const uint8_t* src = (kT ? step + 32 * j * ld : step) + off[kT ? h : 2 * h + j];
-                dma16(k < K ? src : kZeros, at + 8192 * j);
+                dma16(k < K[h] ? src : kZeros, at + 8192 * j);
             }
         }
     }
@@ -406,16 +430,29 @@ struct Fragments {
     }
 };
 
+// First column, within the tile, of wave wn's part of B half h.
+template <bool kTB>
+__device__ __forceinline__ int column0(int wn, int h)
+{
+    return kTB ? 128 * h + 32 * wn : 64 * wn + 32 * h;
+}
+
 // The 256 x 256 products of A rows m0 .. and B rows n0 ..; K in bytes of a
 // row, or with kTA (then kTB too, or B alone) the k rows: see Source.
-// acc[half of A][half of B][tile of A].
+// acc[half of A][half of B][tile of A].  Rows from mend on are not wanted.
 template <class Acc, bool kTA, bool kTB>
 __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m0, int64_t n0, int64_t Ka, int64_t Kb,
-                                         int steps, uint8_t* lds, Acc (&acc)[2][2][2])
+                                         int64_t mend, int steps, uint8_t* lds, Acc (&acc)[2][2][2])
 {
     const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
-    const Source<kTA> sa(A, m0, Ka);
-    const Source<kTB> sb(B, n0, Kb);
+    Source<kTA> sa;
+    Source<kTB> sb;
+    sa.set(A, m0, Ka, m0 + 128 < mend);
+    sb.template set<!kTB>(B, n0, Kb, kTB ? n0 + 128 < B.rows : n0 + 32 < B.rows);
+    // a wave's quadrants beyond the rows or columns are left out
+    const bool rows0 = m0 + 64 * wm < mend, rows1 = m0 + 128 + 64 * wm < mend;
+    const int64_t n = n0 + column0<kTB>(wn, 0);
+    const bool cols0 = n < B.rows, cols1 = n0 + column0<kTB>(wn, 1) < B.rows;
     const Fragments<kTA, 2> fa(2 * wm);
     const Fragments<kTB, 1> fb(wn);
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
@@ -438,7 +475,8 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
     barrier();
     if (wm == 1) barrier();
 
-    auto multiply = [&](Acc(&c)[2], const uint4(&bf)[1][4]) {
+    auto multiply = [&](Acc(&c)[2], const uint4(&bf)[1][4], bool used) {
+        if (!used) return;
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
@@ -456,25 +494,25 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
         const uint8_t* cur = lds + buf * kNext;
         const uint8_t* nxt = lds + (buf ^ 1) * kNext;
         const uint32_t fill = base + buf * kNext;
-        fa.read(a, cur + kA0);
+        if (rows0) fa.read(a, cur + kA0);
         sb.fetch(0, t + 2, fill + kB0);
         between();
-        multiply(acc[0][0], b0);
+        multiply(acc[0][0], b0, rows0 && cols0);
         barrier();
         fb.read(b1, cur + kB1);
         sa.fetch(0, t + 2, fill + kA0);
         between();
-        multiply(acc[0][1], b1);
+        multiply(acc[0][1], b1, rows0 && cols1);
         barrier();
-        fa.read(a, cur + kA1);
+        if (rows1) fa.read(a, cur + kA1);
         sb.fetch(1, t + 2, fill + kB1);
         between();
-        multiply(acc[1][1], b1);
+        multiply(acc[1][1], b1, rows1 && cols1);
         barrier();
         fb.read(b1, nxt + kB0);
         sa.fetch(1, t + 2, fill + kA1);
         between();
-        multiply(acc[1][0], b0);
+        multiply(acc[1][0], b0, rows1 && cols0);
         barrier();
     };
     for (int t = 0; t < steps; t += 2) {
@@ -482,55 +520,86 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
         if (t + 1 < steps) step(t + 1, 1, b[1], b[0]);
     }
     if (wm == 0) barrier();
-    wait_dma<0>();  // nothing is on its way into LDS any more
+    wait_dma<0>();
+    barrier();  // nothing is on its way into LDS or being read any more
 }
 
-// The tile's outputs: out(m, n, v) with the 8 neighbouring columns n .. n + 7
-// of a row m (columns from N on are not to be stored).  A lane holds 4 of
-// every 8; the halves of the wave exchange theirs.
-template <class Acc, class Out>
-__device__ __forceinline__ void big_store(const Acc (&acc)[2][2][2], int64_t m0, int64_t n0, int64_t M, int64_t N,
-                                          const Out& out)
+// The tile's outputs.  value(v, h, i, k, e): accumulator e of the MFMA tile
+// of A half h, tile i and B half k as a float.  Each wave stages 64 rows of 128 bytes in its own
+// 8 KB of LDS (16-byte piece c of row r at c ^ r % 8, which spreads both the
+// writes, a row per lane, and the reads, a row per 8 lanes, over the banks)
+// and stores 8 whole row pieces of 128 bytes at a time.
+template <bool kTB, bool kF32, class Acc, class Value>
+__device__ __forceinline__ void big_store(const Acc (&acc)[2][2][2], int64_t m0, int64_t n0, int64_t mend, int64_t N,
+                                          uint8_t* lds, void* c, int64_t c_at, int64_t ldc, const Value& value)
 {
-    typedef typename std::conditional<std::is_same<Acc, f32x16_t>::value, float, int>::type Val;
     const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave >> 2, wn = wave & 3;
+    uint8_t* stage = lds + wave * 8192;
+    const bool wide = (reinterpret_cast<uintptr_t>(c) & 15) == 0 && (kF32 || ((ldc | c_at) & 7) == 0);
+    constexpr int kCols = kF32 ? 4 : 8;       // columns of a piece
+    constexpr int kUnits = kF32 ? 2 : 1;      // stagings for the 64 columns of a half of A
+    const int g = lane >> 5;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+        const int64_t row0 = m0 + 128 * h + 64 * wm;
+        if (row0 >= mend) continue;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t m = m0 + 128 * h + 64 * wm + 32 * i + (lane & 31);
+        for (int u = 0; u < kUnits; ++u) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int i = 0; i < 2; ++i) {
+                const int r = 32 * i + (lane & 31);
 #pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    const int64_t n = n0 + 128 * k + 32 * wn + 8 * (q + (lane >> 5));
-                    Val v[8];
+                for (int k = kF32 ? u : 0; k < (kF32 ? u + 1 : 2); ++k) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const auto r = __builtin_amdgcn_permlane32_swap(
-                            __builtin_bit_cast(uint32_t, (Val)acc[h][k][i][4 * q + j]),
-                            __builtin_bit_cast(uint32_t, (Val)acc[h][k][i][4 * q + 4 + j]), false, false);
-                        v[j] = __builtin_bit_cast(Val, (uint32_t)r[0]);
-                        v[4 + j] = __builtin_bit_cast(Val, (uint32_t)r[1]);
+                    for (int q = 0; q < 4; ++q) {
+                        float y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) y[j] = value(acc[h][k][i][4 * q + j], h, i, k, 4 * q + j);
+                        uint8_t* row = stage + 128 * r;
+                        if constexpr (kF32) {
+                            *reinterpret_cast<float4*>(row + (((2 * q + g) ^ (r & 7)) << 4)) =
+                                make_float4(y[0], y[1], y[2], y[3]);
+                        } else {
+                            *reinterpret_cast<uint2*>(row + (((4 * k + q) ^ (r & 7)) << 4) + 8 * g) =
+                                make_uint2(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]));
+                        }
                     }
-                    if (m < M && n < N) out(m, n, v);
                 }
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                const int r = 8 * it + (lane >> 3), p = lane & 7;
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + 128 * r + ((p ^ (r & 7)) << 4));
+                const int64_t m = row0 + r;
+                const int64_t n = n0 + (kF32 ? column0<kTB>(wn, u) + 4 * p : column0<kTB>(wn, p >> 2) + 8 * (p & 3));
+                if (m >= mend || n >= N) continue;
+                const int64_t at = c_at + m * ldc + n;
+                if constexpr (kF32) {
+                    float* d = static_cast<float*>(c) + at;
+                    if (n + 4 <= N) {
+                        *reinterpret_cast<uint4*>(d) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j)
+                            if (n + j < N) d[j] = __uint_as_float(w[j]);
+                    }
+                } else {
+                    uint16_t* d = static_cast<uint16_t*>(c) + at;
+                    if (wide && n + 8 <= N) {
+                        *reinterpret_cast<uint4*>(d) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j)
+                            if (n + j < N) d[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+                    }
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
         }
-}
-
-// 8 neighbouring columns of an output row, as 16-byte stores where the place
-// allows them (wide).
-template <bool kF32>
-__device__ __forceinline__ void store_row8(void* c, int64_t at, int64_t n, int64_t N, bool wide, const float (&y)[8])
-{
-    if (!kF32 && wide && n + 8 <= N) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c) + at) =
-            make_uint4(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7]));
-        return;
     }
-    const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
-    store_cols<kF32>(c, at, n, N, lo);
-    if (n + 4 < N) store_cols<kF32>(c, at + 4, n + 4, N, hi);
 }
 
 // Tile `in` of a product of tm x tn tiles, walked in groups of 8 tile rows,
@@ -542,13 +611,32 @@ __device__ __forceinline__ void grouped_order(int in, int tm, int tn, int& m, in
     n = at / rows;
 }
 
-// Workgroups are dealt to the 8 XCDs in turn; number `hw` of `total` pieces
-// of work such that each XCD gets neighbouring ones.  False: none left.
+// Workgroups are dealt to the 8 XCDs in turn: the hw-th of `total` pieces of
+// work such that each XCD gets neighbouring ones.  False: none left.
 __device__ __forceinline__ bool xcd_order(int64_t hw, int64_t total, int64_t& at)
 {
     const int64_t each = (total + 7) / 8;
     at = hw % 8 * each + hw / 8;
     return hw / 8 < each && at < total;
+}
+
+// The tile of this workgroup among `total`, and which of its row halves (-1:
+// both).  Whole rounds of one tile per compute unit first; if what remains
+// fills at most half the compute units, its tiles are done as two halves of
+// 128 rows each.
+__device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, int& half)
+{
+    const int64_t hw = blockIdx.x, rest = total % cus, full = total - rest;
+    half = -1;
+    if (hw < full) return xcd_order(hw, full, at);
+    const bool split = 2 * rest <= cus;
+    if (!xcd_order(hw - full, split ? 2 * rest : rest, at)) return false;
+    if (split) {
+        half = (int)(at & 1);
+        at >>= 1;
+    }
+    at += full;
+    return true;
 }
 
 constexpr int kThinM = 2, kThinN = 2;
@@ -562,11 +650,11 @@ __global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
     const int64_t cols = kPass == 0 ? g.N : g.K;
     const int tn = (int)((cols + kTile - 1) / kTile);
     View A, B;
-    int64_t m0, n0, Ka, Kb, row0 = 0, c_at = 0, at;
-    int steps, im, in_;
+    int64_t m0, n0, mend, Ka, Kb, c_at = 0, at;
+    int steps, im, in_, half;
     if constexpr (kPass == 2) {
         const int tm = (int)((g.N + kTile - 1) / kTile);
-        if (!xcd_order(blockIdx.x, g.E * tm * tn, at)) return;
+        if (!tile_order(g.E * tm * tn, g.cus, at, half)) return;
         const int64_t e = at / (tm * tn);
         grouped_order((int)(at % (tm * tn)), tm, tn, im, in_);
         int64_t begin, end;
@@ -577,7 +665,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
         steps = (int)((end - begin + 63) / 64);
         c_at = e * g.c_expert;
     } else {
-        if (!xcd_order(blockIdx.x, (int64_t)tn * count_tiles(g.ends, g.E, g.T, kTile), at)) return;
+        if (!tile_order((int64_t)tn * count_tiles(g.ends, g.E, g.T, kTile), g.cus, at, half)) return;
         Slice s;
         if (!find_slice(g.ends, g.E, g.T, kTile, tn, at, s)) return;
         grouped_order((int)s.tile, (int)((s.end - s.begin + kTile - 1) / kTile), tn, im, in_);
@@ -588,40 +676,48 @@ __global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
         Ka = 2 * K;
         Kb = kPass == 0 ? 2 * K : K;
         steps = (int)((K + 63) / 64);
-        row0 = s.begin;
+        c_at = s.begin * g.ldc;
     }
-    m0 = (int64_t)kTile * im;
+    m0 = (int64_t)kTile * im + (half == 1 ? 128 : 0);
     n0 = (int64_t)kTile * in_;
+    mend = half == 0 ? min(m0 + 128, A.rows) : A.rows;
+    if (m0 >= mend) return;
     f32x16_t acc[2][2][2] = {};
-    if (steps > 0) big_tile<f32x16_t, kPass == 2, kPass != 0>(A, B, m0, n0, Ka, Kb, steps, lds, acc);
-    const bool wide = (reinterpret_cast<uintptr_t>(g.c) & 15) == 0 && ((g.ldc | c_at) & 7) == 0;
-    big_store(acc, m0, n0, A.rows, cols, [&](int64_t m, int64_t n, const float (&y)[8]) {
-        store_row8<kF32>(g.c, c_at + (row0 + m) * g.ldc + n, n, cols, wide, y);
-    });
+    if (steps > 0) big_tile<f32x16_t, kPass == 2, kPass != 0>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
+    big_store<kPass != 0, kF32>(acc, m0, n0, mend, cols, lds, g.c, c_at, g.ldc,
+                                [](float v, int, int, int, int) { return v; });
 }
 
 template <bool kF32>
 __global__ __launch_bounds__(512, 2) void k_i8_big(const int8_t* __restrict__ a, int64_t lda, const float* __restrict__ sa,
                                                    const int8_t* __restrict__ b, int64_t ldb, const float* __restrict__ sb,
-                                                   int64_t M, int64_t N, int64_t K, void* __restrict__ c, int64_t ldc)
+                                                   int64_t M, int64_t N, int64_t K, void* __restrict__ c, int64_t ldc, int cus)
 {
     __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBufBytes];
     const int tm = (int)((M + kTile - 1) / kTile), tn = (int)((N + kTile - 1) / kTile);
     int64_t at;
-    if (!xcd_order(blockIdx.x, (int64_t)tm * tn, at)) return;
-    int im, in_;
+    int im, in_, half;
+    if (!tile_order((int64_t)tm * tn, cus, at, half)) return;
     grouped_order((int)at, tm, tn, im, in_);
     const View A{reinterpret_cast<const uint8_t*>(a), lda, M}, B{reinterpret_cast<const uint8_t*>(b), ldb, N};
-    const int64_t m0 = (int64_t)kTile * im, n0 = (int64_t)kTile * in_;
+    const int64_t m0 = (int64_t)kTile * im + (half == 1 ? 128 : 0), n0 = (int64_t)kTile * in_;
+    const int64_t mend = half == 0 ? min(m0 + 128, M) : M;
+    if (m0 >= mend) return;
     i32x16_t acc[2][2][2] = {};
-    if (K > 0) big_tile<i32x16_t, false, false>(A, B, m0, n0, K, K, (int)((K + 127) / 128), lds, acc);
-    const bool wide = (reinterpret_cast<uintptr_t>(c) & 15) == 0 && (ldc & 7) == 0;
-    big_store(acc, m0, n0, M, N, [&](int64_t m, int64_t n, const int (&v)[8]) {
-        const float s = sa[m];
-        float y[8];
+    if (K > 0) big_tile<i32x16_t, false, false>(A, B, m0, n0, K, K, mend, (int)((K + 127) / 128), lds, acc);
+    const int lane = threadIdx.x & 63, wm = wave_id() >> 2, wn = wave_id() & 3;
+    float row_scale[2][2], col_scale[2][16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = ((float)v[j] * s) * sb[min(n + j, N - 1)];
-        store_row8<kF32>(c, m * ldc + n, n, N, wide, y);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) row_scale[h][i] = sa[min(m0 + 128 * h + 64 * wm + 32 * i + (lane & 31), M - 1)];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            col_scale[k][e] = sb[min(n0 + column0<false>(wn, k) + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3), N - 1)];
+    big_store<false, kF32>(acc, m0, n0, mend, N, lds, c, 0, ldc, [&](int v, int h, int i, int k, int e) {
+        return ((float)v * row_scale[h][i]) * col_scale[k][e];
     });
 }
 
@@ -684,16 +780,16 @@ __global__ __launch_bounds__(256) void k_i8_thin(const int8_t* __restrict__ a, i
 }
 
 void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb, const float* sb,
-                    int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, hipStream_t s)
+                    int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, int cus, hipStream_t s)
 {
     if (M == 0 || N == 0) return;
     if (M > 64) {
         const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-        const dim3 big((uint32_t)((tiles + 7) / 8 * 8));
+        const dim3 big((uint32_t)(tiles + cus + 8));  // the remainder may be done in halves
         if (out_fp32)
-            hipLaunchKernelGGL(k_i8_big<true>, big, dim3(512), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
+            hipLaunchKernelGGL(k_i8_big<true>, big, dim3(512), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc, cus);
         else
-            hipLaunchKernelGGL(k_i8_big<false>, big, dim3(512), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
+            hipLaunchKernelGGL(k_i8_big<false>, big, dim3(512), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc, cus);
         return;
     }
     const int64_t grid = (M + 16 * kThinM - 1) / (16 * kThinM) * ((N + 16 * kThinN - 1) / (16 * kThinN));
@@ -710,7 +806,7 @@ void launch_grouped_big(const GroupedArgs& g, bool out_fp32, hipStream_t s)
 {
     const int64_t cols = ((kPass == 0 ? g.N : g.K) + kTile - 1) / kTile;
     const int64_t rows = kPass == 2 ? g.E * ((g.N + kTile - 1) / kTile) : g.T / kTile + g.E + 1;
-    const dim3 grid((uint32_t)((rows * cols + 7) / 8 * 8));
+    const dim3 grid((uint32_t)(rows * cols + g.cus + 8));  // the remainder may be done in halves
     if (out_fp32)
         hipLaunchKernelGGL((k_grouped_big<kPass, true>), grid, dim3(512), 0, s, g);
     else

@@ -149,7 +149,7 @@ void launch_i8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, 
 // C[m, n] = sa[m] sb[n] sum_k a[m, k] b[n, k], the sum exact in int32 (K a
 // multiple of 16, K > 0).
 void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb, const float* sb,
-                    int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, hipStream_t s);
+                    int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, int cus, hipStream_t s);
 
 // ---- products grouped by expert ----
 // Rows of expert e: [ends[e - 1], ends[e]) (0 before the first), the ends
@@ -164,6 +164,7 @@ struct GroupedArgs {
     int64_t E, T, N, K;  // layer outputs N, inputs K
     void* c;
     int64_t ldc, c_expert;
+    int cus;             // compute units of the device
 };
 
 void launch_grouped(int pass, const GroupedArgs& g, bool out_fp32, hipStream_t s);

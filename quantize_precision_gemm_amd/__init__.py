@@ -664,6 +664,16 @@ def nvfp4_bf16_gemm(pass_, a, b, out_dtype=torch.bfloat16, out=None, stream=None
     return out
 
 
+# The calls below are short (a few microseconds of GPU work for one token), so
+# their checks are too: device indices compared as integers, addresses passed
+# as integers, no checks of a tensor that the call has just made.
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _out_code(dtype, what="output"):
     if dtype == torch.float32:
         return OUT_FP32
@@ -674,7 +684,8 @@ def _out_code(dtype, what="output"):
 
 def _pitch(x, multiple=8):
     """Row pitch of a matrix; the stride of one row or none means nothing."""
-    return x.stride(0) if x.shape[0] > 1 and x.shape[1] > 0 else _round_up(x.shape[1], multiple)
+    rows, cols = x.shape
+    return x.stride(0) if rows > 1 and cols > 0 else _round_up(cols, multiple)
 
 
 def _for_stream(t, stream):
@@ -701,53 +712,60 @@ def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=Non
     ends: int32 device tensor (E): one past the last row of each expert.
     """
     _check_bf16(a)
-    dev = a.device
+    index = a.get_device()
     if not isinstance(ends, torch.Tensor) or ends.dtype != torch.int32 or ends.dim() != 1 or \
-            not _same_device(ends.device, dev) or not ends.is_contiguous():
+            not ends.is_cuda or ends.get_device() != index or not ends.is_contiguous():
         raise ValueError("ends: expected a contiguous 1-D int32 tensor on the operands' device")
-    E, T = ends.shape[0], a.shape[0]
+    E, (T, a_cols) = ends.shape[0], a.shape
     if pass_ == WGRAD:
         _check_bf16(b)
         if b.shape[0] != T:
             raise ValueError(f"b: {b.shape[0]} rows, a has {T}")
-        N, K = a.shape[1], b.shape[1]
+        N, K = a_cols, b.shape[1]
         shape = (E, N, K)
         ldb, stride_b = _pitch(b), 0
     elif pass_ in (FPROP, DGRAD):
         _check_bf16_experts(b, "b")
-        if b.shape[0] != E:
-            raise ValueError(f"b: {b.shape[0]} experts, ends has {E}")
-        N, K = b.shape[1], b.shape[2]
-        if a.shape[1] != (K if pass_ == FPROP else N):
-            raise ValueError(f"a: {a.shape[1]} columns do not fit b's {tuple(b.shape)}")
+        experts, N, K = b.shape
+        if experts != E:
+            raise ValueError(f"b: {experts} experts, ends has {E}")
+        if a_cols != (K if pass_ == FPROP else N):
+            raise ValueError(f"a: {a_cols} columns do not fit b's {tuple(b.shape)}")
         shape = (T, N if pass_ == FPROP else K)
         # the strides of a dimension of one element or none mean nothing
         ldb = b.stride(1) if N > 1 and K > 0 else _round_up(K, 8)
-        stride_b = b.stride(0) if E > 1 and b.numel() > 0 else N * ldb
+        stride_b = b.stride(0) if E > 1 and N > 0 and K > 0 else N * ldb
     else:
         raise ValueError(f"unknown pass {pass_}")
-    if not _same_device(b.device, dev):
-        raise ValueError(f"b: on {b.device}, expected {dev}")
-    if out is None:
-        if N % 8 or K % 8:
-            raise ValueError("N and K must be multiples of 8")
-        out = _for_stream(torch.empty(shape, dtype=out_dtype, device=dev), stream)
+    if b.get_device() != index:
+        raise ValueError(f"b: on {b.device}, expected {a.device}")
+    if N % 8 or K % 8:
+        raise ValueError(f"N = {N} and K = {K} must be multiples of 8")
     stride_c = 0
-    if pass_ == WGRAD:
-        if not isinstance(out, torch.Tensor) or tuple(out.shape) != shape or not _same_device(out.device, dev):
-            raise ValueError(f"out: expected a tensor of shape {shape} on {dev}")
+    if out is None:
+        code = _out_code(out_dtype)
+        out = _for_stream(torch.empty(shape, dtype=out_dtype, device=a.device), stream)
+        ldc = shape[-1]
+        stride_c = N * K
+    elif pass_ == WGRAD:
+        if not isinstance(out, torch.Tensor) or tuple(out.shape) != shape or not _same_device(out.device, a.device):
+            raise ValueError(f"out: expected a tensor of shape {shape} on {a.device}")
+        code = _out_code(out.dtype)
         if out.numel() > 0 and out.stride(2) != 1:
             raise TypeError("output must have a contiguous last dimension")
         ldc = out.stride(1) if N > 1 and K > 0 else _round_up(K, 4)
         stride_c = out.stride(0) if E > 1 and out.numel() > 0 else N * ldc
-        if ldc < K or stride_c < (N - 1) * ldc + K and out.numel() > 0:
+        if out.numel() > 0 and (ldc < K or stride_c < (N - 1) * ldc + K):
             raise ValueError("out: rows or experts overlap")
     else:
-        _check_gemm_out(out, shape, dev)
+        _check_gemm_out(out, shape, a.device)
+        code = _out_code(out.dtype)
         ldc = _pitch(out, 4)
-    st = load_library().nvfp4_bf16_grouped_gemm(pass_, _ptr(a), _pitch(a), _ptr(b), ldb, stride_b, _ptr(ends), E, T, N,
-                                                K, _ptr(out), ldc, stride_c, _out_code(out.dtype), _stream(stream))
-    _check(st, "nvfp4_bf16_grouped_gemm")
+    st = load_library().nvfp4_bf16_grouped_gemm(pass_, a.data_ptr(), _pitch(a), b.data_ptr(), ldb, stride_b,
+                                                ends.data_ptr(), E, T, N, K, out.data_ptr(), ldc, stride_c, code,
+                                                _raw_stream(stream))
+    if st:
+        _check(st, "nvfp4_bf16_grouped_gemm")
     return out
 
 
@@ -782,41 +800,45 @@ class AdamWGroup:
         if any(len(x) != k for x in lists):
             raise ValueError("the lists of an AdamW group have one entry per tensor")
         state = torch.float8_e4m3fn if eight else torch.float32
+        for what, t in (("params", self.params), ("grads", self.grads)):
+            if k and not isinstance(t[0], torch.Tensor):
+                raise TypeError(f"{what}[0]: expected a CUDA tensor")
         self.p_dtype = _out_code(self.params[0].dtype, "params") if k else OUT_FP32
         self.g_dtype = _out_code(self.grads[0].dtype, "grads") if k else OUT_FP32
         self.device = self.params[0].device if k else None
-        self._table = (_AdamWTensor * max(k, 1))()
-        for i in range(k):
-            n = self.params[i].numel()
-            blocks = -(-n // self.BLOCK)
-            wanted = (("params", self.params[i], self.params[0].dtype, n), ("grads", self.grads[i], self.grads[0].dtype, n),
-                      ("m", self.m[i], state, n), ("v", self.v[i], state, n),
-                      ("m_scales", self.m_scales[i], torch.float32, blocks),
-                      ("v_scales", self.v_scales[i], torch.float32, blocks),
-                      ("copies", self.copies[i], torch.bfloat16, n))
-            for what, t, dtype, count in wanted:
-                if t is None and (what == "copies" or not eight and what.endswith("_scales")):
-                    continue
-                self._check_tensor(f"{what}[{i}]", t, dtype, count)
-            if self.copies[i] is not None and self.p_dtype != OUT_FP32:
+        self._table = table = (_AdamWTensor * max(k, 1))()
+        if not k:
+            self.count = 0
+            return
+        kinds = [("p", "params", self.params, self.params[0].dtype), ("g", "grads", self.grads, self.grads[0].dtype),
+                 ("m", "m", self.m, state), ("v", "v", self.v, state), ("copy", "copies", self.copies, torch.bfloat16)]
+        if eight:
+            kinds += [("m_scale", "m_scales", self.m_scales, torch.float32),
+                      ("v_scale", "v_scales", self.v_scales, torch.float32)]
+        for i, p in enumerate(self.params):
+            table[i].n = p.numel() if isinstance(p, torch.Tensor) else 0
+        for field, what, tensors, dtype in kinds:
+            if what == "copies" and any(t is not None for t in tensors) and self.p_dtype != OUT_FP32:
                 raise ValueError("copies are made of float32 params")
-            row = self._table[i]
-            for field, (_, t, _, _) in zip(("p", "g", "m", "v", "m_scale", "v_scale", "copy"), wanted):
-                setattr(row, field, None if t is None else t.data_ptr())
-            row.n = n
+            for i, t in enumerate(tensors):
+                if t is None and what == "copies":
+                    continue
+                n = table[i].n
+                self._check_tensor(what, i, t, dtype, -(-n // self.BLOCK) if what.endswith("scales") else n)
+                setattr(table[i], field, t.data_ptr())
         self.count = k
 
-    def _check_tensor(self, what, t, dtype, count):
+    def _check_tensor(self, what, i, t, dtype, count):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{what}: expected a CUDA tensor")
+            raise TypeError(f"{what}[{i}]: expected a CUDA tensor")
         if t.dtype != dtype:
-            raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+            raise TypeError(f"{what}[{i}]: dtype {t.dtype}, expected {dtype}")
         if t.device != self.device:
-            raise ValueError(f"{what}: on {t.device}, expected {self.device}")
+            raise ValueError(f"{what}[{i}]: on {t.device}, expected {self.device}")
         if t.numel() != count:
-            raise ValueError(f"{what}: {t.numel()} elements, expected {count}")
+            raise ValueError(f"{what}[{i}]: {t.numel()} elements, expected {count}")
         if not t.is_contiguous():
-            raise ValueError(f"{what}: must be contiguous")
+            raise ValueError(f"{what}[{i}]: must be contiguous")
 
     @classmethod
     def with_states(cls, params, grads, bits=32, copies=None):
@@ -848,13 +870,15 @@ def nvfp4_adamw(group, step, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0
     if grad_scale is not None:
         if not isinstance(grad_scale, torch.Tensor) or grad_scale.dtype != torch.float32 or grad_scale.numel() != 1:
             raise TypeError("grad_scale: expected a one-element float32 tensor")
-        if group.device is not None and not _same_device(grad_scale.device, group.device):
+        if group.device is not None and grad_scale.device != group.device:
             raise ValueError(f"grad_scale: on {grad_scale.device}, expected {group.device}")
+        grad_scale = grad_scale.data_ptr()
     if group.count == 0:
         return
     st = load_library().nvfp4_adamw(group._table, group.count, group.p_dtype, group.g_dtype, group.bits, step, lr,
-                                    beta1, beta2, eps, weight_decay, _ptr(grad_scale), _stream(stream))
-    _check(st, "nvfp4_adamw")
+                                    beta1, beta2, eps, weight_decay, grad_scale, _raw_stream(stream))
+    if st:
+        _check(st, "nvfp4_adamw")
 
 
 class I8Tensor:
@@ -876,14 +900,15 @@ def _check_i8(t, what):
     c, s = t.codes, t.scales
     if not (isinstance(c, torch.Tensor) and c.is_cuda and c.dtype == torch.int8 and c.dim() == 2):
         raise TypeError(f"{what}.codes: expected a 2-D int8 CUDA tensor")
-    if c.numel() > 0 and c.stride(1) != 1:
+    if c.stride(1) != 1 and c.numel() > 0:
         raise ValueError(f"{what}.codes: the last dimension must be contiguous")
     if not isinstance(s, torch.Tensor) or s.dtype != torch.float32 or s.dim() != 1 or not s.is_contiguous():
         raise TypeError(f"{what}.scales: expected a contiguous 1-D float32 tensor")
     if s.shape[0] != c.shape[0]:
         raise ValueError(f"{what}.scales: {s.shape[0]} values for {c.shape[0]} rows")
-    if s.device != c.device:
+    if not s.is_cuda or s.get_device() != c.get_device():
         raise ValueError(f"{what}.scales: on {s.device}, expected {c.device}")
+    return c, s
 
 
 def nvfp4_i8_quantize(x, out=None, stream=None):
@@ -892,37 +917,43 @@ def nvfp4_i8_quantize(x, out=None, stream=None):
     _check_bf16(x)
     rows, cols = x.shape
     if out is None:
-        out = I8Tensor(_for_stream(torch.empty((rows, cols), dtype=torch.int8, device=x.device), stream),
-                       _for_stream(torch.empty(rows, dtype=torch.float32, device=x.device), stream))
-    _check_i8(out, "out")
-    if tuple(out.shape) != (rows, cols):
-        raise ValueError(f"out: shape {tuple(out.shape)}, expected {(rows, cols)}")
-    if not _same_device(out.codes.device, x.device):
-        raise ValueError(f"out: on {out.codes.device}, expected {x.device}")
-    st = load_library().nvfp4_i8_quantize(_ptr(x), rows, cols, _pitch(x), _ptr(out.codes), _pitch(out.codes, 16),
-                                          _ptr(out.scales), _stream(stream))
-    _check(st, "nvfp4_i8_quantize")
+        codes = _for_stream(torch.empty((rows, cols), dtype=torch.int8, device=x.device), stream)
+        scales = _for_stream(torch.empty(rows, dtype=torch.float32, device=x.device), stream)
+        out = I8Tensor(codes, scales)
+    else:
+        codes, scales = _check_i8(out, "out")
+        if tuple(codes.shape) != (rows, cols):
+            raise ValueError(f"out: shape {tuple(codes.shape)}, expected {(rows, cols)}")
+        if codes.get_device() != x.get_device():
+            raise ValueError(f"out: on {codes.device}, expected {x.device}")
+    st = load_library().nvfp4_i8_quantize(x.data_ptr(), rows, cols, _pitch(x), codes.data_ptr(), _pitch(codes, 16),
+                                          scales.data_ptr(), _raw_stream(stream))
+    if st:
+        _check(st, "nvfp4_i8_quantize")
     return out
 
 
 def nvfp4_i8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
     """a (M x K) times b (N x K) transposed, both I8Tensors (see nvfp4_i8_gemm
     in nvfp4.h): M x N, float32 or bfloat16."""
-    _check_i8(a, "a")
-    _check_i8(b, "b")
-    (M, K), N = a.shape, b.shape[0]
-    dev = a.codes.device
-    if b.shape[1] != K:
-        raise ValueError(f"b: {b.shape[1]} columns, a has {K}")
-    if not _same_device(b.codes.device, dev):
-        raise ValueError(f"b: on {b.codes.device}, expected {dev}")
+    (ac, sa), (bc, sb) = _check_i8(a, "a"), _check_i8(b, "b")
+    (M, K), (N, b_cols) = ac.shape, bc.shape
+    if b_cols != K:
+        raise ValueError(f"b: {b_cols} columns, a has {K}")
+    if bc.get_device() != ac.get_device():
+        raise ValueError(f"b: on {bc.device}, expected {ac.device}")
     if out is None:
-        out = _for_stream(_new_gemm_out((M, N), out_dtype, dev), stream)
-    _check_gemm_out(out, (M, N), dev)
-    st = load_library().nvfp4_i8_gemm(_ptr(a.codes), _pitch(a.codes, 16), _ptr(a.scales), _ptr(b.codes),
-                                      _pitch(b.codes, 16), _ptr(b.scales), M, N, K, _ptr(out), _pitch(out, 4),
-                                      _out_code(out.dtype), _stream(stream))
-    _check(st, "nvfp4_i8_gemm")
+        code = _out_code(out_dtype)
+        out = _for_stream(_new_gemm_out((M, N), out_dtype, ac.device), stream)
+        ldc = _round_up(N, 4)
+    else:
+        _check_gemm_out(out, (M, N), ac.device)
+        code = _out_code(out.dtype)
+        ldc = _pitch(out, 4)
+    st = load_library().nvfp4_i8_gemm(ac.data_ptr(), _pitch(ac, 16), sa.data_ptr(), bc.data_ptr(), _pitch(bc, 16),
+                                      sb.data_ptr(), M, N, K, out.data_ptr(), ldc, code, _raw_stream(stream))
+    if st:
+        _check(st, "nvfp4_i8_gemm")
     return out
 
 

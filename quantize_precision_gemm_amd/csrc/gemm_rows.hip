@@ -278,17 +278,20 @@ __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t 
 // 32 wn .. +31 of each B half: four quadrants of two 32 x 32 MFMA tiles.  A
 // step has four phases, each of a memory part and 8 MFMAs, between barriers:
 //   phase  reads from LDS         multiplies   starts the DMA of
-//     0    A0 (8 x 16 B a lane)   A0 B0        B0 of step t + 2
-//     1    B1 (4)                 A0 B1        A0
-//     2    A1 (8)                 A1 B1        B1
-//     3    B0 of step t + 1 (4)   A1 B0        A1
+//     0    A0 (8 x 16 B a lane)   A0 B0        A1 of step t + 1
+//     1    B1 (4)                 A0 B1        B0 of step t + 2
+//     2    A1 (8)                 A1 B1        A0 of step t + 2
+//     3    B0 of step t + 1 (4)   A1 B0        B1 of step t + 2
 // Waves 4-7 run one barrier behind waves 0-3 (the other wave of each SIMD),
-// so one wave's memory part lies beside the other's MFMAs.  A half is
-// refilled in the phase after its read, when every wave's reads of it have
-// come back (each waits for its own before the barrier that ends its memory
-// part); it is next read 6 phases later, and every memory part ends with a
-// wait for all but the last 12 DMA instructions, which are those of the last
-// 6 phases.
+// so one wave's memory part lies beside the other's MFMAs.  A wave's reads of
+// a phase have come back before the barrier that ends its MFMAs; a half is
+// refilled two phases after its read, which is behind that barrier for every
+// wave.  It is next read 5 phases after that, and every memory part ends with
+// a wait for all but the last 10 DMA instructions, those of the last 5 phases.
+//
+// What bounds it: reading LDS (192 KB a step) and the DMA's writes (64 KB)
+// keep the LDS busy for about as long as the MFMAs take, and under full load
+// the power limit lowers the clock (1.5 to 1.7 GHz).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256;
 constexpr int kHalfBytes = 128 * 128;
@@ -460,15 +463,15 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
     // offset of its operand's first
     constexpr int kA0 = 0, kA1 = kHalfBytes, kB0 = kBufBytes, kB1 = kBufBytes + kHalfBytes, kNext = 2 * kHalfBytes;
 
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        sb.fetch(0, t, base + t * kNext + kB0);
-        sa.fetch(0, t, base + t * kNext + kA0);
-        sb.fetch(1, t, base + t * kNext + kB1);
-        sa.fetch(1, t, base + t * kNext + kA1);
-    }
+    sb.fetch(0, 0, base + kB0);
+    sa.fetch(0, 0, base + kA0);
+    sb.fetch(1, 0, base + kB1);
+    sa.fetch(1, 0, base + kA1);
+    sb.fetch(0, 1, base + kNext + kB0);
+    sa.fetch(0, 1, base + kNext + kA0);
+    sb.fetch(1, 1, base + kNext + kB1);
     uint4 a[2][4], b[2][1][4];
-    wait_dma<12>();
+    wait_dma<10>();
     barrier();
     fb.read(b[0], lds + kB0);
     wait_lds();
@@ -476,44 +479,42 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
     if (wm == 1) barrier();
 
     auto multiply = [&](Acc(&c)[2], const uint4(&bf)[1][4], bool used) {
-        if (!used) return;
-        __builtin_amdgcn_s_setprio(1);
+        if (used) {
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+            for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) c[i] = mma(bf[0][s], a[i][s], c[i]);
-        __builtin_amdgcn_s_setprio(0);
+                for (int i = 0; i < 2; ++i) c[i] = mma(bf[0][s], a[i][s], c[i]);
+            __builtin_amdgcn_s_setprio(0);
+        }
+        wait_lds();
+        barrier();
     };
     auto between = [&]() {  // the memory part ends
-        wait_dma<12>();
-        wait_lds();
+        wait_dma<10>();
         barrier();
     };
     // one step from buffer `buf`; b0 holds its B half 0, b1 takes its half 1 and then the next step's half 0
     auto step = [&](int t, int buf, uint4(&b0)[1][4], uint4(&b1)[1][4]) {
         const uint8_t* cur = lds + buf * kNext;
         const uint8_t* nxt = lds + (buf ^ 1) * kNext;
-        const uint32_t fill = base + buf * kNext;
+        const uint32_t fill = base + buf * kNext, other = base + (buf ^ 1) * kNext;
         if (rows0) fa.read(a, cur + kA0);
-        sb.fetch(0, t + 2, fill + kB0);
+        sa.fetch(1, t + 1, other + kA1);
         between();
         multiply(acc[0][0], b0, rows0 && cols0);
-        barrier();
         fb.read(b1, cur + kB1);
-        sa.fetch(0, t + 2, fill + kA0);
+        sb.fetch(0, t + 2, fill + kB0);
         between();
         multiply(acc[0][1], b1, rows0 && cols1);
-        barrier();
         if (rows1) fa.read(a, cur + kA1);
-        sb.fetch(1, t + 2, fill + kB1);
+        sa.fetch(0, t + 2, fill + kA0);
         between();
         multiply(acc[1][1], b1, rows1 && cols1);
-        barrier();
         fb.read(b1, nxt + kB0);
-        sa.fetch(1, t + 2, fill + kA1);
+        sb.fetch(1, t + 2, fill + kB1);
         between();
         multiply(acc[1][0], b0, rows1 && cols0);
-        barrier();
     };
     for (int t = 0; t < steps; t += 2) {
         step(t, 0, b[0], b[1]);
@@ -524,12 +525,23 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
     barrier();  // nothing is on its way into LDS or being read any more
 }
 
+// kStream: past the caches (a weight gradient is larger than they are).
+template <bool kStream>
+__device__ __forceinline__ void store16(void* d, uint4 v)
+{
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    if constexpr (kStream)
+        __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, static_cast<u32x4_t*>(d));
+    else
+        *static_cast<uint4*>(d) = v;
+}
+
 // The tile's outputs.  value(v, h, i, k, e): accumulator e of the MFMA tile
 // of A half h, tile i and B half k as a float.  Each wave stages 64 rows of 128 bytes in its own
 // 8 KB of LDS (16-byte piece c of row r at c ^ r % 8, which spreads both the
 // writes, a row per lane, and the reads, a row per 8 lanes, over the banks)
 // and stores 8 whole row pieces of 128 bytes at a time.
-template <bool kTB, bool kF32, class Acc, class Value>
+template <bool kTB, bool kF32, bool kStream, class Acc, class Value>
 __device__ __forceinline__ void big_store(const Acc (&acc)[2][2][2], int64_t m0, int64_t n0, int64_t mend, int64_t N,
                                           uint8_t* lds, void* c, int64_t c_at, int64_t ldc, const Value& value)
 {
@@ -578,7 +590,7 @@ __device__ __forceinline__ void big_store(const Acc (&acc)[2][2][2], int64_t m0,
                 if constexpr (kF32) {
                     float* d = static_cast<float*>(c) + at;
                     if (n + 4 <= N) {
-                        *reinterpret_cast<uint4*>(d) = v;
+                        store16<kStream>(d, v);
                     } else {
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -588,7 +600,7 @@ __device__ __forceinline__ void big_store(const Acc (&acc)[2][2][2], int64_t m0,
                 } else {
                     uint16_t* d = static_cast<uint16_t*>(c) + at;
                     if (wide && n + 8 <= N) {
-                        *reinterpret_cast<uint4*>(d) = v;
+                        store16<kStream>(d, v);
                     } else {
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -612,23 +624,30 @@ __device__ __forceinline__ void grouped_order(int in, int tm, int tn, int& m, in
 }
 
 // Workgroups are dealt to the 8 XCDs in turn: the hw-th of `total` pieces of
-// work such that each XCD gets neighbouring ones.  False: none left.
+// work such that each XCD gets neighbouring ones, the first total % 8 XCDs
+// one more.  False: none left.
 __device__ __forceinline__ bool xcd_order(int64_t hw, int64_t total, int64_t& at)
 {
-    const int64_t each = (total + 7) / 8;
-    at = hw % 8 * each + hw / 8;
-    return hw / 8 < each && at < total;
+    const int64_t x = hw % 8, each = total / 8, more = total % 8;
+    at = x * each + min(x, more) + hw / 8;
+    return hw < total;
 }
 
 // The tile of this workgroup among `total`, and which of its row halves (-1:
-// both).  Whole rounds of one tile per compute unit first; if what remains
-// fills at most half the compute units, its tiles are done as two halves of
-// 128 rows each.
+// both).  Whole rounds of one tile per compute unit come first, each round
+// dealt so that an XCD gets neighbouring tiles of it (dealt over all rounds
+// at once, the XCD of the largest experts would finish last: 468 against
+// 354 us for a wgrad of 16 uneven experts, 8192 x 2560 x 5120).  If what remains fills at most
+// half the compute units, its tiles are done as two halves of 128 rows each.
 __device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, int& half)
 {
     const int64_t hw = blockIdx.x, rest = total % cus, full = total - rest;
     half = -1;
-    if (hw < full) return xcd_order(hw, full, at);
+    if (hw < full) {
+        if (!xcd_order(hw % cus, cus, at)) return false;
+        at += hw - hw % cus;
+        return true;
+    }
     const bool split = 2 * rest <= cus;
     if (!xcd_order(hw - full, split ? 2 * rest : rest, at)) return false;
     if (split) {
@@ -684,7 +703,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
     if (m0 >= mend) return;
     f32x16_t acc[2][2][2] = {};
     if (steps > 0) big_tile<f32x16_t, kPass == 2, kPass != 0>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
-    big_store<kPass != 0, kF32>(acc, m0, n0, mend, cols, lds, g.c, c_at, g.ldc,
+    big_store<kPass != 0, kF32, kPass == 2>(acc, m0, n0, mend, cols, lds, g.c, c_at, g.ldc,
                                 [](float v, int, int, int, int) { return v; });
 }
 
@@ -716,7 +735,7 @@ __global__ __launch_bounds__(512, 2) void k_i8_big(const int8_t* __restrict__ a,
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             col_scale[k][e] = sb[min(n0 + column0<false>(wn, k) + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3), N - 1)];
-    big_store<false, kF32>(acc, m0, n0, mend, N, lds, c, 0, ldc, [&](int v, int h, int i, int k, int e) {
+    big_store<false, kF32, false>(acc, m0, n0, mend, N, lds, c, 0, ldc, [&](int v, int h, int i, int k, int e) {
         return ((float)v * row_scale[h][i]) * col_scale[k][e];
     });
 }

@@ -293,9 +293,8 @@ __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t 
 // keep the LDS busy for about as long as the MFMAs take, and under full load
 // the power limit lowers the clock (1.5 to 1.7 GHz).
 // ---------------------------------------------------------------------------
-constexpr int kTile = 256;
 constexpr int kHalfBytes = 128 * 128;
-constexpr int kBufBytes = 4 * kHalfBytes;
+constexpr int kLdsBytes = 8 * kHalfBytes;
 
 __device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
 
@@ -327,14 +326,16 @@ __device__ __forceinline__ void barrier()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Where one thread's DMA pieces of an operand tile come from: instruction j
-// of half h at p + off[2 h + j] (N) or p + off[h] + 32 j k rows (T).
-template <bool kT>
+// Where one thread's DMA pieces of an operand tile of kHalves x 128 rows come
+// from in a workgroup of kThreads: instruction j of half h at
+// p + off[kLoads h + j] (N) or p + off[h] + kThreads / 16 * j k rows (T).
+template <bool kT, int kThreads, int kHalves>
 struct Source {
+    static constexpr int kLoads = kHalfBytes / (16 * kThreads);  // instructions of a half
     const uint8_t* p;
-    uint32_t off[kT ? 2 : 4];
-    int whole[2];           // steps of each half that lie wholly inside K
-    int64_t K[2], ld;       // K: 0 for a half of which nothing is used
+    uint32_t off[kT ? kHalves : kHalves * kLoads];
+    int whole[kHalves];     // steps of each half that lie wholly inside K
+    int64_t K[kHalves], ld; // K: 0 for a half of which nothing is used
 
     // the tile's first row r0; K in bytes (N) or k rows (T); second: whether
     // half 1 is used.  kPairs (N): half h holds the rows 32 h .. 32 h + 31 of
@@ -344,17 +345,18 @@ struct Source {
     {
         const int tid = threadIdx.x;
         ld = uniform(v.ld);
-        K[0] = uniform(K_);
-        K[1] = second ? K[0] : 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) whole[h] = (int)(K[h] >> (kT ? 6 : 7));
+        for (int h = 0; h < kHalves; ++h) {
+            K[h] = h == 0 || second ? uniform(K_) : 0;
+            whole[h] = (int)(K[h] >> (kT ? 6 : 7));
+        }
         if constexpr (!kT) {
             const int c = (tid & 7) ^ ((tid >> 4) & 7);
             const int last = (int)min(v.rows - 1 - r0, (int64_t)255);
             p = uniform(v.p + r0 * ld);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 64 * i + (tid >> 3);  // half r / 128
+            for (int i = 0; i < kHalves * kLoads; ++i) {
+                const int r = kThreads / 8 * i + (tid >> 3);  // half r / 128
                 const int row = kPairs ? (r >> 5 & 3) * 64 + (r >> 7) * 32 + (r & 31) : r;
                 off[i] = (uint32_t)min(row, last) * (uint32_t)ld + 16 * c;
             }
@@ -364,7 +366,7 @@ struct Source {
             const int last = (int)min(v.rows - 8 - r0, (int64_t)248);
             p = uniform(v.p + 2 * r0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kHalves; ++h)
                 off[h] = (uint32_t)kr * (uint32_t)ld + 2 * min(128 * h + 16 * block + 8 * (tid & 1), last);
         }
     }
@@ -374,17 +376,19 @@ struct Source {
     {
         const uint32_t at = lds + wave_id() * 1024;
         const uint8_t* step = p + (kT ? (int64_t)t * 64 * ld : (int64_t)t * 128);
+        constexpr int kRows = kThreads / 16;  // k rows of an instruction (T)
         if (t < whole[h]) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) dma16(kT ? step + 32 * j * ld : step, off[kT ? h : 2 * h + j], at + 8192 * j);
+            for (int j = 0; j < kLoads; ++j)
+                dma16(kT ? step + kRows * j * ld : step, off[kT ? h : kLoads * h + j], at + 16 * kThreads * j);
         } else {  // the last step's pieces past K, and the steps behind it: zeros
             const int tid = threadIdx.x;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int64_t k = kT ? (int64_t)t * 64 + 32 * j + (tid >> 4)
+            for (int j = 0; j < kLoads; ++j) {
+                const int64_t k = kT ? (int64_t)t * 64 + kRows * j + (tid >> 4)
                                      : (int64_t)t * 128 + 16 * ((tid & 7) ^ ((tid >> 4) & 7));
-                const uint8_t* src = (kT ? step + 32 * j * ld : step) + off[kT ? h : 2 * h + j];
-                dma16(k < K[h] ? src : kZeros, at + 8192 * j);
+                const uint8_t* src = (kT ? step + kRows * j * ld : step) + off[kT ? h : kLoads * h + j];
+                dma16(k < K[h] ? src : kZeros, at + 16 * kThreads * j);
             }
         }
     }
@@ -448,8 +452,8 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
                                          int64_t mend, int steps, uint8_t* lds, Acc (&acc)[2][2][2])
 {
     const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
-    Source<kTA> sa;
-    Source<kTB> sb;
+    Source<kTA, 512, 2> sa;
+    Source<kTB, 512, 2> sb;
     sa.set(A, m0, Ka, m0 + 128 < mend);
     sb.template set<!kTB>(B, n0, Kb, kTB ? n0 + 128 < B.rows : n0 + 32 < B.rows);
     // a wave's quadrants beyond the rows or columns are left out
@@ -461,7 +465,7 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
     // A's halves of both buffers, then B's: every place is within a 16-bit
     // offset of its operand's first
-    constexpr int kA0 = 0, kA1 = kHalfBytes, kB0 = kBufBytes, kB1 = kBufBytes + kHalfBytes, kNext = 2 * kHalfBytes;
+    constexpr int kA0 = 0, kA1 = kHalfBytes, kB0 = 4 * kHalfBytes, kB1 = 5 * kHalfBytes, kNext = 2 * kHalfBytes;
 
     sb.fetch(0, 0, base + kB0);
     sa.fetch(0, 0, base + kA0);
@@ -525,6 +529,70 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
     barrier();  // nothing is on its way into LDS or being read any more
 }
 
+// ---------------------------------------------------------------------------
+// Fewer tiles than compute units: a workgroup of 4 waves computes 128 x 128
+// outputs, with the same places in LDS.  Four buffers of 32 KB hold steps t
+// to t + 3, because a tile that has a compute unit to itself waits for memory
+// (a step's latency is 1.0 to 1.4 us, its MFMAs take 0.25): the DMA of step
+// t + 4 starts when every wave's reads of step t have come back.  Wave
+// (wm, wn) of 2 x 2 owns 64 x 64; it reads the fragments of the next step
+// while it multiplies those of this one.
+// ---------------------------------------------------------------------------
+template <class Acc, bool kTA, bool kTB>
+__device__ __forceinline__ void mid_tile(const View& A, const View& B, int64_t m0, int64_t n0, int64_t Ka, int64_t Kb,
+                                         int64_t mend, int steps, uint8_t* lds, Acc (&acc)[2][2])
+{
+    const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
+    Source<kTA, 256, 1> sa;
+    Source<kTB, 256, 1> sb;
+    sa.set(A, m0, Ka, true);
+    sb.set(B, n0, Kb, true);
+    const bool used = m0 + 64 * wm < mend && n0 + 64 * wn < B.rows;
+    const Fragments<kTA, 2> fa(2 * wm);
+    const Fragments<kTB, 2> fb(2 * wn);
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    constexpr int kB = 4 * kHalfBytes;  // B's buffers lie behind A's
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        sa.fetch(0, t, base + t * kHalfBytes);
+        sb.fetch(0, t, base + t * kHalfBytes + kB);
+    }
+    uint4 a[2][2][4], b[2][2][4];
+    wait_dma<24>();
+    barrier();
+    if (used) {
+        fa.read(a[0], lds);
+        fb.read(b[0], lds + kB);
+    }
+    auto step = [&](int t, int cur) {
+        wait_lds();
+        wait_dma<16>();  // all but steps t + 2 and t + 3
+        barrier();
+        const int next = ((t + 1) & 3) * kHalfBytes, fill = (t & 3) * kHalfBytes;
+        if (used) {
+            fa.read(a[cur ^ 1], lds + next);
+            fb.read(b[cur ^ 1], lds + next + kB);
+        }
+        sa.fetch(0, t + 4, base + fill);
+        sb.fetch(0, t + 4, base + fill + kB);
+        if (used) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[j][i] = mma(b[cur][j][s], a[cur][i][s], acc[j][i]);
+        }
+    };
+    for (int t = 0; t < steps; t += 2) {
+        step(t, 0);
+        if (t + 1 < steps) step(t + 1, 1);
+    }
+    wait_lds();
+    wait_dma<0>();
+    barrier();  // nothing is on its way into LDS or being read any more
+}
+
 // kStream: past the caches (a weight gradient is larger than they are).
 template <bool kStream>
 __device__ __forceinline__ void store16(void* d, uint4 v)
@@ -536,81 +604,134 @@ __device__ __forceinline__ void store16(void* d, uint4 v)
         *static_cast<uint4*>(d) = v;
 }
 
-// The tile's outputs.  value(v, h, i, k, e): accumulator e of the MFMA tile
-// of A half h, tile i and B half k as a float.  Each wave stages 64 rows of 128 bytes in its own
-// 8 KB of LDS (16-byte piece c of row r at c ^ r % 8, which spreads both the
-// writes, a row per lane, and the reads, a row per 8 lanes, over the banks)
-// and stores 8 whole row pieces of 128 bytes at a time.
-template <bool kTB, bool kF32, bool kStream, class Acc, class Value>
-__device__ __forceinline__ void big_store(const Acc (&acc)[2][2][2], int64_t m0, int64_t n0, int64_t mend, int64_t N,
-                                          uint8_t* lds, void* c, int64_t c_at, int64_t ldc, const Value& value)
+// 64 x 64 outputs of a wave: rows row0 .., columns col[0] .. + 31 and
+// col[1] .. + 31; value(i, k, e): accumulator e of row tile i and column tile
+// k as a float.  The wave stages 64 rows of 128 bytes in its own 8 KB of LDS
+// (16-byte piece c of row r at c ^ r % 8, which spreads both the writes, a
+// row per lane, and the reads, a row per 8 lanes, over the banks) and stores
+// 8 row pieces of 128 bytes at a time.
+template <bool kF32, bool kStream, class Value>
+__device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const int64_t (&col)[2], int64_t mend, int64_t N,
+                                           void* c, int64_t c_at, int64_t ldc, const Value& value)
 {
-    const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave >> 2, wn = wave & 3;
-    uint8_t* stage = lds + wave * 8192;
+    const int lane = threadIdx.x & 63, g = lane >> 5;
     const bool wide = (reinterpret_cast<uintptr_t>(c) & 15) == 0 && (kF32 || ((ldc | c_at) & 7) == 0);
-    constexpr int kCols = kF32 ? 4 : 8;       // columns of a piece
-    constexpr int kUnits = kF32 ? 2 : 1;      // stagings for the 64 columns of a half of A
-    const int g = lane >> 5;
+    constexpr int kCols = kF32 ? 4 : 8;   // columns of a piece
+    constexpr int kUnits = kF32 ? 2 : 1;  // stagings for the 64 columns
+    if (row0 >= mend) return;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t row0 = m0 + 128 * h + 64 * wm;
-        if (row0 >= mend) continue;
+    for (int u = 0; u < kUnits; ++u) {
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
+        for (int i = 0; i < 2; ++i) {
+            const int r = 32 * i + (lane & 31);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 32 * i + (lane & 31);
+            for (int k = kF32 ? u : 0; k < (kF32 ? u + 1 : 2); ++k)
 #pragma unroll
-                for (int k = kF32 ? u : 0; k < (kF32 ? u + 1 : 2); ++k) {
+                for (int q = 0; q < 4; ++q) {
+                    float y[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float y[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) y[j] = value(acc[h][k][i][4 * q + j], h, i, k, 4 * q + j);
-                        uint8_t* row = stage + 128 * r;
-                        if constexpr (kF32) {
-                            *reinterpret_cast<float4*>(row + (((2 * q + g) ^ (r & 7)) << 4)) =
-                                make_float4(y[0], y[1], y[2], y[3]);
-                        } else {
-                            *reinterpret_cast<uint2*>(row + (((4 * k + q) ^ (r & 7)) << 4) + 8 * g) =
-                                make_uint2(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]));
-                        }
-                    }
+                    for (int j = 0; j < 4; ++j) y[j] = value(i, k, 4 * q + j);
+                    uint8_t* row = stage + 128 * r;
+                    if constexpr (kF32)
+                        *reinterpret_cast<float4*>(row + (((2 * q + g) ^ (r & 7)) << 4)) =
+                            make_float4(y[0], y[1], y[2], y[3]);
+                    else
+                        *reinterpret_cast<uint2*>(row + (((4 * k + q) ^ (r & 7)) << 4) + 8 * g) =
+                            make_uint2(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]));
                 }
-            }
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                const int r = 8 * it + (lane >> 3), p = lane & 7;
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + 128 * r + ((p ^ (r & 7)) << 4));
-                const int64_t m = row0 + r;
-                const int64_t n = n0 + (kF32 ? column0<kTB>(wn, u) + 4 * p : column0<kTB>(wn, p >> 2) + 8 * (p & 3));
-                if (m >= mend || n >= N) continue;
-                const int64_t at = c_at + m * ldc + n;
-                if constexpr (kF32) {
-                    float* d = static_cast<float*>(c) + at;
-                    if (n + 4 <= N) {
-                        store16<kStream>(d, v);
-                    } else {
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < kCols; ++j)
-                            if (n + j < N) d[j] = __uint_as_float(w[j]);
-                    }
-                } else {
-                    uint16_t* d = static_cast<uint16_t*>(c) + at;
-                    if (wide && n + 8 <= N) {
-                        store16<kStream>(d, v);
-                    } else {
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < kCols; ++j)
-                            if (n + j < N) d[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-                    }
-                }
-            }
-            __builtin_amdgcn_wave_barrier();
         }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+            const int r = 8 * it + (lane >> 3), p = lane & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + 128 * r + ((p ^ (r & 7)) << 4));
+            const int64_t m = row0 + r;
+            const int64_t n = kF32 ? col[u] + 4 * p : (p < 4 ? col[0] : col[1]) + 8 * (p & 3);
+            if (m >= mend || n >= N) continue;
+            const int64_t at = c_at + m * ldc + n;
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if constexpr (kF32) {
+                float* d = static_cast<float*>(c) + at;
+                if (n + 4 <= N) {
+                    store16<kStream>(d, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j)
+                        if (n + j < N) d[j] = __uint_as_float(w[j]);
+                }
+            } else {
+                uint16_t* d = static_cast<uint16_t*>(c) + at;
+                if (wide && n + 8 <= N) {
+                    store16<kStream>(d, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j)
+                        if (n + j < N) d[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+                }
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Sums as they are.
+struct Plain {
+    __device__ __forceinline__ void row(int, int, int64_t) {}
+    __device__ __forceinline__ void columns(int, int64_t, int) {}
+    __device__ __forceinline__ float operator()(float v, int, int, int, int) const { return v; }
+};
+
+// Integer sums times the scales of their row and column.
+struct Scaled {
+    const float *sa, *sb;
+    int64_t M, N;
+    float rows[2][2], cols[2][16];
+
+    __device__ __forceinline__ Scaled(const float* sa_, const float* sb_, int64_t M_, int64_t N_)
+        : sa(sa_), sb(sb_), M(M_), N(N_)
+    {
+    }
+    __device__ __forceinline__ void row(int h, int i, int64_t m) { rows[h][i] = sa[min(m, M - 1)]; }
+    // columns n + first + 8 (e / 4) + e % 4 of accumulators e
+    __device__ __forceinline__ void columns(int k, int64_t n, int first)
+    {
+        const int64_t at = min(n, N - 1);
+        const int last = (int)min(N - 1 - at, (int64_t)31);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) cols[k][e] = (sb + at)[min(first + 8 * (e >> 2) + (e & 3), last)];
+    }
+    __device__ __forceinline__ float operator()(int v, int h, int i, int k, int e) const
+    {
+        return ((float)v * rows[h][i]) * cols[k][e];
+    }
+};
+
+// The products of one tile (kBig: 256 x 256 by 8 waves, else 128 x 128 by 4)
+// and their way into memory.
+template <bool kBig, class Acc, bool kTA, bool kTB, bool kF32, bool kStream, class Convert>
+__device__ __forceinline__ void tile(const View& A, const View& B, int64_t m0, int64_t n0, int64_t Ka, int64_t Kb,
+                                     int64_t mend, int steps, uint8_t* lds, void* c, int64_t c_at, int64_t ldc,
+                                     Convert convert)
+{
+    constexpr int kHalves = kBig ? 2 : 1;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int wm = kBig ? wave >> 2 : wave >> 1, wn = kBig ? wave & 3 : wave & 1;
+    Acc acc[kHalves][2][2] = {};  // [half of A][column piece][32 rows]
+    if constexpr (kBig) {
+        if (steps > 0) big_tile<Acc, kTA, kTB>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
+    } else {
+        if (steps > 0) mid_tile<Acc, kTA, kTB>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc[0]);
+    }
+    const int64_t col[2] = {n0 + (kBig ? column0<kTB>(wn, 0) : 64 * wn), n0 + (kBig ? column0<kTB>(wn, 1) : 64 * wn + 32)};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) convert.columns(k, col[k], 4 * (lane >> 5));
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+        const int64_t row0 = m0 + 128 * h + 64 * wm;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) convert.row(h, i, row0 + 32 * i + (lane & 31));
+        store_wave<kF32, kStream>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc,
+                                  [&](int i, int k, int e) { return convert(acc[h][k][i][e], h, i, k, e); });
     }
 }
 
@@ -639,6 +760,7 @@ __device__ __forceinline__ bool xcd_order(int64_t hw, int64_t total, int64_t& at
 // at once, the XCD of the largest experts would finish last: 468 against
 // 354 us for a wgrad of 16 uneven experts, 8192 x 2560 x 5120).  If what remains fills at most
 // half the compute units, its tiles are done as two halves of 128 rows each.
+template <bool kBig>
 __device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, int& half)
 {
     const int64_t hw = blockIdx.x, rest = total % cus, full = total - rest;
@@ -648,7 +770,7 @@ __device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, 
         at += hw - hw % cus;
         return true;
     }
-    const bool split = 2 * rest <= cus;
+    const bool split = kBig && 2 * rest <= cus;
     if (!xcd_order(hw - full, split ? 2 * rest : rest, at)) return false;
     if (split) {
         half = (int)(at & 1);
@@ -662,10 +784,11 @@ constexpr int kThinM = 2, kThinN = 2;
 
 }  // namespace
 
-template <int kPass, bool kF32>
-__global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
+template <bool kBig, int kPass, bool kF32>
+__global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_grouped(GroupedArgs g)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBufBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLdsBytes];
+    constexpr int kTile = kBig ? 256 : 128;
     const int64_t cols = kPass == 0 ? g.N : g.K;
     const int tn = (int)((cols + kTile - 1) / kTile);
     View A, B;
@@ -673,7 +796,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
     int steps, im, in_, half;
     if constexpr (kPass == 2) {
         const int tm = (int)((g.N + kTile - 1) / kTile);
-        if (!tile_order(g.E * tm * tn, g.cus, at, half)) return;
+        if (!tile_order<kBig>(g.E * tm * tn, g.cus, at, half)) return;
         const int64_t e = at / (tm * tn);
         grouped_order((int)(at % (tm * tn)), tm, tn, im, in_);
         int64_t begin, end;
@@ -684,7 +807,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
         steps = (int)((end - begin + 63) / 64);
         c_at = e * g.c_expert;
     } else {
-        if (!tile_order((int64_t)tn * count_tiles(g.ends, g.E, g.T, kTile), g.cus, at, half)) return;
+        if (!tile_order<kBig>((int64_t)tn * count_tiles(g.ends, g.E, g.T, kTile), g.cus, at, half)) return;
         Slice s;
         if (!find_slice(g.ends, g.E, g.T, kTile, tn, at, s)) return;
         grouped_order((int)s.tile, (int)((s.end - s.begin + kTile - 1) / kTile), tn, im, in_);
@@ -701,43 +824,28 @@ __global__ __launch_bounds__(512, 2) void k_grouped_big(GroupedArgs g)
     n0 = (int64_t)kTile * in_;
     mend = half == 0 ? min(m0 + 128, A.rows) : A.rows;
     if (m0 >= mend) return;
-    f32x16_t acc[2][2][2] = {};
-    if (steps > 0) big_tile<f32x16_t, kPass == 2, kPass != 0>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
-    big_store<kPass != 0, kF32, kPass == 2>(acc, m0, n0, mend, cols, lds, g.c, c_at, g.ldc,
-                                [](float v, int, int, int, int) { return v; });
+    tile<kBig, f32x16_t, kPass == 2, kPass != 0, kF32, kPass == 2>(A, B, m0, n0, Ka, Kb, mend, steps, lds, g.c, c_at, g.ldc,
+                                                                   Plain());
 }
 
-template <bool kF32>
-__global__ __launch_bounds__(512, 2) void k_i8_big(const int8_t* __restrict__ a, int64_t lda, const float* __restrict__ sa,
-                                                   const int8_t* __restrict__ b, int64_t ldb, const float* __restrict__ sb,
-                                                   int64_t M, int64_t N, int64_t K, void* __restrict__ c, int64_t ldc, int cus)
+template <bool kBig, bool kF32>
+__global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_i8(
+    const int8_t* __restrict__ a, int64_t lda, const float* __restrict__ sa, const int8_t* __restrict__ b, int64_t ldb,
+    const float* __restrict__ sb, int64_t M, int64_t N, int64_t K, void* __restrict__ c, int64_t ldc, int cus)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kBufBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLdsBytes];
+    constexpr int kTile = kBig ? 256 : 128;
     const int tm = (int)((M + kTile - 1) / kTile), tn = (int)((N + kTile - 1) / kTile);
     int64_t at;
     int im, in_, half;
-    if (!tile_order((int64_t)tm * tn, cus, at, half)) return;
+    if (!tile_order<kBig>((int64_t)tm * tn, cus, at, half)) return;
     grouped_order((int)at, tm, tn, im, in_);
     const View A{reinterpret_cast<const uint8_t*>(a), lda, M}, B{reinterpret_cast<const uint8_t*>(b), ldb, N};
     const int64_t m0 = (int64_t)kTile * im + (half == 1 ? 128 : 0), n0 = (int64_t)kTile * in_;
     const int64_t mend = half == 0 ? min(m0 + 128, M) : M;
     if (m0 >= mend) return;
-    i32x16_t acc[2][2][2] = {};
-    if (K > 0) big_tile<i32x16_t, false, false>(A, B, m0, n0, K, K, mend, (int)((K + 127) / 128), lds, acc);
-    const int lane = threadIdx.x & 63, wm = wave_id() >> 2, wn = wave_id() & 3;
-    float row_scale[2][2], col_scale[2][16];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) row_scale[h][i] = sa[min(m0 + 128 * h + 64 * wm + 32 * i + (lane & 31), M - 1)];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            col_scale[k][e] = sb[min(n0 + column0<false>(wn, k) + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3), N - 1)];
-    big_store<false, kF32, false>(acc, m0, n0, mend, N, lds, c, 0, ldc, [&](int v, int h, int i, int k, int e) {
-        return ((float)v * row_scale[h][i]) * col_scale[k][e];
-    });
+    tile<kBig, i32x16_t, false, false, kF32, false>(A, B, m0, n0, K, K, mend, (int)((K + 127) / 128), lds, c, 0, ldc,
+                                                    Scaled(sa, sb, M, N));
 }
 
 template <int kPass, bool kF32>
@@ -798,68 +906,95 @@ __global__ __launch_bounds__(256) void k_i8_thin(const int8_t* __restrict__ a, i
         });
 }
 
-void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb, const float* sb,
-                    int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, int cus, hipStream_t s)
-{
-    if (M == 0 || N == 0) return;
-    if (M > 64) {
-        const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-        const dim3 big((uint32_t)(tiles + cus + 8));  // the remainder may be done in halves
-        if (out_fp32)
-            hipLaunchKernelGGL(k_i8_big<true>, big, dim3(512), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc, cus);
-        else
-            hipLaunchKernelGGL(k_i8_big<false>, big, dim3(512), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc, cus);
-        return;
-    }
-    const int64_t grid = (M + 16 * kThinM - 1) / (16 * kThinM) * ((N + 16 * kThinN - 1) / (16 * kThinN));
-    if (out_fp32)
-        hipLaunchKernelGGL(k_i8_thin<true>, dim3((uint32_t)grid), dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
-    else
-        hipLaunchKernelGGL(k_i8_thin<false>, dim3((uint32_t)grid), dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
-}
-
 namespace {
 
-template <int kPass>
-void launch_grouped_big(const GroupedArgs& g, bool out_fp32, hipStream_t s)
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Whether tiles of 256 x 256 finish sooner than those of 128 x 128, from the
+// rounds of tiles that the compute units take: a step of a big tile takes
+// about 1.1 us and one of a small tile 0.45 us.
+bool big_tiles(int64_t big, int64_t mid, int cus)
 {
-    const int64_t cols = ((kPass == 0 ? g.N : g.K) + kTile - 1) / kTile;
-    const int64_t rows = kPass == 2 ? g.E * ((g.N + kTile - 1) / kTile) : g.T / kTile + g.E + 1;
-    const dim3 grid((uint32_t)(rows * cols + g.cus + 8));  // the remainder may be done in halves
+    const double b = big % cus * 2 <= cus ? big / cus + (big % cus ? 0.9 : 0.0) : (double)ceil_div(big, cus);
+    return 1.1 * b <= 0.45 * ceil_div(mid, cus);
+}
+
+template <bool kBig, bool kF32>
+void launch_i8_tiles(const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb, const float* sb,
+                     int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, int cus, hipStream_t s)
+{
+    const int64_t t = kBig ? 256 : 128, tiles = ceil_div(M, t) * ceil_div(N, t);
+    const dim3 grid((uint32_t)(tiles + (kBig ? cus : 0)));  // the remainder may be done in halves
+    hipLaunchKernelGGL((k_i8<kBig, kF32>), grid, dim3(kBig ? 512 : 256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc,
+                       cus);
+}
+
+template <bool kBig, int kPass>
+void launch_grouped_tiles(const GroupedArgs& g, bool out_fp32, hipStream_t s)
+{
+    const int64_t t = kBig ? 256 : 128;
+    // every expert, and the rows of none, can have one partial row tile
+    const int64_t rows = kPass == 2 ? g.E * ceil_div(g.N, t) : g.T / t + g.E + 1;
+    const dim3 grid((uint32_t)(rows * ceil_div(kPass == 0 ? g.N : g.K, t) + (kBig ? g.cus : 0)));
     if (out_fp32)
-        hipLaunchKernelGGL((k_grouped_big<kPass, true>), grid, dim3(512), 0, s, g);
+        hipLaunchKernelGGL((k_grouped<kBig, kPass, true>), grid, dim3(kBig ? 512 : 256), 0, s, g);
     else
-        hipLaunchKernelGGL((k_grouped_big<kPass, false>), grid, dim3(512), 0, s, g);
+        hipLaunchKernelGGL((k_grouped<kBig, kPass, false>), grid, dim3(kBig ? 512 : 256), 0, s, g);
 }
 
 template <int kPass>
 void launch_grouped_thin(const GroupedArgs& g, bool out_fp32, hipStream_t s)
 {
-    const int64_t tm = 16 * kThinM, tn = 16 * kThinN;
-    const int64_t cols = ((kPass == 0 ? g.N : g.K) + tn - 1) / tn;
-    // every expert, and the rows of none, can have one partial row tile
-    const int64_t rows = kPass == 2 ? g.E * ((g.N + tm - 1) / tm) : g.T / tm + g.E + 1;
+    const int64_t cols = ceil_div(kPass == 0 ? g.N : g.K, 16 * kThinN);
+    const int64_t rows = g.T / (16 * kThinM) + g.E + 1;
     if (out_fp32)
         hipLaunchKernelGGL((k_grouped_thin<kPass, true>), dim3((uint32_t)(rows * cols)), dim3(256), 0, s, g);
     else
         hipLaunchKernelGGL((k_grouped_thin<kPass, false>), dim3((uint32_t)(rows * cols)), dim3(256), 0, s, g);
 }
 
+template <int kPass>
+void launch_grouped_pass(const GroupedArgs& g, bool out_fp32, hipStream_t s)
+{
+    const int64_t cols = kPass == 0 ? g.N : g.K;
+    if (kPass == 0 && g.T <= 32 * g.E) return launch_grouped_thin<0>(g, out_fp32, s);
+    // row tiles: half of every expert's last one is taken as empty
+    const int64_t rows = kPass == 2 ? g.N : g.T;
+    const int64_t big = kPass == 2 ? g.E * ceil_div(rows, 256) : g.T / 256 + (g.E + 1) / 2;
+    const int64_t mid = kPass == 2 ? g.E * ceil_div(rows, 128) : g.T / 128 + (g.E + 1) / 2;
+    if (big_tiles(big * ceil_div(cols, 256), mid * ceil_div(cols, 128), g.cus))
+        launch_grouped_tiles<true, kPass>(g, out_fp32, s);
+    else
+        launch_grouped_tiles<false, kPass>(g, out_fp32, s);
+}
+
 }  // namespace
+
+void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb, const float* sb,
+                    int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, int cus, hipStream_t s)
+{
+    if (M == 0 || N == 0) return;
+    if (M <= 64) {
+        const dim3 grid((uint32_t)(ceil_div(M, 16 * kThinM) * ceil_div(N, 16 * kThinN)));
+        if (out_fp32)
+            hipLaunchKernelGGL(k_i8_thin<true>, grid, dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
+        else
+            hipLaunchKernelGGL(k_i8_thin<false>, grid, dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
+        return;
+    }
+    const bool big = big_tiles(ceil_div(M, 256) * ceil_div(N, 256), ceil_div(M, 128) * ceil_div(N, 128), cus);
+    const auto launch = big ? (out_fp32 ? launch_i8_tiles<true, true> : launch_i8_tiles<true, false>)
+                            : (out_fp32 ? launch_i8_tiles<false, true> : launch_i8_tiles<false, false>);
+    launch(a, lda, sa, b, ldb, sb, M, N, K, c, ldc, cus, s);
+}
 
 void launch_grouped(int pass, const GroupedArgs& g, bool out_fp32, hipStream_t s)
 {
     const int64_t rows = pass == 2 ? g.E * g.N : g.T, cols = pass == 0 ? g.N : g.K;
     if (rows == 0 || cols == 0) return;  // (an empty contraction still writes zeros)
-    if (g.T > 32 * g.E) {
-        if (pass == 0) launch_grouped_big<0>(g, out_fp32, s);
-        else if (pass == 1) launch_grouped_big<1>(g, out_fp32, s);
-        else launch_grouped_big<2>(g, out_fp32, s);
-        return;
-    }
-    if (pass == 0) launch_grouped_thin<0>(g, out_fp32, s);
-    else if (pass == 1) launch_grouped_thin<1>(g, out_fp32, s);
-    else launch_grouped_thin<2>(g, out_fp32, s);
+    if (pass == 0) launch_grouped_pass<0>(g, out_fp32, s);
+    else if (pass == 1) launch_grouped_pass<1>(g, out_fp32, s);
+    else launch_grouped_pass<2>(g, out_fp32, s);
 }
 
 }  // namespace nvfp4

@@ -327,71 +327,69 @@ __device__ __forceinline__ void barrier()
 }
 
 // Where one thread's DMA pieces of an operand tile of kHalves x 128 rows come
-// from in a workgroup of kThreads: instruction j of half h at
-// p + off[kLoads h + j] (N) or p + off[h] + kThreads / 16 * j k rows (T).
+// from in a workgroup of kThreads: instruction j of half h of a step at the
+// step's base + off[kLoads h + j].  Steps that lie wholly inside K take the
+// short way (a scalar base and a 32-bit offset; the loops spend more of their
+// time on such overhead than on the transfers); the others check each piece.
 template <bool kT, int kThreads, int kHalves>
 struct Source {
     static constexpr int kLoads = kHalfBytes / (16 * kThreads);  // instructions of a half
     const uint8_t* p;
-    uint32_t off[kT ? kHalves : kHalves * kLoads];
-    int whole[kHalves];     // steps of each half that lie wholly inside K
-    int64_t K[kHalves], ld; // K: 0 for a half of which nothing is used
+    uint32_t off[kHalves * kLoads];
+    int64_t K, advance;  // K in bytes (N) or k rows (T); bytes from step to step
 
-    // the tile's first row r0; K in bytes (N) or k rows (T); second: whether
-    // half 1 is used.  kPairs (N): half h holds the rows 32 h .. 32 h + 31 of
-    // every 64, so that a wave's two 32-column pieces are neighbours.
+    // the tile's first row r0; second: whether half 1 is used (if not, its
+    // lanes all read one place).  kPairs (N): half h holds the rows 32 h ..
+    // 32 h + 31 of every 64, so that a wave's two 32-column pieces are neighbours.
     template <bool kPairs = false>
     __device__ __forceinline__ void set(const View& v, int64_t r0, int64_t K_, bool second)
     {
         const int tid = threadIdx.x;
-        ld = uniform(v.ld);
+        const int64_t ld = uniform(v.ld);
+        K = uniform(K_);
+        advance = kT ? 64 * ld : 128;
+        p = uniform(v.p + (kT ? 2 * r0 : r0 * ld));
+        const int last = (int)min(v.rows - (kT ? 8 : 1) - r0, (int64_t)255);
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-            K[h] = h == 0 || second ? uniform(K_) : 0;
-            whole[h] = (int)(K[h] >> (kT ? 6 : 7));
-        }
-        if constexpr (!kT) {
-            const int c = (tid & 7) ^ ((tid >> 4) & 7);
-            const int last = (int)min(v.rows - 1 - r0, (int64_t)255);
-            p = uniform(v.p + r0 * ld);
-#pragma unroll
-            for (int i = 0; i < kHalves * kLoads; ++i) {
+        for (int i = 0; i < kHalves * kLoads; ++i) {
+            if constexpr (!kT) {
                 const int r = kThreads / 8 * i + (tid >> 3);  // half r / 128
                 const int row = kPairs ? (r >> 5 & 3) * 64 + (r >> 7) * 32 + (r & 31) : r;
-                off[i] = (uint32_t)min(row, last) * (uint32_t)ld + 16 * c;
+                off[i] = (uint32_t)min(row, last) * (uint32_t)ld + 16 * ((tid & 7) ^ ((tid >> 4) & 7));
+            } else {
+                const int kr = kThreads / 16 * (i % kLoads) + (tid >> 4);
+                const int block = ((tid & 15) >> 1) ^ ((kr & 3) | (((kr >> 3) & 1) << 2));
+                off[i] = (uint32_t)kr * (uint32_t)ld +
+                         2 * min(128 * (i / kLoads) + 16 * block + 8 * (tid & 1), last);
             }
-        } else {
-            const int kr = tid >> 4;
-            const int block = ((tid & 15) >> 1) ^ ((kr & 3) | (((kr >> 3) & 1) << 2));
-            const int last = (int)min(v.rows - 8 - r0, (int64_t)248);
-            p = uniform(v.p + 2 * r0);
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-                off[h] = (uint32_t)kr * (uint32_t)ld + 2 * min(128 * h + 16 * block + 8 * (tid & 1), last);
+            if (i >= kLoads && !second) off[i] = 0;
         }
     }
 
-    // half `h` of step t into LDS at `lds`
-    __device__ __forceinline__ void fetch(int h, int t, uint32_t lds) const
+    // half `h` of step t, which lies wholly inside K, into LDS at `lds`;
+    // base: p + t * advance
+    __device__ __forceinline__ void fetch(int h, const uint8_t* base, uint32_t lds) const
     {
         const uint32_t at = lds + wave_id() * 1024;
-        const uint8_t* step = p + (kT ? (int64_t)t * 64 * ld : (int64_t)t * 128);
-        constexpr int kRows = kThreads / 16;  // k rows of an instruction (T)
-        if (t < whole[h]) {
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-                dma16(kT ? step + kRows * j * ld : step, off[kT ? h : kLoads * h + j], at + 16 * kThreads * j);
-        } else {  // the last step's pieces past K, and the steps behind it: zeros
-            const int tid = threadIdx.x;
+        for (int j = 0; j < kLoads; ++j) dma16(base, off[kLoads * h + j], at + 16 * kThreads * j);
+    }
+
+    // the same of any step: zeros for the pieces past K
+    __device__ __forceinline__ void fetch_checked(int h, int t, uint32_t lds) const
+    {
+        const uint32_t at = lds + wave_id() * 1024;
+        const uint8_t* base = p + t * advance;
+        const int tid = threadIdx.x;
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int64_t k = kT ? (int64_t)t * 64 + kRows * j + (tid >> 4)
-                                     : (int64_t)t * 128 + 16 * ((tid & 7) ^ ((tid >> 4) & 7));
-                const uint8_t* src = (kT ? step + kRows * j * ld : step) + off[kT ? h : kLoads * h + j];
-                dma16(k < K[h] ? src : kZeros, at + 16 * kThreads * j);
-            }
+        for (int j = 0; j < kLoads; ++j) {
+            const int64_t k = kT ? (int64_t)t * 64 + kThreads / 16 * j + (tid >> 4)
+                                 : (int64_t)t * 128 + 16 * ((tid & 7) ^ ((tid >> 4) & 7));
+            dma16(k < K ? base + off[kLoads * h + j] : kZeros, at + 16 * kThreads * j);
         }
     }
+
+    __device__ __forceinline__ int whole() const { return (int)(K >> (kT ? 6 : 7)); }
 };
 
 // A lane's fragments of 32-row tiles of one half: kTiles tiles from tile
@@ -467,13 +465,13 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
     // offset of its operand's first
     constexpr int kA0 = 0, kA1 = kHalfBytes, kB0 = 4 * kHalfBytes, kB1 = 5 * kHalfBytes, kNext = 2 * kHalfBytes;
 
-    sb.fetch(0, 0, base + kB0);
-    sa.fetch(0, 0, base + kA0);
-    sb.fetch(1, 0, base + kB1);
-    sa.fetch(1, 0, base + kA1);
-    sb.fetch(0, 1, base + kNext + kB0);
-    sa.fetch(0, 1, base + kNext + kA0);
-    sb.fetch(1, 1, base + kNext + kB1);
+    sb.fetch_checked(0, 0, base + kB0);
+    sa.fetch_checked(0, 0, base + kA0);
+    sb.fetch_checked(1, 0, base + kB1);
+    sa.fetch_checked(1, 0, base + kA1);
+    sb.fetch_checked(0, 1, base + kNext + kB0);
+    sa.fetch_checked(0, 1, base + kNext + kA0);
+    sb.fetch_checked(1, 1, base + kNext + kB1);
     uint4 a[2][4], b[2][1][4];
     wait_dma<10>();
     barrier();
@@ -498,31 +496,47 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
         wait_dma<10>();
         barrier();
     };
-    // one step from buffer `buf`; b0 holds its B half 0, b1 takes its half 1 and then the next step's half 0
-    auto step = [&](int t, int buf, uint4(&b0)[1][4], uint4(&b1)[1][4]) {
+    // One step from buffer `buf`; b0 holds its B half 0, b1 takes its half 1
+    // and then the next step's half 0.  pa1, pa2, pb2: the operands' bases of
+    // steps t + 1 and t + 2, used if those lie wholly inside K.
+    const uint8_t *pa1 = sa.p + sa.advance, *pb2 = sb.p + 2 * sb.advance;
+    auto step = [&](int t, int buf, uint4(&b0)[1][4], uint4(&b1)[1][4], auto whole) {
         const uint8_t* cur = lds + buf * kNext;
         const uint8_t* nxt = lds + (buf ^ 1) * kNext;
         const uint32_t fill = base + buf * kNext, other = base + (buf ^ 1) * kNext;
+        const uint8_t* pa2 = pa1 + sa.advance;
         if (rows0) fa.read(a, cur + kA0);
-        sa.fetch(1, t + 1, other + kA1);
+        if constexpr (whole.value) sa.fetch(1, pa1, other + kA1);
+        else sa.fetch_checked(1, t + 1, other + kA1);
         between();
         multiply(acc[0][0], b0, rows0 && cols0);
         fb.read(b1, cur + kB1);
-        sb.fetch(0, t + 2, fill + kB0);
+        if constexpr (whole.value) sb.fetch(0, pb2, fill + kB0);
+        else sb.fetch_checked(0, t + 2, fill + kB0);
         between();
         multiply(acc[0][1], b1, rows0 && cols1);
         if (rows1) fa.read(a, cur + kA1);
-        sa.fetch(0, t + 2, fill + kA0);
+        if constexpr (whole.value) sa.fetch(0, pa2, fill + kA0);
+        else sa.fetch_checked(0, t + 2, fill + kA0);
         between();
         multiply(acc[1][1], b1, rows1 && cols1);
         fb.read(b1, nxt + kB0);
-        sb.fetch(1, t + 2, fill + kB1);
+        if constexpr (whole.value) sb.fetch(1, pb2, fill + kB1);
+        else sb.fetch_checked(1, t + 2, fill + kB1);
         between();
         multiply(acc[1][0], b0, rows1 && cols0);
+        pa1 = pa2;
+        pb2 += sb.advance;
     };
-    for (int t = 0; t < steps; t += 2) {
-        step(t, 0, b[0], b[1]);
-        if (t + 1 < steps) step(t + 1, 1, b[1], b[0]);
+    const int whole = min(sa.whole(), sb.whole());
+    int t = 0;
+    for (; t + 3 < whole; t += 2) {
+        step(t, 0, b[0], b[1], std::true_type());
+        step(t + 1, 1, b[1], b[0], std::true_type());
+    }
+    for (; t < steps; t += 2) {
+        step(t, 0, b[0], b[1], std::false_type());
+        if (t + 1 < steps) step(t + 1, 1, b[1], b[0], std::false_type());
     }
     if (wm == 0) barrier();
     wait_dma<0>();
@@ -554,8 +568,8 @@ __device__ __forceinline__ void mid_tile(const View& A, const View& B, int64_t m
     constexpr int kB = 4 * kHalfBytes;  // B's buffers lie behind A's
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        sa.fetch(0, t, base + t * kHalfBytes);
-        sb.fetch(0, t, base + t * kHalfBytes + kB);
+        sa.fetch_checked(0, t, base + t * kHalfBytes);
+        sb.fetch_checked(0, t, base + t * kHalfBytes + kB);
     }
     uint4 a[2][2][4], b[2][2][4];
     wait_dma<24>();
@@ -564,29 +578,50 @@ __device__ __forceinline__ void mid_tile(const View& A, const View& B, int64_t m
         fa.read(a[0], lds);
         fb.read(b[0], lds + kB);
     }
-    auto step = [&](int t, int cur) {
+    const uint8_t *pa = sa.p + 4 * sa.advance, *pb = sb.p + 4 * sb.advance;  // the operands' bases of step t + 4
+    // buf: t % 4
+    auto step = [&](int t, int buf, auto whole) {
         wait_lds();
         wait_dma<16>();  // all but steps t + 2 and t + 3
         barrier();
-        const int next = ((t + 1) & 3) * kHalfBytes, fill = (t & 3) * kHalfBytes;
+        const int cur = buf & 1, next = ((buf + 1) & 3) * kHalfBytes, fill = buf * kHalfBytes;
         if (used) {
             fa.read(a[cur ^ 1], lds + next);
             fb.read(b[cur ^ 1], lds + next + kB);
         }
-        sa.fetch(0, t + 4, base + fill);
-        sb.fetch(0, t + 4, base + fill + kB);
-        if (used) {
+        auto multiply = [&](int s) {
+            if (!used) return;
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[j][i] = mma(b[cur][j][s], a[cur][i][s], acc[j][i]);
-        }
+                for (int j = 0; j < 2; ++j) acc[j][i] = mma(b[cur][j][s], a[cur][i][s], acc[j][i]);
+        };
+        multiply(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (whole.value) sa.fetch(0, pa, base + fill);
+        else sa.fetch_checked(0, t + 4, base + fill);
+        multiply(1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (whole.value) sb.fetch(0, pb, base + fill + kB);
+        else sb.fetch_checked(0, t + 4, base + fill + kB);
+        multiply(2);
+        multiply(3);
+        pa += sa.advance;
+        pb += sb.advance;
     };
-    for (int t = 0; t < steps; t += 2) {
-        step(t, 0);
-        if (t + 1 < steps) step(t + 1, 1);
+    const int whole = min(sa.whole(), sb.whole());
+    int t = 0;
+    for (; t + 7 < whole; t += 4) {
+        step(t, 0, std::true_type());
+        step(t + 1, 1, std::true_type());
+        step(t + 2, 2, std::true_type());
+        step(t + 3, 3, std::true_type());
+    }
+    for (; t < steps; t += 4) {
+        step(t, 0, std::false_type());
+        if (t + 1 < steps) step(t + 1, 1, std::false_type());
+        if (t + 2 < steps) step(t + 2, 2, std::false_type());
+        if (t + 3 < steps) step(t + 3, 3, std::false_type());
     }
     wait_lds();
     wait_dma<0>();

@@ -944,8 +944,8 @@ def nvfp4_i8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
         raise ValueError(f"b: on {bc.device}, expected {ac.device}")
     if out is None:
         code = _out_code(out_dtype)
-        out = _for_stream(_new_gemm_out((M, N), out_dtype, ac.device), stream)
-        ldc = _round_up(N, 4)
+        ldc = _round_up(N, 4)  # (the ABI's rule)
+        out = _for_stream(torch.empty_strided((M, N), (ldc, 1), dtype=out_dtype, device=ac.device), stream)
     else:
         _check_gemm_out(out, (M, N), ac.device)
         code = _out_code(out.dtype)

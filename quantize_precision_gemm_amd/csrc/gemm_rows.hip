@@ -14,6 +14,8 @@
 // is row 4 (l / 16) + j of the first operand, column l % 16 of the second.
 // The output's columns are passed as the first operand, so that a lane holds
 // 4 neighbouring columns of one output row.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "internal.hpp"
@@ -89,73 +91,70 @@ struct Slice {
     int64_t tile;          // this workgroup's tile of them
 };
 
+// Inclusive scans over the wave, by lane moves inside the vector unit (a row
+// of 16 by 1, 2, 4, 8 lanes, then the last lane of each row into the next).
+template <class Op>
+__device__ __forceinline__ int wave_scan(int v, int none, const Op& op)
+{
+    v = op(v, __builtin_amdgcn_update_dpp(none, v, 0x111, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(none, v, 0x112, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(none, v, 0x114, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(none, v, 0x118, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(none, v, 0x142, 0xA, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(none, v, 0x143, 0xC, 0xF, false));
+    return v;
+}
+
 // Rows [begin, end) of the experts e0 + lane, in order and range whatever the
 // ends hold; the rows behind the last expert count as expert E's.  prev: the
 // end before e0's rows, and then the last lane's.
 __device__ __forceinline__ void lane_rows(const int32_t* __restrict__ ends, int64_t E, int64_t T, int64_t e0, int& prev,
                                           int& begin, int& end)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t e = e0 + lane;
+    const int64_t e = e0 + (threadIdx.x & 63);
     end = e < E ? min(max(ends[e], 0), (int)T) : (int)T;
-    end = max(end, prev);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(end, o, 64);
-        if (lane >= o) end = max(end, u);
-    }
-    begin = __shfl_up(end, 1, 64);
-    if (lane == 0) begin = prev;
+    end = wave_scan(max(end, prev), 0, [](int x, int y) { return max(x, y); });
+    begin = __builtin_amdgcn_update_dpp(prev, end, 0x138, 0xF, 0xF, false);  // the lane before's end
     prev = __builtin_amdgcn_readlane(end, 63);
 }
 
-// Row tiles of `rows` rows over all experts, each expert's own.
-__device__ __forceinline__ int64_t count_tiles(const int32_t* __restrict__ ends, int64_t E, int64_t T, int rows)
+// One of the tiles of kRows rows of all experts, each row tile counting
+// `cols` times, expert by expert: the one that order(total, at) chooses.
+// False if it chooses none.  Each wave scans the ends, 64 at a time.
+template <int kRows, class Order>
+__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ ends, int64_t E, int64_t T, int cols,
+                                          const Order& order, Slice& s)
 {
-    int prev = 0, begin, end;
-    int64_t total = 0;
-    for (int64_t e0 = 0; e0 <= E; e0 += 64) {
-        lane_rows(ends, E, T, e0, prev, begin, end);
-        int tiles = (end - begin + rows - 1) / rows;
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) tiles += __shfl_xor(tiles, o, 64);
-        total += __builtin_amdgcn_readfirstlane(tiles);
-    }
-    return total;
-}
-
-// Tile `tile` of all, each row tile counting `cols` times, expert by expert;
-// false past them all.  Each wave scans the ends, 64 at a time.
-__device__ __forceinline__ bool find_slice(const int32_t* __restrict__ ends, int64_t E, int64_t T, int rows, int cols,
-                                           int64_t tile, Slice& s)
-{
-    const int lane = threadIdx.x & 63;
-    int prev = 0, begin, end;
-    int64_t before = 0;  // tiles of the experts before this chunk
-    for (int64_t e0 = 0; e0 <= E; e0 += 64) {
-        lane_rows(ends, E, T, e0, prev, begin, end);
-        int tiles = (end - begin + rows - 1) / rows * cols;
-        const int own = tiles;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int u = __shfl_up(tiles, o, 64);
-            if (lane >= o) tiles += u;
+    const auto add = [](int x, int y) { return x + y; };
+    const bool once = E < 64;
+    int64_t total = 0, at = 0;
+    for (int pass = once ? 1 : 0; pass < 2; ++pass) {  // the count, then the search
+        int prev = 0, begin, end;
+        int64_t before = 0;  // tiles of the experts before this chunk
+        for (int64_t e0 = 0; e0 <= E; e0 += 64) {
+            lane_rows(ends, E, T, e0, prev, begin, end);
+            const int own = (end - begin + kRows - 1) / kRows * cols;
+            const int upto = wave_scan(own, 0, add);
+            const int all = __builtin_amdgcn_readlane(upto, 63);
+            if (once && !order((int64_t)all, at)) return false;
+            const unsigned long long past = pass ? __ballot(before + upto > at) : 0;
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                s.e = e0 + l;
+                s.begin = __builtin_amdgcn_readlane(begin, l);
+                s.end = __builtin_amdgcn_readlane(end, l);
+                s.tile = at - (before + __builtin_amdgcn_readlane(upto - own, l));
+                return true;
+            }
+            before += all;
         }
-        const unsigned long long past = __ballot(before + tiles > tile);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            s.e = e0 + l;
-            s.begin = __builtin_amdgcn_readlane(begin, l);
-            s.end = __builtin_amdgcn_readlane(end, l);
-            s.tile = tile - (before + __builtin_amdgcn_readlane(tiles - own, l));
-            return true;
-        }
-        before += __builtin_amdgcn_readlane(tiles, 63);
+        total = before;
+        if (pass == 0 && !order(total, at)) return false;
     }
     return false;
 }
 
-// The rows of expert e (wgrad), as find_slice sees them.
+// The rows of expert e (wgrad), as find_tile sees them.
 __device__ __forceinline__ void expert_rows(const int32_t* __restrict__ ends, int64_t e, int64_t T, int64_t& begin,
                                             int64_t& end)
 {
@@ -166,24 +165,6 @@ __device__ __forceinline__ void expert_rows(const int32_t* __restrict__ ends, in
     b = min(b, (int)T);
     begin = b;
     end = max(b, min(max(ends[e], 0), (int)T));
-}
-
-// 16 bytes (one MFMA operand piece) of row r from byte kb of its K; bytes
-// from kend on read as zero (kb and kend multiples of 16).
-template <bool kT>
-__device__ __forceinline__ uint4 piece(const View& v, int64_t r, int64_t kb, int64_t kend)
-{
-    if constexpr (!kT) {
-        return kb < kend ? *reinterpret_cast<const uint4*>(v.p + r * v.ld + kb) : make_uint4(0, 0, 0, 0);
-    } else {  // bf16 only: 8 values, one from each k row
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t k = (kb >> 1) + j;
-            if (2 * k < kend) w[j >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(v.p + k * v.ld + 2 * r) << (16 * (j & 1));
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
 }
 
 // 4 neighbouring columns of an output row.
@@ -213,35 +194,53 @@ __device__ __forceinline__ void store_cols(void* c, int64_t at, int64_t n, int64
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: a workgroup of 4 waves computes 16 kM rows x 16 kN columns, each
-// wave a quarter of the contraction (128-byte steps dealt in turn), straight
-// from memory to registers; the parts are added in wave order in LDS.
+// Few rows: bound by the weights' bytes.  A workgroup of 4 waves computes
+// 16 kM rows x 16 kN columns (rows x K operands only), each wave a quarter of
+// the contraction, 128-byte steps dealt in turn, straight from memory to
+// registers with kU steps in flight; the parts are added in wave order in LDS.
 // ---------------------------------------------------------------------------
-template <class Acc, bool kTA, bool kTB, int kM, int kN, class Out>
+template <class Acc, int kM, int kN, int kU, class Out>
 __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t kend, int64_t m0, int64_t n0,
                                           f32x4_t* lds, const Out& out)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id();
     const int r = lane & 15, g = lane >> 4;
+    const uint8_t *pa[kM], *pb[kN];
+#pragma unroll
+    for (int i = 0; i < kM; ++i) pa[i] = A.p + min(m0 + 16 * i + r, A.rows - 1) * A.ld + 16 * g;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) pb[j] = B.p + min(n0 + 16 * j + r, B.rows - 1) * B.ld + 16 * g;
     Acc acc[kM][kN] = {};
-    for (int64_t k0 = 128 * wave; k0 < kend; k0 += 512) {
-        const int64_t kb = k0 + 32 * g;
-        uint4 a[kM][2], b[kN][2];
+    auto steps = [&](int64_t k0, auto count, auto whole) {
+        constexpr int kSteps = count.value;
+        uint4 a[kSteps][kM][2], b[kSteps][kN][2];
+        auto piece = [&](const uint8_t* p, int64_t k) {  // pieces past K: zeros
+            return whole.value || k + 16 * g < kend ? *reinterpret_cast<const uint4*>(p + k) : make_uint4(0, 0, 0, 0);
+        };
 #pragma unroll
-        for (int j = 0; j < kN; ++j)
+        for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) b[j][h] = piece<kTB>(B, min(n0 + 16 * j + r, B.rows - 1), kb + 16 * h, kend);
+            for (int h = 0; h < 2; ++h) {
+                const int64_t k = k0 + 512 * u + 64 * h;
 #pragma unroll
-        for (int i = 0; i < kM; ++i)
+                for (int j = 0; j < kN; ++j) b[u][j][h] = piece(pb[j], k);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) a[i][h] = piece<kTA>(A, min(m0 + 16 * i + r, A.rows - 1), kb + 16 * h, kend);
+                for (int i = 0; i < kM; ++i) a[u][i][h] = piece(pa[i], k);
+            }
+        __builtin_amdgcn_sched_barrier(0);  // every load before the first MFMA
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-            for (int i = 0; i < kM; ++i)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < kN; ++j) acc[i][j] = mma(b[j][h], a[i][h], acc[i][j]);
-    }
+                for (int i = 0; i < kM; ++i)
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) acc[i][j] = mma(b[u][j][h], a[u][i][h], acc[i][j]);
+    };
+    int64_t k0 = 128 * wave;
+    for (; k0 + 512 * (kU - 1) + 128 <= kend; k0 += 512 * kU)
+        steps(k0, std::integral_constant<int, kU>(), std::true_type());
+    for (; k0 < kend; k0 += 512) steps(k0, std::integral_constant<int, 1>(), std::false_type());
     Acc* part = reinterpret_cast<Acc*>(lds);
 #pragma unroll
     for (int i = 0; i < kM; ++i)
@@ -793,8 +792,10 @@ __device__ __forceinline__ bool xcd_order(int64_t hw, int64_t total, int64_t& at
 // both).  Whole rounds of one tile per compute unit come first, each round
 // dealt so that an XCD gets neighbouring tiles of it (dealt over all rounds
 // at once, the XCD of the largest experts would finish last: 468 against
-// 354 us for a wgrad of 16 uneven experts, 8192 x 2560 x 5120).  If what remains fills at most
-// half the compute units, its tiles are done as two halves of 128 rows each.
+// 354 us for a wgrad of 16 uneven experts, 8192 x 2560 x 5120).  If what remains is at most
+// 3/8 of the compute units, its tiles are done as two halves of 128 rows each
+// (a half's step takes 0.95 us with 160 of them, 1.3 with 256; a whole
+// tile's 1.1 to 1.4).
 template <bool kBig>
 __device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, int& half)
 {
@@ -805,7 +806,7 @@ __device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, 
         at += hw - hw % cus;
         return true;
     }
-    const bool split = kBig && 2 * rest <= cus;
+    const bool split = kBig && 8 * rest <= 3 * cus;
     if (!xcd_order(hw - full, split ? 2 * rest : rest, at)) return false;
     if (split) {
         half = (int)(at & 1);
@@ -815,7 +816,10 @@ __device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, 
     return true;
 }
 
-constexpr int kThinM = 2, kThinN = 2;
+// Columns / 16 of a thin tile, and the steps a wave has in flight.  One token
+// through 5120 -> 20480 in int8: 1 and 2 22.4 us, 1 and 4 23.0, 1 and 8 25.0,
+// 2 and 2 24.4 (more waves on a compute unit do more than more loads in one).
+constexpr int kThinN = 1, kThinU = 2;
 
 }  // namespace
 
@@ -827,9 +831,10 @@ __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_grouped(Grou
     const int64_t cols = kPass == 0 ? g.N : g.K;
     const int tn = (int)((cols + kTile - 1) / kTile);
     View A, B;
-    int64_t m0, n0, mend, Ka, Kb, c_at = 0, at;
+    int64_t m0, n0, mend, Ka, Kb, c_at = 0;
     int steps, im, in_, half;
     if constexpr (kPass == 2) {
+        int64_t at;
         const int tm = (int)((g.N + kTile - 1) / kTile);
         if (!tile_order<kBig>(g.E * tm * tn, g.cus, at, half)) return;
         const int64_t e = at / (tm * tn);
@@ -842,9 +847,9 @@ __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_grouped(Grou
         steps = (int)((end - begin + 63) / 64);
         c_at = e * g.c_expert;
     } else {
-        if (!tile_order<kBig>((int64_t)tn * count_tiles(g.ends, g.E, g.T, kTile), g.cus, at, half)) return;
         Slice s;
-        if (!find_slice(g.ends, g.E, g.T, kTile, tn, at, s)) return;
+        const auto order = [&](int64_t total, int64_t& tile) { return tile_order<kBig>(total, g.cus, tile, half); };
+        if (!find_tile<kTile>(g.ends, g.E, g.T, tn, order, s)) return;
         grouped_order((int)s.tile, (int)((s.end - s.begin + kTile - 1) / kTile), tn, im, in_);
         const bool none = s.e >= g.E;  // rows of no expert: zeros
         A = View{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
@@ -883,56 +888,39 @@ __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_i8(
                                                     Scaled(sa, sb, M, N));
 }
 
-template <int kPass, bool kF32>
+// fprop
+template <int kM, bool kF32>
 __global__ __launch_bounds__(256) void k_grouped_thin(GroupedArgs g)
 {
-    __shared__ f32x4_t lds[4 * kThinM * kThinN * 64];
-    const int64_t cols = kPass == 0 ? g.N : g.K;
-    const int64_t tn = (cols + 16 * kThinN - 1) / (16 * kThinN);
-    View A, B;
-    int64_t m0, n0, kend, row0;
-    int64_t c_at = 0;
-    if constexpr (kPass == 2) {
-        const int64_t tm = (g.N + 16 * kThinM - 1) / (16 * kThinM);
-        const int64_t e = blockIdx.x / (tm * tn), in = blockIdx.x % (tm * tn);
-        int64_t begin, end;
-        expert_rows(g.ends, e, g.T, begin, end);
-        A = View{reinterpret_cast<const uint8_t*>(g.a + begin * g.lda), 2 * g.lda, g.N};
-        B = View{reinterpret_cast<const uint8_t*>(g.b + begin * g.ldb), 2 * g.ldb, g.K};
-        m0 = in / tn * 16 * kThinM;
-        n0 = in % tn * 16 * kThinN;
-        kend = 2 * (end - begin);
-        row0 = 0;
-        c_at = e * g.c_expert;
-    } else {
-        Slice s;
-        if (!find_slice(g.ends, g.E, g.T, 16 * kThinM, 1, blockIdx.x / tn, s)) return;
-        A = View{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
-        const int64_t e = s.e < g.E ? s.e : 0;
-        B = View{reinterpret_cast<const uint8_t*>(g.b + e * g.b_expert), 2 * g.ldb, cols};
-        m0 = s.tile * 16 * kThinM;
-        n0 = blockIdx.x % tn * 16 * kThinN;
-        kend = s.e < g.E ? 2 * (kPass == 0 ? g.K : g.N) : 0;  // rows of no expert: zeros
-        row0 = s.begin;
-    }
-    thin_tile<f32x4_t, kPass == 2, kPass != 0, kThinM, kThinN>(
-        A, B, kend, m0, n0, lds, [&](int64_t m, int64_t n, f32x4_t v) {
+    __shared__ f32x4_t lds[4 * kM * kThinN * 64];
+    const int64_t tn = (g.N + 16 * kThinN - 1) / (16 * kThinN);
+    Slice s;
+    const auto order = [&](int64_t total, int64_t& at) { return xcd_order(blockIdx.x, total, at); };
+    if (!find_tile<16 * kM>(g.ends, g.E, g.T, (int)tn, order, s)) return;
+    const bool none = s.e >= g.E;  // rows of no expert: zeros
+    const View A{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
+    const View B{reinterpret_cast<const uint8_t*>(g.b + (none ? 0 : s.e) * g.b_expert), 2 * g.ldb, g.N};
+    const int64_t c_at = s.begin * g.ldc;
+    // the row tiles of the same columns lie side by side: they share the weights
+    const int tm = (int)((s.end - s.begin + 16 * kM - 1) / (16 * kM));
+    thin_tile<f32x4_t, kM, kThinN, kThinU>(
+        A, B, none ? 0 : 2 * g.K, s.tile % tm * 16 * kM, s.tile / tm * 16 * kThinN, lds,
+        [&](int64_t m, int64_t n, f32x4_t v) {
             const float y[4] = {v[0], v[1], v[2], v[3]};
-            store_cols<kF32>(g.c, c_at + (row0 + m) * g.ldc + n, n, B.rows, y);
+            store_cols<kF32>(g.c, c_at + m * g.ldc + n, n, g.N, y);
         });
 }
 
-template <bool kF32>
+template <int kM, bool kF32>
 __global__ __launch_bounds__(256) void k_i8_thin(const int8_t* __restrict__ a, int64_t lda, const float* __restrict__ sa,
                                                  const int8_t* __restrict__ b, int64_t ldb, const float* __restrict__ sb,
                                                  int64_t M, int64_t N, int64_t K, void* __restrict__ c, int64_t ldc)
 {
-    __shared__ f32x4_t lds[4 * kThinM * kThinN * 64];
-    const int64_t tn = (N + 16 * kThinN - 1) / (16 * kThinN);
+    __shared__ f32x4_t lds[4 * kM * kThinN * 64];
+    const int64_t tm = (M + 16 * kM - 1) / (16 * kM);
     const View A{reinterpret_cast<const uint8_t*>(a), lda, M}, B{reinterpret_cast<const uint8_t*>(b), ldb, N};
-    thin_tile<i32x4_t, false, false, kThinM, kThinN>(
-        A, B, K, blockIdx.x / tn * 16 * kThinM, blockIdx.x % tn * 16 * kThinN, lds,
-        [&](int64_t m, int64_t n, i32x4_t v) {
+    thin_tile<i32x4_t, kM, kThinN, kThinU>(
+        A, B, K, blockIdx.x % tm * 16 * kM, blockIdx.x / tm * 16 * kThinN, lds, [&](int64_t m, int64_t n, i32x4_t v) {
             const float s = sa[m];
             float y[4];
 #pragma unroll
@@ -945,13 +933,23 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Whether tiles of 256 x 256 finish sooner than those of 128 x 128, from the
-// rounds of tiles that the compute units take: a step of a big tile takes
-// about 1.1 us and one of a small tile 0.45 us.
-bool big_tiles(int64_t big, int64_t mid, int cus)
+enum class Tiles { kThin, kMid, kBig };
+
+// The kernel that takes the least time, by what each was measured to take (us
+// on 256 compute units, int8 and bf16 alike):
+//   thin  6 and its traffic from the caches at 8.5 TB/s (`traffic` bytes; none: 0)
+//   mid   1.5, and 5 and 0.5 per step for each round of its tiles
+//   big   1.5, and 9 and 1.15 per step for each round (0.95 in a last round of halves)
+// For example int8, N = K = 5120: 16 rows 11.7 / 20.2 / 31.9, 64 rows 24.8 /
+// 21.2 / 32.4, 2048 rows - / 79 / 55; N = 1024, K = 2048, 256 rows 10.7 / 13.1 / 19.3.
+Tiles choose(double traffic, double mid, double big, double steps, int cus)
 {
-    const double b = big % cus * 2 <= cus ? big / cus + (big % cus ? 0.9 : 0.0) : (double)ceil_div(big, cus);
-    return 1.1 * b <= 0.45 * ceil_div(mid, cus);
+    const double thin = traffic > 0 ? 6.0 + traffic / 8.5e6 : 1e30;
+    const double m = 1.5 + std::ceil(mid / cus) * (5.0 + 0.5 * steps);
+    const double whole = std::floor(big / cus), rest = big - whole * cus;
+    const double b = 1.5 + whole * (9.0 + 1.15 * steps) +
+                     (rest > 0 ? 9.0 + (8 * rest <= 3 * cus ? 0.95 : 1.15) * steps : 0.0);
+    return thin <= m && thin <= b ? Tiles::kThin : m <= b ? Tiles::kMid : Tiles::kBig;
 }
 
 template <bool kBig, bool kF32>
@@ -977,27 +975,49 @@ void launch_grouped_tiles(const GroupedArgs& g, bool out_fp32, hipStream_t s)
         hipLaunchKernelGGL((k_grouped<kBig, kPass, false>), grid, dim3(kBig ? 512 : 256), 0, s, g);
 }
 
-template <int kPass>
+// Row tiles of a thin product of about `rows` rows: 16, 32 or 64.
+int thin_rows(double rows) { return rows <= 16.0 ? 1 : rows <= 32.0 ? 2 : 4; }
+
+template <int kM>
 void launch_grouped_thin(const GroupedArgs& g, bool out_fp32, hipStream_t s)
 {
-    const int64_t cols = ceil_div(kPass == 0 ? g.N : g.K, 16 * kThinN);
-    const int64_t rows = g.T / (16 * kThinM) + g.E + 1;
+    const dim3 grid((uint32_t)((g.T / (16 * kM) + g.E + 1) * ceil_div(g.N, 16 * kThinN)));
     if (out_fp32)
-        hipLaunchKernelGGL((k_grouped_thin<kPass, true>), dim3((uint32_t)(rows * cols)), dim3(256), 0, s, g);
+        hipLaunchKernelGGL((k_grouped_thin<kM, true>), grid, dim3(256), 0, s, g);
     else
-        hipLaunchKernelGGL((k_grouped_thin<kPass, false>), dim3((uint32_t)(rows * cols)), dim3(256), 0, s, g);
+        hipLaunchKernelGGL((k_grouped_thin<kM, false>), grid, dim3(256), 0, s, g);
+}
+
+template <int kM>
+void launch_i8_thin(const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb, const float* sb,
+                    int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, hipStream_t s)
+{
+    const dim3 grid((uint32_t)(ceil_div(M, 16 * kM) * ceil_div(N, 16 * kThinN)));
+    if (out_fp32)
+        hipLaunchKernelGGL((k_i8_thin<kM, true>), grid, dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
+    else
+        hipLaunchKernelGGL((k_i8_thin<kM, false>), grid, dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
 }
 
 template <int kPass>
 void launch_grouped_pass(const GroupedArgs& g, bool out_fp32, hipStream_t s)
 {
     const int64_t cols = kPass == 0 ? g.N : g.K;
-    if (kPass == 0 && g.T <= 32 * g.E) return launch_grouped_thin<0>(g, out_fp32, s);
-    // row tiles: half of every expert's last one is taken as empty
-    const int64_t rows = kPass == 2 ? g.N : g.T;
-    const int64_t big = kPass == 2 ? g.E * ceil_div(rows, 256) : g.T / 256 + (g.E + 1) / 2;
-    const int64_t mid = kPass == 2 ? g.E * ceil_div(rows, 128) : g.T / 128 + (g.E + 1) / 2;
-    if (big_tiles(big * ceil_div(cols, 256), mid * ceil_div(cols, 128), g.cus))
+    const double T = (double)g.T, experts = (double)std::max<int64_t>(1, std::min(g.E, g.T)), each = T / experts;
+    const int m = thin_rows(each);
+    // row tiles of t rows: half of an expert's last one is taken as empty
+    const auto row_tiles = [&](double t) {
+        return kPass == 2 ? (double)(g.E * ceil_div(g.N, (int64_t)t)) : std::max(experts, T / t + experts / 2);
+    };
+    const auto tiles = [&](int64_t t) { return row_tiles((double)t) * ceil_div(cols, t); };
+    const double K = kPass == 0 ? (double)g.K : kPass == 1 ? (double)g.N : each;
+    const double traffic =
+        kPass == 0 ? row_tiles(16.0 * m) * ceil_div(cols, 16) * (std::min(each, 16.0 * m) + 16) * 2 * K : 0.0;
+    const Tiles t = choose(traffic, tiles(128), tiles(256), std::ceil(K / 64), g.cus);
+    if (kPass == 0 && t == Tiles::kThin)
+        return m == 1 ? launch_grouped_thin<1>(g, out_fp32, s)
+               : m == 2 ? launch_grouped_thin<2>(g, out_fp32, s) : launch_grouped_thin<4>(g, out_fp32, s);
+    if (t == Tiles::kBig)
         launch_grouped_tiles<true, kPass>(g, out_fp32, s);
     else
         launch_grouped_tiles<false, kPass>(g, out_fp32, s);
@@ -1009,15 +1029,15 @@ void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t*
                     int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, int cus, hipStream_t s)
 {
     if (M == 0 || N == 0) return;
-    if (M <= 64) {
-        const dim3 grid((uint32_t)(ceil_div(M, 16 * kThinM) * ceil_div(N, 16 * kThinN)));
-        if (out_fp32)
-            hipLaunchKernelGGL(k_i8_thin<true>, grid, dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
-        else
-            hipLaunchKernelGGL(k_i8_thin<false>, grid, dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
-        return;
+    const int m = thin_rows((double)M);
+    const double traffic = (double)ceil_div(M, 16 * m) * ceil_div(N, 16) * (std::min(M, (int64_t)16 * m) + 16) * K;
+    const auto tiles = [&](int64_t t) { return (double)ceil_div(M, t) * ceil_div(N, t); };
+    const Tiles t = choose(traffic, tiles(128), tiles(256), (double)ceil_div(K, 128), cus);
+    if (t == Tiles::kThin || K == 0) {
+        const auto thin = m == 1 ? launch_i8_thin<1> : m == 2 ? launch_i8_thin<2> : launch_i8_thin<4>;
+        return thin(a, lda, sa, b, ldb, sb, M, N, K, c, ldc, out_fp32, s);
     }
-    const bool big = big_tiles(ceil_div(M, 256) * ceil_div(N, 256), ceil_div(M, 128) * ceil_div(N, 128), cus);
+    const bool big = t == Tiles::kBig;
     const auto launch = big ? (out_fp32 ? launch_i8_tiles<true, true> : launch_i8_tiles<true, false>)
                             : (out_fp32 ? launch_i8_tiles<false, true> : launch_i8_tiles<false, false>);
     launch(a, lda, sa, b, ldb, sb, M, N, K, c, ldc, cus, s);

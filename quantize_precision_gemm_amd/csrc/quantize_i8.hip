@@ -10,6 +10,11 @@
 // 1 / (2 A 2^d), that is 1 / (254 X) > 2^-16 of its value, and fp32 rounds by
 // 2^-24 of it.
 //
+// A true division of every element would bind the kernel to its arithmetic
+// (37 us for 8192 x 5120): y = x (127 / amax), two roundings, lies within
+// 2^-23 of the quotient, and rounding y to 18 bits makes a tie a tie again
+// (it has 8 bits) without carrying any other quotient across one.
+//
 // Bound by HBM traffic: 2 bytes read and 1 written per element.
 #include "internal.hpp"
 #include "nvfp4_device.hpp"
@@ -18,64 +23,94 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kHeld = 4;  // 16-byte pieces that a lane keeps between the maximum and the codes
 
-// Factor that keeps 127 x below fp32's maximum (a power of two on both sides
-// of the quotient leaves it as it is).
-__device__ __forceinline__ float headroom(float amax) { return amax >= 0x1p120f ? 0x1p-8f : 1.0f; }
-
-__device__ __forceinline__ uint32_t code_of(float x, float amax_s)
+__device__ __forceinline__ uint32_t max_of(uint32_t top, const uint4& v)
 {
-    const float y = (x * 127.0f) / amax_s;
-    return (uint32_t)(int)__builtin_rintf(__builtin_fminf(__builtin_fmaxf(y, -127.0f), 127.0f)) & 0xFFu;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    return top;
+}
+
+__device__ __forceinline__ uint32_t code_of(float x, float scale)
+{
+    const float y = x * scale;
+    const float t = y * 65.0f;              // y to 18 bits: 24 - 6
+    const float y18 = t - (t - y);
+    return (uint32_t)(int)__builtin_rintf(y18) & 0xFFu;
+}
+
+__device__ __forceinline__ uint2 codes_of(const uint4& v, float lift, float scale)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = code_of(__uint_as_float(w[j] << 16) * lift, scale);
+        const uint32_t hi = code_of(__uint_as_float(w[j] & 0xFFFF0000u) * lift, scale);
+        o[j >> 1] |= (lo | (hi << 8)) << (16 * (j & 1));
+    }
+    return make_uint2(o[0], o[1]);
 }
 
 }  // namespace
 
-// One workgroup per row: the maximum, then the codes (the row's second read
-// comes from the cache).
-__global__ __launch_bounds__(kThreads) void k_i8_quant(const uint16_t* __restrict__ x, int64_t cols, int64_t ld,
-                                                       int8_t* __restrict__ codes, int64_t ld_codes,
-                                                       float* __restrict__ scales)
+// kWaves waves per row (4: a workgroup of one row; 1: a workgroup of 4 rows).
+template <int kWaves>
+__global__ __launch_bounds__(256) void k_i8_quant(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld,
+                                                  int8_t* __restrict__ codes, int64_t ld_codes,
+                                                  float* __restrict__ scales)
 {
-    __shared__ uint32_t part[kThreads / 64];
-    const int64_t row = blockIdx.x;
+    constexpr int kLanes = 64 * kWaves;
+    __shared__ uint32_t part[4];
+    const int64_t row = kWaves == 4 ? blockIdx.x : blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= rows) return;  // (a whole wave, and with kWaves = 4 none)
+    const int lane = kWaves == 4 ? threadIdx.x : threadIdx.x & 63;
     const uint16_t* src = x + row * ld;
+    uint4 held[kHeld];
     uint32_t top = 0;
-    for (int64_t k = 8 * (int64_t)threadIdx.x; k < cols; k += 8 * kThreads) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src + k);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    for (int i = 0; i < kHeld; ++i) {
+        const int64_t k = 8 * (lane + (int64_t)kLanes * i);
+        held[i] = k < cols ? *reinterpret_cast<const uint4*>(src + k) : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) top = max_of(top, held[i]);
+    for (int64_t k = 8 * (lane + (int64_t)kLanes * kHeld); k < cols; k += 8 * kLanes)
+        top = max_of(top, *reinterpret_cast<const uint4*>(src + k));
     top = wave_max_u32(top);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = max(max(part[0], part[1]), max(part[2], part[3]));
-    const float amax = __uint_as_float(top << 16);
-    if (threadIdx.x == 0) scales[row] = amax / 127.0f;
-    const float f = headroom(amax);
-    const float amax_s = amax > 0.0f ? amax * f : 1.0f;
-    int8_t* dst = codes + row * ld_codes;
-    for (int64_t k = 8 * (int64_t)threadIdx.x; k < cols; k += 8 * kThreads) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src + k);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[2] = {0u, 0u};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = code_of(__uint_as_float(w[j] << 16) * f, amax_s);
-            const uint32_t hi = code_of(__uint_as_float(w[j] & 0xFFFF0000u) * f, amax_s);
-            o[j >> 1] |= (lo | (hi << 8)) << (16 * (j & 1));
-        }
-        *reinterpret_cast<uint2*>(dst + k) = make_uint2(o[0], o[1]);
+    if constexpr (kWaves == 4) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+        __syncthreads();
+        top = max(max(part[0], part[1]), max(part[2], part[3]));
     }
+    const float amax = __uint_as_float(top << 16);
+    if (lane == 0) scales[row] = amax / 127.0f;
+    // a power of two on both sides of the quotient keeps 127 / amax finite
+    const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+    const float scale = amax > 0.0f ? 127.0f / (amax * lift) : 0.0f;
+    int8_t* dst = codes + row * ld_codes;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int64_t k = 8 * (lane + (int64_t)kLanes * i);
+        if (k < cols) *reinterpret_cast<uint2*>(dst + k) = codes_of(held[i], lift, scale);
+    }
+    for (int64_t k = 8 * (lane + (int64_t)kLanes * kHeld); k < cols; k += 8 * kLanes)
+        *reinterpret_cast<uint2*>(dst + k) = codes_of(*reinterpret_cast<const uint4*>(src + k), lift, scale);
 }
 
 void launch_i8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int8_t* codes, int64_t ld_codes,
                      float* scales, hipStream_t s)
 {
     if (rows == 0) return;
-    hipLaunchKernelGGL(k_i8_quant, dim3((uint32_t)rows), dim3(kThreads), 0, s, x, cols, ld, codes, ld_codes, scales);
+    // a wave holds 2048 columns; with fewer rows than that fills the device, a workgroup takes one
+    if (cols <= 512 * kHeld && rows > 1024)
+        hipLaunchKernelGGL(k_i8_quant<1>, dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, x, rows, cols, ld, codes,
+                           ld_codes, scales);
+    else
+        hipLaunchKernelGGL(k_i8_quant<4>, dim3((uint32_t)rows), dim3(256), 0, s, x, rows, cols, ld, codes, ld_codes,
+                           scales);
 }
 
 }  // namespace nvfp4

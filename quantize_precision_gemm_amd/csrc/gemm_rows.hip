@@ -650,7 +650,6 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
 {
     const int lane = threadIdx.x & 63, g = lane >> 5;
     const bool wide = (reinterpret_cast<uintptr_t>(c) & 15) == 0 && (kF32 || ((ldc | c_at) & 7) == 0);
-    constexpr int kCols = kF32 ? 4 : 8;   // columns of a piece
     constexpr int kUnits = kF32 ? 2 : 1;  // stagings for the 64 columns
     if (row0 >= mend) return;
 #pragma unroll
@@ -690,17 +689,24 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
                     store16<kStream>(d, v);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j)
+                    for (int j = 0; j < 4; ++j)
                         if (n + j < N) d[j] = __uint_as_float(w[j]);
                 }
             } else {
                 uint16_t* d = static_cast<uint16_t*>(c) + at;
                 if (wide && n + 8 <= N) {
                     store16<kStream>(d, v);
-                } else {
+                } else {  // rows are 8-byte aligned at least
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j)
-                        if (n + j < N) d[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+                    for (int h = 0; h < 2; ++h) {
+                        if (n + 4 * h + 4 <= N) {
+                            *reinterpret_cast<uint2*>(d + 4 * h) = make_uint2(w[2 * h], w[2 * h + 1]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (n + 4 * h + j < N) d[4 * h + j] = (uint16_t)(w[2 * h + (j >> 1)] >> (16 * (j & 1)));
+                        }
+                    }
                 }
             }
         }
@@ -938,14 +944,14 @@ enum class Tiles { kThin, kMid, kBig };
 // The kernel that takes the least time, by what each was measured to take (us
 // on 256 compute units, int8 and bf16 alike):
 //   thin  6 and its traffic from the caches at 8.5 TB/s (`traffic` bytes; none: 0)
-//   mid   1.5, and 5 and 0.5 per step for each round of its tiles
+//   mid   1.5, and 4 and 0.47 per step for each round of its tiles
 //   big   1.5, and 9 and 1.15 per step for each round (0.95 in a last round of halves)
 // For example int8, N = K = 5120: 16 rows 11.7 / 20.2 / 31.9, 64 rows 24.8 /
 // 21.2 / 32.4, 2048 rows - / 79 / 55; N = 1024, K = 2048, 256 rows 10.7 / 13.1 / 19.3.
 Tiles choose(double traffic, double mid, double big, double steps, int cus)
 {
     const double thin = traffic > 0 ? 6.0 + traffic / 8.5e6 : 1e30;
-    const double m = 1.5 + std::ceil(mid / cus) * (5.0 + 0.5 * steps);
+    const double m = 1.5 + std::ceil(mid / cus) * (4.0 + 0.47 * steps);
     const double whole = std::floor(big / cus), rest = big - whole * cus;
     const double b = 1.5 + whole * (9.0 + 1.15 * steps) +
                      (rest > 0 ? 9.0 + (8 * rest <= 3 * cus ? 0.95 : 1.15) * steps : 0.0);

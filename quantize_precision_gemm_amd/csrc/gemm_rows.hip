@@ -268,8 +268,8 @@ __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t 
 //     c ^ (r / 2) % 8: the 16 rows of a fragment read, 128 bytes apart, then
 //     cover all banks;
 //   K x rows  (T): 64 k rows of 256 bytes, 32-byte block b of k row r at
-//     b ^ (r % 4 + 4 (r / 8 % 2)): the 4 k rows that a 16-lane group of a
-//     transposing read touches, 256 bytes apart, then lie in 4 bank groups.
+//     b ^ 2 (r % 4): a transposing read takes two neighbouring blocks of 4 k
+//     rows, 256 bytes apart, per 32 lanes, which then lie in 8 bank groups.
 // Pieces past the operand's K are read from a page of zeros, rows past its
 // end from its last row (their products are not stored).
 //
@@ -357,7 +357,7 @@ struct Source {
                 off[i] = (uint32_t)min(row, last) * (uint32_t)ld + 16 * ((tid & 7) ^ ((tid >> 4) & 7));
             } else {
                 const int kr = kThreads / 16 * (i % kLoads) + (tid >> 4);
-                const int block = ((tid & 15) >> 1) ^ ((kr & 3) | (((kr >> 3) & 1) << 2));
+                const int block = ((tid & 15) >> 1) ^ (kr & 3) << 1;
                 off[i] = (uint32_t)kr * (uint32_t)ld +
                          2 * min(128 * (i / kLoads) + 16 * block + 8 * (tid & 1), last);
             }
@@ -407,7 +407,7 @@ struct Fragments {
         } else {
             const int r = lane & 15, g = lane >> 4;
             at = (8 * (g >> 1) + (r >> 2)) * 256 + 8 * (r & 3);
-            block = ((2 * first + (g & 1)) ^ ((r >> 2) | ((g >> 1) << 2))) << 5;
+            block = ((2 * first + (g & 1)) ^ (r >> 2) << 1) << 5;
         }
     }
 
@@ -641,9 +641,10 @@ __device__ __forceinline__ void store16(void* d, uint4 v)
 // 64 x 64 outputs of a wave: rows row0 .., columns col[0] .. + 31 and
 // col[1] .. + 31; value(i, k, e): accumulator e of row tile i and column tile
 // k as a float.  The wave stages 64 rows of 128 bytes in its own 8 KB of LDS
-// (16-byte piece c of row r at c ^ r % 8, which spreads both the writes, a
-// row per lane, and the reads, a row per 8 lanes, over the banks) and stores
-// 8 row pieces of 128 bytes at a time.
+// (16-byte piece c of row r at c ^ r / 2 % 8, and the 8-byte halves of the
+// bf16 pieces of rows 16 .. 31 of 32 exchanged: the writes, a row per lane,
+// and the reads, a row per 8 lanes, meet no bank twice) and stores 8 row
+// pieces of 128 bytes at a time.
 template <bool kF32, bool kStream, class Value>
 __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const int64_t (&col)[2], int64_t mend, int64_t N,
                                            void* c, int64_t c_at, int64_t ldc, const Value& value)
@@ -666,10 +667,10 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
                     for (int j = 0; j < 4; ++j) y[j] = value(i, k, 4 * q + j);
                     uint8_t* row = stage + 128 * r;
                     if constexpr (kF32)
-                        *reinterpret_cast<float4*>(row + (((2 * q + g) ^ (r & 7)) << 4)) =
+                        *reinterpret_cast<float4*>(row + (((2 * q + g) ^ (r >> 1 & 7)) << 4)) =
                             make_float4(y[0], y[1], y[2], y[3]);
                     else
-                        *reinterpret_cast<uint2*>(row + (((4 * k + q) ^ (r & 7)) << 4) + 8 * g) =
+                        *reinterpret_cast<uint2*>(row + (((4 * k + q) ^ (r >> 1 & 7)) << 4) + 8 * (g ^ (r >> 4 & 1))) =
                             make_uint2(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]));
                 }
         }
@@ -677,7 +678,8 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
             const int r = 8 * it + (lane >> 3), p = lane & 7;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + 128 * r + ((p ^ (r & 7)) << 4));
+            uint4 v = *reinterpret_cast<const uint4*>(stage + 128 * r + ((p ^ (r >> 1 & 7)) << 4));
+            if (!kF32 && (it & 2)) v = make_uint4(v.z, v.w, v.x, v.y);
             const int64_t m = row0 + r;
             const int64_t n = kF32 ? col[u] + 4 * p : (p < 4 ? col[0] : col[1]) + 8 * (p & 3);
             if (m >= mend || n >= N) continue;

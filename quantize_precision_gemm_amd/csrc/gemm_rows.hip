@@ -641,9 +641,9 @@ __device__ __forceinline__ void store16(void* d, uint4 v)
 // 64 x 64 outputs of a wave: rows row0 .., columns col[0] .. + 31 and
 // col[1] .. + 31; value(i, k, e): accumulator e of row tile i and column tile
 // k as a float.  The wave stages 64 rows of 128 bytes in its own 8 KB of LDS
-// (16-byte piece c of row r at c ^ r / 2 % 8, and the 8-byte halves of the
-// bf16 pieces of rows 16 .. 31 of 32 exchanged: the writes, a row per lane,
-// and the reads, a row per 8 lanes, meet no bank twice) and stores 8 row
+// (16-byte piece c of row r at c ^ r % 8, and the 8-byte halves of the bf16
+// pieces of every other 8 rows exchanged: the writes, a row per lane, then
+// meet no bank twice within the 128 bytes that the LDS takes at a time) and stores 8 row
 // pieces of 128 bytes at a time.
 template <bool kF32, bool kStream, class Value>
 __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const int64_t (&col)[2], int64_t mend, int64_t N,
@@ -667,10 +667,10 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
                     for (int j = 0; j < 4; ++j) y[j] = value(i, k, 4 * q + j);
                     uint8_t* row = stage + 128 * r;
                     if constexpr (kF32)
-                        *reinterpret_cast<float4*>(row + (((2 * q + g) ^ (r >> 1 & 7)) << 4)) =
+                        *reinterpret_cast<float4*>(row + (((2 * q + g) ^ (r & 7)) << 4)) =
                             make_float4(y[0], y[1], y[2], y[3]);
                     else
-                        *reinterpret_cast<uint2*>(row + (((4 * k + q) ^ (r >> 1 & 7)) << 4) + 8 * (g ^ (r >> 4 & 1))) =
+                        *reinterpret_cast<uint2*>(row + (((4 * k + q) ^ (r & 7)) << 4) + 8 * (g ^ (r >> 3 & 1))) =
                             make_uint2(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]));
                 }
         }
@@ -678,8 +678,8 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
             const int r = 8 * it + (lane >> 3), p = lane & 7;
-            uint4 v = *reinterpret_cast<const uint4*>(stage + 128 * r + ((p ^ (r >> 1 & 7)) << 4));
-            if (!kF32 && (it & 2)) v = make_uint4(v.z, v.w, v.x, v.y);
+            uint4 v = *reinterpret_cast<const uint4*>(stage + 128 * r + ((p ^ (r & 7)) << 4));
+            if (!kF32 && (it & 1)) v = make_uint4(v.z, v.w, v.x, v.y);
             const int64_t m = row0 + r;
             const int64_t n = kF32 ? col[u] + 4 * p : (p < 4 ? col[0] : col[1]) + 8 * (p & 3);
             if (m >= mend || n >= N) continue;

@@ -540,7 +540,8 @@ int nvfp4_mfma_sustain(int64_t blocks, int64_t iters, int32_t operands, float* o
  *   a, lda    as for nvfp4_bf16_gemm.
  *   b         W: expert e at b + e * stride_b elements (a multiple of 8), its
  *             rows ldb apart; WGRAD: X, stride_b ignored.
- *   E, T, N, K  >= 0 and below 2^31; N and K multiples of 8; T any.
+ *   E, T, N, K  >= 0 and below 2^31; N and K multiples of 8; T any; fewer
+ *             than 2^22 output tiles of 256 x 256, lda and ldb below 2^22.
  *   c, ldc, c_dtype  as for nvfp4_gemm; WGRAD: expert e at c + e * stride_c
  *             elements (a multiple of 4), its rows ldc apart; otherwise
  *             stride_c is ignored.
@@ -560,7 +561,7 @@ typedef struct nvfp4_adamw_tensor {
     float* m_scale;   /* 8-bit states: one scale per 128 elements (ceil(n / 128) values) */
     float* v_scale;
     uint16_t* copy;   /* bf16 copy of the updated fp32 parameters, or NULL */
-    int64_t n;
+    int64_t n;        /* 0 to 2^33 */
 } nvfp4_adamw_tensor;
 
 /*
@@ -627,7 +628,8 @@ int nvfp4_i8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x, i
  *   a, b      device int8, M x lda and N x ldb; 16-byte aligned, lda and ldb
  *             multiples of 16 and at least K.
  *   K         a multiple of 16 below 2^17 (so that no sum leaves int32).
- *   M, N      any, below 2^31.
+ *   M, N      any, below 2^31; fewer than 2^22 output tiles of 256 x 256, lda
+ *             and ldb below 2^23.
  *   c, ldc, c_dtype  as for nvfp4_gemm.
  * Returns NVFP4_OK or a negative status; nothing is enqueued on failure.
  */

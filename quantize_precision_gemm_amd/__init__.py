@@ -781,7 +781,8 @@ class AdamWGroup:
     copies   bfloat16 copies of float32 params written by the step, or None; an
              entry may be None
 
-    The group holds references to its tensors; all of one kind have one dtype.
+    The group holds its tensors and their addresses; all of one kind have one
+    dtype.  A tensor that gets other memory (t.data = ...) needs a new group.
     """
 
     BLOCK = 128  # elements that share the scale of an 8-bit state
@@ -826,6 +827,9 @@ class AdamWGroup:
                 n = table[i].n
                 self._check_tensor(what, i, t, dtype, -(-n // self.BLOCK) if what.endswith("scales") else n)
                 setattr(table[i], field, t.data_ptr())
+        seen = [table[i].p for i in range(k) if table[i].n]
+        if len(set(seen)) != len(seen):
+            raise ValueError("params: the same tensor twice in one group")
         self.count = k
 
     def _check_tensor(self, what, i, t, dtype, count):

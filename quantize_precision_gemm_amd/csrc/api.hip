@@ -641,7 +641,14 @@ int nvfp4_mfma_sustain(int64_t blocks, int64_t iters, int32_t operands, float* o
 
 namespace {
 
-// nvfp4_adamw: one launch takes up to kAdamWTensors tensors.
+// Tiles of 256 x 256 outputs that one grid holds: 512 threads each, and a
+// grid has fewer than 2^32 threads.
+constexpr int64_t kMostBigTiles = int64_t(1) << 22;
+
+// nvfp4_adamw: one launch takes up to kAdamWTensors tensors and 2^23
+// workgroups (a tensor has at most 2^33 elements, that many workgroups).
+constexpr int64_t kMostChunks = int64_t(1) << 23;
+
 bool adamw_vec(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight)
 {
     return aligned(t.p, p_bf16 ? 8 : 16) && aligned(t.g, g_bf16 ? 8 : 16) && aligned(t.m, eight ? 4 : 16) &&
@@ -658,7 +665,7 @@ int check_adamw(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eigh
         return NVFP4_ERR_ALIGN;
     if (!eight && (!aligned(t.m, 4) || !aligned(t.v, 4))) return NVFP4_ERR_ALIGN;
     if (eight && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))) return NVFP4_ERR_ALIGN;
-    if (nvfp4::adamw_chunks(t.n) >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+    if (nvfp4::adamw_chunks(t.n) > kMostChunks) return NVFP4_ERR_SHAPE;
     return NVFP4_OK;
 }
 
@@ -700,7 +707,7 @@ int nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t p_dtyp
         const nvfp4_adamw_tensor& t = tensors[i];
         if (t.n == 0) continue;
         const int64_t c = nvfp4::adamw_chunks(t.n);
-        if (a.count == nvfp4::kAdamWTensors || chunks + c >= (int64_t(1) << 31)) {
+        if (a.count == nvfp4::kAdamWTensors || chunks + c > kMostChunks) {
             nvfp4::launch_adamw(a, p_bf16, g_bf16, eight, s);
             a.count = 0;
             chunks = 0;
@@ -740,7 +747,7 @@ int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int
     if (!aligned(a_scales, 4) || !aligned(b_scales, 4)) return NVFP4_ERR_ALIGN;
     if (!aligned(c, c_dtype == NVFP4_OUT_FP32 ? 16 : 8) || ldc % 4 != 0) return NVFP4_ERR_ALIGN;
     if (lda < K || ldb < K || ldc < N) return NVFP4_ERR_SHAPE;
-    if ((M + 15) / 16 * ((N + 15) / 16) >= (int64_t(1) << 31)) return NVFP4_ERR_SHAPE;
+    if ((M + 255) / 256 * ((N + 255) / 256) >= kMostBigTiles) return NVFP4_ERR_SHAPE;
     if (lda >= (int64_t(1) << 23) || ldb >= (int64_t(1) << 23)) return NVFP4_ERR_SHAPE;  // 32-bit offsets in a tile
     nvfp4::launch_i8_gemm(a, lda, a_scales, b, ldb, b_scales, M, N, K, c, ldc, c_dtype == NVFP4_OUT_FP32,
                           std::max(device_cus(), 1), static_cast<hipStream_t>(stream));
@@ -776,9 +783,8 @@ int nvfp4_bf16_grouped_gemm(int32_t pass, const void* a, int64_t lda, const void
     // a tile's 256 rows (or 64 k rows) are addressed with 32-bit offsets
     const int64_t span = int64_t(1) << 22;
     if (lda >= span || ldb >= span) return NVFP4_ERR_SHAPE;
-    // the smallest tile a launch may take is 16 x 16
-    const int64_t tiles = (wgrad ? E * ((N + 15) / 16) : T / 16 + E + 1) * ((c_cols + 15) / 16);
-    if (tiles >= lim) return NVFP4_ERR_SHAPE;
+    const int64_t tiles = (wgrad ? E * ((N + 255) / 256) : T / 256 + E + 1) * ((c_cols + 255) / 256);
+    if (tiles >= kMostBigTiles) return NVFP4_ERR_SHAPE;
     const nvfp4::GroupedArgs g{static_cast<const uint16_t*>(a), lda, static_cast<const uint16_t*>(b), ldb, stride_b,
                                ends, E, T, N, K, c, ldc, stride_c, std::max(device_cus(), 1)};
     nvfp4::launch_grouped(pass, g, c_dtype == NVFP4_OUT_FP32, static_cast<hipStream_t>(stream));

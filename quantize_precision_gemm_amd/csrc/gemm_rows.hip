@@ -950,10 +950,12 @@ enum class Tiles { kThin, kMid, kBig };
 //   big   1.5, and 9 and 1.15 per step for each round (0.95 in a last round of halves)
 // For example int8, N = K = 5120: 16 rows 11.7 / 20.2 / 31.9, 64 rows 24.8 /
 // 21.2 / 32.4, 2048 rows - / 79 / 55; N = 1024, K = 2048, 256 rows 10.7 / 13.1 / 19.3.
-Tiles choose(double traffic, double mid, double big, double steps, int cus)
+// thin_grid, mid_grid: their workgroups; a grid holds fewer than 2^32 threads.
+Tiles choose(double traffic, int64_t thin_grid, double mid, int64_t mid_grid, double big, double steps, int cus)
 {
-    const double thin = traffic > 0 ? 6.0 + traffic / 8.5e6 : 1e30;
-    const double m = 1.5 + std::ceil(mid / cus) * (4.0 + 0.47 * steps);
+    constexpr int64_t most = int64_t(1) << 24;  // workgroups of 256 threads
+    const double thin = traffic > 0 && thin_grid < most ? 6.0 + traffic / 8.5e6 : 1e30;
+    const double m = mid_grid < most ? 1.5 + std::ceil(mid / cus) * (4.0 + 0.47 * steps) : 1e30;
     const double whole = std::floor(big / cus), rest = big - whole * cus;
     const double b = 1.5 + whole * (9.0 + 1.15 * steps) +
                      (rest > 0 ? 9.0 + (8 * rest <= 3 * cus ? 0.95 : 1.15) * steps : 0.0);
@@ -970,13 +972,20 @@ void launch_i8_tiles(const int8_t* a, int64_t lda, const float* sa, const int8_t
                        cus);
 }
 
+// Workgroups of a grouped launch: every expert, and the rows of none, can
+// have one partial row tile.
+template <int kPass>
+int64_t grouped_grid(const GroupedArgs& g, int64_t row_tile, int64_t col_tile)
+{
+    const int64_t rows = kPass == 2 ? g.E * ceil_div(g.N, row_tile) : g.T / row_tile + g.E + 1;
+    return rows * ceil_div(kPass == 0 ? g.N : g.K, col_tile);
+}
+
 template <bool kBig, int kPass>
 void launch_grouped_tiles(const GroupedArgs& g, bool out_fp32, hipStream_t s)
 {
     const int64_t t = kBig ? 256 : 128;
-    // every expert, and the rows of none, can have one partial row tile
-    const int64_t rows = kPass == 2 ? g.E * ceil_div(g.N, t) : g.T / t + g.E + 1;
-    const dim3 grid((uint32_t)(rows * ceil_div(kPass == 0 ? g.N : g.K, t) + (kBig ? g.cus : 0)));
+    const dim3 grid((uint32_t)(grouped_grid<kPass>(g, t, t) + (kBig ? g.cus : 0)));  // (halves of the remainder)
     if (out_fp32)
         hipLaunchKernelGGL((k_grouped<kBig, kPass, true>), grid, dim3(kBig ? 512 : 256), 0, s, g);
     else
@@ -989,7 +998,7 @@ int thin_rows(double rows) { return rows <= 16.0 ? 1 : rows <= 32.0 ? 2 : 4; }
 template <int kM>
 void launch_grouped_thin(const GroupedArgs& g, bool out_fp32, hipStream_t s)
 {
-    const dim3 grid((uint32_t)((g.T / (16 * kM) + g.E + 1) * ceil_div(g.N, 16 * kThinN)));
+    const dim3 grid((uint32_t)grouped_grid<0>(g, 16 * kM, 16 * kThinN));
     if (out_fp32)
         hipLaunchKernelGGL((k_grouped_thin<kM, true>), grid, dim3(256), 0, s, g);
     else
@@ -1021,7 +1030,8 @@ void launch_grouped_pass(const GroupedArgs& g, bool out_fp32, hipStream_t s)
     const double K = kPass == 0 ? (double)g.K : kPass == 1 ? (double)g.N : each;
     const double traffic =
         kPass == 0 ? row_tiles(16.0 * m) * ceil_div(cols, 16) * (std::min(each, 16.0 * m) + 16) * 2 * K : 0.0;
-    const Tiles t = choose(traffic, tiles(128), tiles(256), std::ceil(K / 64), g.cus);
+    const Tiles t = choose(traffic, grouped_grid<kPass>(g, 16 * m, 16 * kThinN), tiles(128),
+                           grouped_grid<kPass>(g, 128, 128), tiles(256), std::ceil(K / 64), g.cus);
     if (kPass == 0 && t == Tiles::kThin)
         return m == 1 ? launch_grouped_thin<1>(g, out_fp32, s)
                : m == 2 ? launch_grouped_thin<2>(g, out_fp32, s) : launch_grouped_thin<4>(g, out_fp32, s);
@@ -1038,10 +1048,12 @@ void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t*
 {
     if (M == 0 || N == 0) return;
     const int m = thin_rows((double)M);
-    const double traffic = (double)ceil_div(M, 16 * m) * ceil_div(N, 16) * (std::min(M, (int64_t)16 * m) + 16) * K;
+    const double traffic =
+        (double)ceil_div(M, 16 * m) * ceil_div(N, 16) * (std::min(M, (int64_t)16 * m) + 16) * std::max<int64_t>(K, 1);
     const auto tiles = [&](int64_t t) { return (double)ceil_div(M, t) * ceil_div(N, t); };
-    const Tiles t = choose(traffic, tiles(128), tiles(256), (double)ceil_div(K, 128), cus);
-    if (t == Tiles::kThin || K == 0) {
+    const Tiles t = choose(traffic, ceil_div(M, 16 * m) * ceil_div(N, 16 * kThinN), tiles(128),
+                           ceil_div(M, 128) * ceil_div(N, 128), tiles(256), (double)ceil_div(K, 128), cus);
+    if (t == Tiles::kThin) {
         const auto thin = m == 1 ? launch_i8_thin<1> : m == 2 ? launch_i8_thin<2> : launch_i8_thin<4>;
         return thin(a, lda, sa, b, ldb, sb, M, N, K, c, ldc, out_fp32, s);
     }

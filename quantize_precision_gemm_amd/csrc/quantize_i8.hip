@@ -62,55 +62,58 @@ __global__ __launch_bounds__(256) void k_i8_quant(const uint16_t* __restrict__ x
                                                   int8_t* __restrict__ codes, int64_t ld_codes,
                                                   float* __restrict__ scales)
 {
-    constexpr int kLanes = 64 * kWaves;
+    constexpr int kLanes = 64 * kWaves, kRows = 4 / kWaves;
     __shared__ uint32_t part[4];
-    const int64_t row = kWaves == 4 ? blockIdx.x : blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= rows) return;  // (a whole wave, and with kWaves = 4 none)
     const int lane = kWaves == 4 ? threadIdx.x : threadIdx.x & 63;
-    const uint16_t* src = x + row * ld;
-    uint4 held[kHeld];
-    uint32_t top = 0;
+    for (int64_t row = (int64_t)blockIdx.x * kRows + (kWaves == 4 ? 0 : threadIdx.x >> 6); row < rows;
+         row += (int64_t)gridDim.x * kRows) {
+        const uint16_t* src = x + row * ld;
+        uint4 held[kHeld];
+        uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int64_t k = 8 * (lane + (int64_t)kLanes * i);
-        held[i] = k < cols ? *reinterpret_cast<const uint4*>(src + k) : make_uint4(0, 0, 0, 0);
-    }
+        for (int i = 0; i < kHeld; ++i) {
+            const int64_t k = 8 * (lane + (int64_t)kLanes * i);
+            held[i] = k < cols ? *reinterpret_cast<const uint4*>(src + k) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) top = max_of(top, held[i]);
-    for (int64_t k = 8 * (lane + (int64_t)kLanes * kHeld); k < cols; k += 8 * kLanes)
-        top = max_of(top, *reinterpret_cast<const uint4*>(src + k));
-    top = wave_max_u32(top);
-    if constexpr (kWaves == 4) {
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-        __syncthreads();
-        top = max(max(part[0], part[1]), max(part[2], part[3]));
-    }
-    const float amax = __uint_as_float(top << 16);
-    if (lane == 0) scales[row] = amax / 127.0f;
-    // a power of two on both sides of the quotient keeps 127 / amax finite
-    const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
-    const float scale = amax > 0.0f ? 127.0f / (amax * lift) : 0.0f;
-    int8_t* dst = codes + row * ld_codes;
+        for (int i = 0; i < kHeld; ++i) top = max_of(top, held[i]);
+        for (int64_t k = 8 * (lane + (int64_t)kLanes * kHeld); k < cols; k += 8 * kLanes)
+            top = max_of(top, *reinterpret_cast<const uint4*>(src + k));
+        top = wave_max_u32(top);
+        if constexpr (kWaves == 4) {
+            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+            __syncthreads();
+            top = max(max(part[0], part[1]), max(part[2], part[3]));
+            __syncthreads();  // part is written again for the next row
+        }
+        const float amax = __uint_as_float(top << 16);
+        if (lane == 0) scales[row] = amax / 127.0f;
+        // a power of two on both sides of the quotient keeps 127 / amax finite
+        const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+        const float scale = amax > 0.0f ? 127.0f / (amax * lift) : 0.0f;
+        int8_t* dst = codes + row * ld_codes;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int64_t k = 8 * (lane + (int64_t)kLanes * i);
-        if (k < cols) *reinterpret_cast<uint2*>(dst + k) = codes_of(held[i], lift, scale);
+        for (int i = 0; i < kHeld; ++i) {
+            const int64_t k = 8 * (lane + (int64_t)kLanes * i);
+            if (k < cols) *reinterpret_cast<uint2*>(dst + k) = codes_of(held[i], lift, scale);
+        }
+        for (int64_t k = 8 * (lane + (int64_t)kLanes * kHeld); k < cols; k += 8 * kLanes)
+            *reinterpret_cast<uint2*>(dst + k) = codes_of(*reinterpret_cast<const uint4*>(src + k), lift, scale);
     }
-    for (int64_t k = 8 * (lane + (int64_t)kLanes * kHeld); k < cols; k += 8 * kLanes)
-        *reinterpret_cast<uint2*>(dst + k) = codes_of(*reinterpret_cast<const uint4*>(src + k), lift, scale);
 }
 
 void launch_i8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int8_t* codes, int64_t ld_codes,
                      float* scales, hipStream_t s)
 {
     if (rows == 0) return;
-    // a wave holds 2048 columns; with fewer rows than that fills the device, a workgroup takes one
+    // a wave holds 2048 columns; with fewer rows than fill the device so, a workgroup takes one row
+    const int64_t most = int64_t(1) << 22;  // workgroups; each takes more rows beyond that
     if (cols <= 512 * kHeld && rows > 1024)
-        hipLaunchKernelGGL(k_i8_quant<1>, dim3((uint32_t)((rows + 3) / 4)), dim3(256), 0, s, x, rows, cols, ld, codes,
-                           ld_codes, scales);
+        hipLaunchKernelGGL(k_i8_quant<1>, dim3((uint32_t)(rows < 4 * most ? (rows + 3) / 4 : most)), dim3(256), 0, s, x,
+                           rows, cols, ld, codes, ld_codes, scales);
     else
-        hipLaunchKernelGGL(k_i8_quant<4>, dim3((uint32_t)rows), dim3(256), 0, s, x, rows, cols, ld, codes, ld_codes,
-                           scales);
+        hipLaunchKernelGGL(k_i8_quant<4>, dim3((uint32_t)(rows < most ? rows : most)), dim3(256), 0, s, x, rows, cols, ld,
+                           codes, ld_codes, scales);
 }
 
 }  // namespace nvfp4

@@ -347,7 +347,7 @@ def test_refuses_tensors_that_do_not_fit(env):
                       (([f], [f], [e], [e], [s[:1]], [s]), ValueError), (([f, f], [f, b], [f, f], [f, f]), TypeError),
                       (([f, b], [f, f], [f, f], [f, f]), TypeError), (([f[::2]], [f[::2]], [f[::2]], [f[::2]]), ValueError),
                       (([b], [f], [f], [f], None, None, [b]), ValueError), (([f], [f], [f], [f], None, None, [f]), TypeError),
-                      (([f], [f.cpu()], [f], [f]), TypeError)]:
+                      (([f], [f.cpu()], [f], [f]), TypeError), (([f, f], [f, f], [f, f], [f, f]), ValueError)]:
         with pytest.raises(err):
             q.AdamWGroup(*args)
     grp = q.AdamWGroup([f], [f.clone()], [f.clone()], [f.clone()])
@@ -358,3 +358,51 @@ def test_refuses_tensors_that_do_not_fit(env):
         q.nvfp4_adamw(grp, 1, 1e-3, grad_scale=s)
     with pytest.raises(ValueError):
         q.nvfp4_adamw(grp, 1, 1e-3, grad_scale=torch.ones(1))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_large_step_equals_its_parts(env, bits):
+    """A launch that moves more than the caches hold, against the same
+    elements in groups of their own that the caches do hold."""
+    torch, q, dev = env
+    n, part = 50_000_000, 128 * 1000
+    d = tensors(torch, dev, [n, 77], torch.float32, torch.float32, bits, True, 6)
+    cuts = [(s, s + part) for s in (0, 128 * 100000, (n - part) // 128 * 128)]
+
+    def cut(k, t, s, e):
+        return t[s // 128:e // 128].clone() if k.endswith("scales") else t[s:e].clone()
+    small = [{k: None if v is None else [cut(k, v[0], s, e)] for k, v in d.items()} for s, e in cuts]
+    print(f"adamw large bits {bits}", flush=True)
+    q.nvfp4_adamw(q.AdamWGroup(**d), 9, **HYPER)
+    for (s, e), one in zip(cuts, small):
+        q.nvfp4_adamw(q.AdamWGroup(**one), 9, **HYPER)
+        for k, v in one.items():
+            if v is not None and k != "grads":
+                assert torch.equal(v[0].view(torch.uint8), cut(k, d[k][0], s, e).view(torch.uint8)), k
+
+
+def test_offsets_past_32_bits(env):
+    """A tensor of more than 2^32 elements in 8 bits: its ends as if alone."""
+    torch, q, dev = env
+    n, part = 2 ** 32 + 128 * 9 + 5, 128 * 50
+    p = torch.zeros(n, dtype=torch.bfloat16, device=dev)
+    g = torch.zeros(n, dtype=torch.bfloat16, device=dev)
+    tail = (n - part) // 128 * 128
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(8)
+    for s, e in ((0, part), (tail, n)):
+        p[s:e] = torch.randn(e - s, generator=gen, device=dev).bfloat16()
+        g[s:e] = torch.randn(e - s, generator=gen, device=dev).bfloat16()
+    grp = q.AdamWGroup.with_states([p], [g], bits=8)
+    small = [q.AdamWGroup.with_states([p[s:e].clone()], [g[s:e].clone()], bits=8) for s, e in ((0, part), (tail, n))]
+    print("adamw past 32 bits", flush=True)
+    for step in (1, 2):
+        for x in [grp] + small:
+            q.nvfp4_adamw(x, step, **HYPER)
+    torch.cuda.synchronize()
+    for (s, e), x in zip(((0, part), (tail, n)), small):
+        assert torch.equal(p[s:e], x.params[0])
+        for a, b in ((grp.m[0], x.m[0]), (grp.v[0], x.v[0])):
+            assert torch.equal(a[s:e].view(torch.uint8), b.view(torch.uint8))
+        for a, b in ((grp.m_scales[0], x.m_scales[0]), (grp.v_scales[0], x.v_scales[0])):
+            assert torch.equal(a[s // 128:][: b.numel()], b)

@@ -93,6 +93,14 @@ CASES = [
     ([300], 300, 256, 64),
     ([40, 24], 0, 8, 1032),
     ([700, 20, 1000], 0, 1288, 648),
+    # whole and partial rounds of the largest tiles, in each pass
+    ([3000, 0, 2690], 10, 2568, 2056),
+    ([130] * 60, 0, 264, 2056),
+    ([2600, 5100, 100], 0, 2056, 2568),
+    # rows for the 16-, 32- and 64-row products, more of some than a tile holds
+    ([16, 3, 20, 9], 0, 520, 4104),
+    ([30, 32, 41, 25], 1, 264, 2056),
+    ([64, 50, 100, 3], 0, 136, 1032),
 ]
 
 
@@ -326,3 +334,27 @@ def test_refuses_tensors_that_do_not_fit(env):
     odd = torch.zeros(8, 20, dtype=torch.bfloat16, device=dev)
     with pytest.raises(ValueError):
         q.nvfp4_bf16_grouped_gemm(q.FPROP, odd, torch.zeros(2, 16, 20, dtype=torch.bfloat16, device=dev), ends)
+
+
+def test_offsets_past_32_bits(env):
+    """Operands and outputs whose last rows lie more than 4 GiB behind their first."""
+    torch, q, dev = env
+    N, K, T, far = 64, 72, 1100, 2 ** 21  # 1100 rows, 4 MiB apart
+    ends = torch.tensor([40, 40, T], dtype=torch.int32, device=dev)
+    for pass_ in (FPROP, DGRAD, WGRAD):
+        a, b = operands(torch, dev, pass_, T, 3, N, K, 40)
+        want, size, C = reference(torch, pass_, a, b, [40, 40, T], 3)
+        wide = torch.empty(T, far, dtype=torch.bfloat16, device=dev)
+        wide[:, : a.shape[1]] = a
+        if pass_ == WGRAD:
+            place = b
+            out = torch.empty(3, N, far, dtype=torch.float32, device=dev)[:, :, :K]
+        else:
+            place = torch.empty(3, 2 ** 30, dtype=torch.bfloat16, device=dev)[:, : N * K].view(3, N, K)
+            place.copy_(b)
+            out = torch.empty(T, far, dtype=torch.float32, device=dev)[:, : want.shape[1]]
+        print(f"grouped far pass {pass_}", flush=True)
+        q.nvfp4_bf16_grouped_gemm(pass_, wide[:, : a.shape[1]], place, ends, out=out)
+        torch.cuda.synchronize()
+        check(torch, out, want, size, C, f"far pass {pass_}")
+        del wide, place, out

@@ -122,7 +122,8 @@ def check_gemm(torch, got, a, sa, b, sb, what):
                                    (16, 5003, 1296), (17, 256, 64), (31, 65, 2048), (33, 4100, 576), (64, 512, 640),
                                    (65, 100, 144), (127, 129, 1040), (128, 256, 512), (200, 1000, 272), (255, 257, 400),
                                    (256, 256, 128), (257, 513, 112), (300, 520, 1296), (777, 1288, 640), (1100, 72, 3088),
-                                   (520, 2056, 16)])
+                                   (520, 2056, 16),
+                                   (5000, 2568, 2064), (7900, 2568, 1040), (48, 512, 4112)])
 def test_gemm(env, M, N, K):
     torch, q, dev = env
     a, sa, b, sb = problem(torch, dev, M, N, K, M + N + K)
@@ -251,3 +252,39 @@ def test_refuses_tensors_that_do_not_fit(env):
         q.nvfp4_i8_gemm(q.I8Tensor(c[:, :24], s), q.I8Tensor(c[:, :24], s))
     with pytest.raises(ValueError):
         q.nvfp4_i8_quantize(torch.zeros(4, 32, dtype=torch.bfloat16, device=dev), out=q.I8Tensor(c[:3], s[:3]))
+
+
+def test_offsets_past_32_bits(env):
+    torch, q, dev = env
+    N, K, far = 40, 96, 2 ** 22
+    for M in (1100, 1300):
+        a, sa, b, sb = problem(torch, dev, M, N, K, 4)
+        wide = torch.empty(M, far, dtype=torch.int8, device=dev)[:, :K]
+        wide.copy_(a)
+        out = torch.empty(M, far // 2, dtype=torch.bfloat16, device=dev)[:, :N]
+        print(f"i8 far {M}", flush=True)
+        q.nvfp4_i8_gemm(q.I8Tensor(wide, sa), q.I8Tensor(b, sb), out=out)
+        torch.cuda.synchronize()
+        check_gemm(torch, out, a, sa, b, sb, "far")
+        x = torch.randn(M, K, device=dev).bfloat16()
+        far_x = torch.empty(M, far // 2, dtype=torch.bfloat16, device=dev)[:, :K]
+        far_x.copy_(x)
+        got = q.nvfp4_i8_quantize(far_x, out=q.I8Tensor(wide, torch.empty(M, device=dev)))
+        want, _ = exact_codes(torch, x)
+        assert torch.equal(got.codes, want)
+
+
+def test_quantize_many_short_rows(env):
+    """More rows than a launch has workgroups."""
+    torch, q, dev = env
+    g = torch.Generator(device=dev)
+    g.manual_seed(3)
+    rows = 4 * 2 ** 22 + 5
+    x = torch.randn(rows, 16, generator=g, device=dev).bfloat16()
+    print("i8 quantize many rows", flush=True)
+    got = q.nvfp4_i8_quantize(x)
+    torch.cuda.synchronize()
+    for part in (slice(0, 100000), slice(rows - 100000, rows)):
+        codes, scales = exact_codes(torch, x[part])
+        assert torch.equal(got.codes[part], codes)
+        assert ((got.scales[part].double() - scales).abs() <= 2.0 ** -24 * scales).all().item()

@@ -37,6 +37,7 @@ GROUPED = dict(pass_=0, a=FAKE, lda=64, b=FAKE, ldb=64, sb=64 * 32, ends=FAKE, E
     ({"pass_": 1, "lda": 24}, -2), ({"pass_": 1, "ldc": 60}, -2),
     ({"pass_": 2, "sc": 64 * 31}, -2), ({"pass_": 2, "sc": 64 * 32 + 2}, -3),
     ({"T": (1 << 31) - 8, "N": 1 << 20, "ldc": 1 << 20, "sb": 1 << 26}, -2),  # more tiles than a grid holds
+    ({"lda": 1 << 22}, -2), ({"ldb": 1 << 22, "sb": 1 << 28}, -2),  # rows further apart than 32-bit offsets reach
 ])
 def test_grouped_validation(lib, change, status):
     d = dict(GROUPED, **change)
@@ -58,7 +59,7 @@ ADAMW = dict(p=FAKE, g=FAKE, m=FAKE, v=FAKE, m_scale=FAKE, v_scale=FAKE, copy=FA
     ({"pd": 0}, -4),  # a copy of bf16 parameters
     ({"p": FAKE + 2}, -3), ({"g": FAKE + 2}, -3), ({"copy": FAKE + 1}, -3), ({"m_scale": FAKE + 2}, -3),
     ({"m": FAKE + 2, "bits": 32}, -3), ({"v": FAKE + 1, "bits": 32}, -3), ({"gs": FAKE + 2}, -3),
-    ({"n": 1 << 60}, -2),
+    ({"n": 1 << 60}, -2), ({"n": (1 << 33) + 1}, -2),
 ])
 def test_adamw_validation(lib, change, status):
     d = dict(ADAMW, **change)
@@ -99,7 +100,7 @@ I8 = dict(a=FAKE, lda=64, sa=FAKE, b=FAKE, ldb=64, sb=FAKE, M=3, N=5, K=64, c=FA
     ({"a": None}, -1), ({"b": None}, -1), ({"c": None}, -1), ({"sa": None}, -1), ({"sb": None}, -1),
     ({"a": FAKE + 8}, -3), ({"b": FAKE + 4}, -3), ({"lda": 72}, -3), ({"ldb": 72}, -3), ({"sa": FAKE + 1}, -3),
     ({"sb": FAKE + 2}, -3), ({"c": FAKE + 8}, -3), ({"c": FAKE + 4, "dtype": 0}, -3), ({"ldc": 6}, -3),
-    ({"lda": 48}, -2), ({"ldb": 48}, -2), ({"ldc": 4}, -2),
+    ({"lda": 48}, -2), ({"ldb": 48}, -2), ({"ldc": 4}, -2), ({"lda": 1 << 23}, -2), ({"ldb": 1 << 23}, -2),
     ({"M": (1 << 31) - 1, "N": (1 << 31) - 4, "ldc": 1 << 31}, -2),
 ])
 def test_i8_gemm_validation(lib, change, status):

@@ -293,7 +293,7 @@ __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t 
 // the power limit lowers the clock (1.5 to 1.7 GHz).
 // ---------------------------------------------------------------------------
 constexpr int kHalfBytes = 128 * 128;
-constexpr int kLdsBytes = 8 * kHalfBytes;
+constexpr int kLdsBytes = 9 * kHalfBytes;
 
 __device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
 
@@ -627,6 +627,92 @@ __device__ __forceinline__ void mid_tile(const View& A, const View& B, int64_t m
     barrier();  // nothing is on its way into LDS or being read any more
 }
 
+// The 128 x 256 products of a 256 x 256 tile of which no more rows are
+// wanted: the same loop with the 8 waves of the big tile, 2 x 4 of 64 x 64
+// outputs each, and three buffers of 48 KB.
+template <class Acc, bool kTA, bool kTB>
+__device__ __forceinline__ void wide_tile(const View& A, const View& B, int64_t m0, int64_t n0, int64_t Ka, int64_t Kb,
+                                          int64_t mend, int steps, uint8_t* lds, Acc (&acc)[2][2])
+{
+    const int wave = wave_id(), wm = wave >> 2, wn = wave & 3;
+    Source<kTA, 512, 1> sa;
+    Source<kTB, 512, 2> sb;
+    sa.set(A, m0, Ka, true);
+    sb.set(B, n0, Kb, n0 + 128 < B.rows);
+    const bool used = m0 + 64 * wm < mend && n0 + 64 * wn < B.rows;
+    const Fragments<kTA, 2> fa(2 * wm);
+    const Fragments<kTB, 2> fb(2 * (wn & 1));
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    constexpr int kBuf = 3 * kHalfBytes, kB = kHalfBytes;  // a buffer: A, then B's halves
+    const int b_half = kB + (wn >> 1) * kHalfBytes;        // the wave's columns
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        sa.fetch_checked(0, t, base + t * kBuf);
+        sb.fetch_checked(0, t, base + t * kBuf + kB);
+        sb.fetch_checked(1, t, base + t * kBuf + kB + kHalfBytes);
+    }
+    uint4 a[2][2][4], b[2][2][4];
+    wait_dma<12>();
+    barrier();
+    if (used) {
+        fa.read(a[0], lds);
+        fb.read(b[0], lds + b_half);
+    }
+    const uint8_t *pa = sa.p + 3 * sa.advance, *pb = sb.p + 3 * sb.advance;  // the operands' bases of step t + 3
+    int buf = 0;                                                             // the buffer of step t
+    auto step = [&](int t, auto parity, auto whole) {
+        constexpr int cur = parity.value;
+        wait_lds();
+        wait_dma<6>();  // all but step t + 2
+        barrier();
+        const int next = buf == 2 * kBuf ? 0 : buf + kBuf;
+        if (used) {
+            fa.read(a[cur ^ 1], lds + next);
+            fb.read(b[cur ^ 1], lds + next + b_half);
+        }
+        auto multiply = [&](int s) {
+            if (!used) return;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[j][i] = mma(b[cur][j][s], a[cur][i][s], acc[j][i]);
+        };
+        multiply(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (whole.value) sa.fetch(0, pa, base + buf);
+        else sa.fetch_checked(0, t + 3, base + buf);
+        multiply(1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (whole.value) {
+            sb.fetch(0, pb, base + buf + kB);
+            sb.fetch(1, pb, base + buf + kB + kHalfBytes);
+        } else {
+            sb.fetch_checked(0, t + 3, base + buf + kB);
+            sb.fetch_checked(1, t + 3, base + buf + kB + kHalfBytes);
+        }
+        multiply(2);
+        multiply(3);
+        pa += sa.advance;
+        pb += sb.advance;
+        buf = next;
+    };
+    typedef std::integral_constant<int, 0> Even;
+    typedef std::integral_constant<int, 1> Odd;
+    const int whole = min(sa.whole(), sb.whole());
+    int t = 0;
+    for (; t + 4 < whole; t += 2) {
+        step(t, Even(), std::true_type());
+        step(t + 1, Odd(), std::true_type());
+    }
+    for (; t < steps; t += 2) {
+        step(t, Even(), std::false_type());
+        if (t + 1 < steps) step(t + 1, Odd(), std::false_type());
+    }
+    wait_lds();
+    wait_dma<0>();
+    barrier();  // nothing is on its way into LDS or being read any more
+}
+
 // kStream: past the caches (a weight gradient is larger than they are).
 template <bool kStream>
 __device__ __forceinline__ void store16(void* d, uint4 v)
@@ -718,22 +804,22 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
 
 // Sums as they are.
 struct Plain {
-    __device__ __forceinline__ void row(int, int, int64_t) {}
+    __device__ __forceinline__ void row(int, int64_t) {}
     __device__ __forceinline__ void columns(int, int64_t, int) {}
-    __device__ __forceinline__ float operator()(float v, int, int, int, int) const { return v; }
+    __device__ __forceinline__ float operator()(float v, int, int, int) const { return v; }
 };
 
 // Integer sums times the scales of their row and column.
 struct Scaled {
     const float *sa, *sb;
     int64_t M, N;
-    float rows[2][2], cols[2][16];
+    float rows[2], cols[2][16];
 
     __device__ __forceinline__ Scaled(const float* sa_, const float* sb_, int64_t M_, int64_t N_)
         : sa(sa_), sb(sb_), M(M_), N(N_)
     {
     }
-    __device__ __forceinline__ void row(int h, int i, int64_t m) { rows[h][i] = sa[min(m, M - 1)]; }
+    __device__ __forceinline__ void row(int i, int64_t m) { rows[i] = sa[min(m, M - 1)]; }
     // columns n + first + 8 (e / 4) + e % 4 of accumulators e
     __device__ __forceinline__ void columns(int k, int64_t n, int first)
     {
@@ -742,9 +828,9 @@ struct Scaled {
 #pragma unroll
         for (int e = 0; e < 16; ++e) cols[k][e] = (sb + at)[min(first + 8 * (e >> 2) + (e & 3), last)];
     }
-    __device__ __forceinline__ float operator()(int v, int h, int i, int k, int e) const
+    __device__ __forceinline__ float operator()(int v, int i, int k, int e) const
     {
-        return ((float)v * rows[h][i]) * cols[k][e];
+        return ((float)v * rows[i]) * cols[k][e];
     }
 };
 
@@ -755,26 +841,38 @@ __device__ __forceinline__ void tile(const View& A, const View& B, int64_t m0, i
                                      int64_t mend, int steps, uint8_t* lds, void* c, int64_t c_at, int64_t ldc,
                                      Convert convert)
 {
-    constexpr int kHalves = kBig ? 2 : 1;
     const int lane = threadIdx.x & 63, wave = wave_id();
     const int wm = kBig ? wave >> 2 : wave >> 1, wn = kBig ? wave & 3 : wave & 1;
-    Acc acc[kHalves][2][2] = {};  // [half of A][column piece][32 rows]
     if constexpr (kBig) {
-        if (steps > 0) big_tile<Acc, kTA, kTB>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
-    } else {
-        if (steps > 0) mid_tile<Acc, kTA, kTB>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc[0]);
+        if (m0 + 128 < mend) {
+            Acc acc[2][2][2] = {};  // [half of A][half of B][32 rows]
+            if (steps > 0) big_tile<Acc, kTA, kTB>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
+            const int64_t col[2] = {n0 + column0<kTB>(wn, 0), n0 + column0<kTB>(wn, 1)};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) convert.columns(k, col[k], 4 * (lane >> 5));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t row0 = m0 + 128 * h + 64 * wm;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) convert.row(i, row0 + 32 * i + (lane & 31));
+                store_wave<kF32, kStream>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc,
+                                          [&](int i, int k, int e) { return convert(acc[h][k][i][e], i, k, e); });
+            }
+            return;
+        }
     }
-    const int64_t col[2] = {n0 + (kBig ? column0<kTB>(wn, 0) : 64 * wn), n0 + (kBig ? column0<kTB>(wn, 1) : 64 * wn + 32)};
+    Acc acc[2][2] = {};  // [32 columns][32 rows]
+    if (steps > 0) {
+        if constexpr (kBig) wide_tile<Acc, kTA, kTB>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
+        else mid_tile<Acc, kTA, kTB>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
+    }
+    const int64_t row0 = m0 + 64 * wm, col[2] = {n0 + 64 * wn, n0 + 64 * wn + 32};
 #pragma unroll
     for (int k = 0; k < 2; ++k) convert.columns(k, col[k], 4 * (lane >> 5));
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h) {
-        const int64_t row0 = m0 + 128 * h + 64 * wm;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) convert.row(h, i, row0 + 32 * i + (lane & 31));
-        store_wave<kF32, kStream>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc,
-                                  [&](int i, int k, int e) { return convert(acc[h][k][i][e], h, i, k, e); });
-    }
+    for (int i = 0; i < 2; ++i) convert.row(i, row0 + 32 * i + (lane & 31));
+    store_wave<kF32, kStream>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc,
+                              [&](int i, int k, int e) { return convert(acc[k][i][e], i, k, e); });
 }
 
 // Tile `in` of a product of tm x tn tiles, walked in groups of 8 tile rows,
@@ -814,7 +912,7 @@ __device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, 
         at += hw - hw % cus;
         return true;
     }
-    const bool split = kBig && 8 * rest <= 3 * cus;
+    const bool split = kBig && 2 * rest <= cus;
     if (!xcd_order(hw - full, split ? 2 * rest : rest, at)) return false;
     if (split) {
         half = (int)(at & 1);

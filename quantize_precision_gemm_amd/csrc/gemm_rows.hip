@@ -898,10 +898,10 @@ __device__ __forceinline__ bool xcd_order(int64_t hw, int64_t total, int64_t& at
 // both).  Whole rounds of one tile per compute unit come first, each round
 // dealt so that an XCD gets neighbouring tiles of it (dealt over all rounds
 // at once, the XCD of the largest experts would finish last: 468 against
-// 354 us for a wgrad of 16 uneven experts, 8192 x 2560 x 5120).  If what remains is at most
-// 3/8 of the compute units, its tiles are done as two halves of 128 rows each
-// (a half's step takes 0.95 us with 160 of them, 1.3 with 256; a whole
-// tile's 1.1 to 1.4).
+// 354 us for a wgrad of 16 uneven experts, 8192 x 2560 x 5120).  If what
+// remains is at most half the compute units, its tiles are done as two halves
+// of 128 rows each (a step of up to 160 halves takes 0.71 us, of 256 about
+// 1.0, a whole tile's 1.15 to 1.6).
 template <bool kBig>
 __device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, int& half)
 {
@@ -968,7 +968,7 @@ __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_grouped(Grou
     }
     m0 = (int64_t)kTile * im + (half == 1 ? 128 : 0);
     n0 = (int64_t)kTile * in_;
-    mend = half == 0 ? min(m0 + 128, A.rows) : A.rows;
+    mend = half >= 0 ? min(m0 + 128, A.rows) : A.rows;
     if (m0 >= mend) return;
     tile<kBig, f32x16_t, kPass == 2, kPass != 0, kF32, kPass == 2>(A, B, m0, n0, Ka, Kb, mend, steps, lds, g.c, c_at, g.ldc,
                                                                    Plain());
@@ -988,7 +988,7 @@ __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_i8(
     grouped_order((int)at, tm, tn, im, in_);
     const View A{reinterpret_cast<const uint8_t*>(a), lda, M}, B{reinterpret_cast<const uint8_t*>(b), ldb, N};
     const int64_t m0 = (int64_t)kTile * im + (half == 1 ? 128 : 0), n0 = (int64_t)kTile * in_;
-    const int64_t mend = half == 0 ? min(m0 + 128, M) : M;
+    const int64_t mend = half >= 0 ? min(m0 + 128, M) : M;
     if (m0 >= mend) return;
     tile<kBig, i32x16_t, false, false, kF32, false>(A, B, m0, n0, K, K, mend, (int)((K + 127) / 128), lds, c, 0, ldc,
                                                     Scaled(sa, sb, M, N));
@@ -1045,9 +1045,11 @@ enum class Tiles { kThin, kMid, kBig };
 // on 256 compute units, int8 and bf16 alike):
 //   thin  6 and its traffic from the caches at 8.5 TB/s (`traffic` bytes; none: 0)
 //   mid   1.5, and 4 and 0.47 per step for each round of its tiles
-//   big   1.5, and 9 and 1.15 per step for each round (0.95 in a last round of halves)
-// For example int8, N = K = 5120: 16 rows 11.7 / 20.2 / 31.9, 64 rows 24.8 /
-// 21.2 / 32.4, 2048 rows - / 79 / 55; N = 1024, K = 2048, 256 rows 10.7 / 13.1 / 19.3.
+//   big   1.5, and 9 and 1.15 per step for each round (7 and 0.72 to 1.0 in a
+//         last round of halves)
+// For example int8, N = K = 5120: 16 rows 12.4 / 20.4 / 25.0, 64 rows 25.0 /
+// 21.2 / 26.1, 777 rows - / 43.1 / 36.3, 2048 rows - / 75.5 / 54.4; N = 1024,
+// K = 2048, 256 rows 10.8 / 13.5 / 18.1.
 // thin_grid, mid_grid: their workgroups; a grid holds fewer than 2^32 threads.
 Tiles choose(double traffic, int64_t thin_grid, double mid, int64_t mid_grid, double big, double steps, int cus)
 {
@@ -1056,7 +1058,7 @@ Tiles choose(double traffic, int64_t thin_grid, double mid, int64_t mid_grid, do
     const double m = mid_grid < most ? 1.5 + std::ceil(mid / cus) * (4.0 + 0.47 * steps) : 1e30;
     const double whole = std::floor(big / cus), rest = big - whole * cus;
     const double b = 1.5 + whole * (9.0 + 1.15 * steps) +
-                     (rest > 0 ? 9.0 + (8 * rest <= 3 * cus ? 0.95 : 1.15) * steps : 0.0);
+                     (rest == 0 ? 0.0 : 2 * rest <= cus ? 7.0 + (8 * rest <= 3 * cus ? 0.72 : 1.0) * steps : 9.0 + 1.15 * steps);
     return thin <= m && thin <= b ? Tiles::kThin : m <= b ? Tiles::kMid : Tiles::kBig;
 }
 

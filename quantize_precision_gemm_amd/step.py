@@ -12,7 +12,8 @@ quantised first, by role (2.A, 2.B.2-2.B.4):
   dY, X  16-point random Hadamard transform along tokens, transposed, 1x16;
          SR for dY, RNE for X, one sign vector for both   (wgrad)
 
-A layer kept in BF16 (2.B.1) runs the same three GEMMs on the bf16 tensors.
+A layer kept in BF16 (2.B.1) runs the same three GEMMs on the bf16 tensors;
+a layer of experts kept in BF16 runs them grouped by expert.
 
 Every operation is a library call; this module only allocates buffers (once,
 in the constructors) and orders the launches.  Nothing here computes.
@@ -247,6 +248,53 @@ class BF16Linear:
     def wgrad_ops(self):
         q = self.q
         return [("bf16_wgrad", lambda: q.nvfp4_bf16_gemm(q.WGRAD, self.dy, self.x, out=self.dw))]
+
+
+class BF16Experts:
+    """A linear layer of E experts kept in bf16: the three GEMMs grouped by
+    expert (nvfp4_bf16_grouped_gemm).
+
+    x (T x K), dy (T x N): the tokens sorted by expert; ends (E, int32): one
+    past the last token of each; w (E x N x K).  Outputs: y (T x N, bf16), dx
+    (T x K, bf16), dw (E x N x K, fp32).  x, dy and ends may be refilled from
+    step to step (another routing needs no other buffers).
+    """
+
+    def __init__(self, q, torch, x, w, dy, ends):
+        self.q, self.torch = q, torch
+        self.x, self.w, self.dy, self.ends = x, w, dy, ends
+        T, K = x.shape
+        E, N = w.shape[:2]
+        assert w.shape == (E, N, K) and dy.shape == (T, N) and ends.shape == (E,)
+        self.T, self.K, self.N, self.E = T, K, N, E
+        dev = x.device
+        self.y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        self.dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        self.dw = torch.empty((E, N, K), dtype=torch.float32, device=dev)
+
+    def flops(self):
+        return 3 * 2.0 * self.T * self.N * self.K
+
+    def weight_ops(self):
+        return []
+
+    def forward_ops(self):
+        q = self.q
+        return [("experts_fprop", lambda: q.nvfp4_bf16_grouped_gemm(q.FPROP, self.x, self.w, self.ends, out=self.y))]
+
+    def backward_shared_ops(self):
+        return []
+
+    def backward_quant_ops(self):
+        return []
+
+    def dgrad_ops(self):
+        q = self.q
+        return [("experts_dgrad", lambda: q.nvfp4_bf16_grouped_gemm(q.DGRAD, self.dy, self.w, self.ends, out=self.dx))]
+
+    def wgrad_ops(self):
+        q = self.q
+        return [("experts_wgrad", lambda: q.nvfp4_bf16_grouped_gemm(q.WGRAD, self.dy, self.x, self.ends, out=self.dw))]
 
 
 class TrainingStep:

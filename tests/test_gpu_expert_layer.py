@@ -1,0 +1,63 @@
+"""The expert layer of examples/expert_layer.py: its three passes through
+the training-step driver, its training and its answers in int8."""
+import os
+import sys
+
+import pytest
+
+from tests.gpu_util import ROOT, ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    ensure_built()
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import expert_layer
+    import quantize_precision_gemm_amd as q
+    return torch, q, expert_layer
+
+
+def test_experts_in_a_training_step(env):
+    """BF16Experts beside a plain bf16 layer in one TrainingStep: the outputs
+    of the calls made one by one."""
+    torch, q, _ = env
+    from quantize_precision_gemm_amd.step import BF16Experts, BF16Linear, TrainingStep
+    dev = torch.device("cuda:0")
+    g = torch.Generator(device=dev)
+    g.manual_seed(3)
+
+    def rnd(*s):
+        return torch.randn(s, generator=g, device=dev).bfloat16()
+    T, K, N, E = 300, 256, 136, 3
+    ends = torch.tensor([120, 120, 300], dtype=torch.int32, device=dev)
+    experts = BF16Experts(q, torch, rnd(T, K), rnd(E, N, K), rnd(T, N), ends)
+    dense = BF16Linear(q, torch, rnd(T + 4, K), rnd(N, K), rnd(T + 4, N))  # (its tokens come in eights)
+    for serial in (False, True):
+        for t in (experts.y, experts.dx, experts.dw):
+            t.zero_()
+        print(f"experts in a step, serial {serial}", flush=True)
+        TrainingStep(torch, [dense, experts], dev, serial_gemms=serial).run()
+        torch.cuda.synchronize()
+        assert torch.equal(experts.y, q.nvfp4_bf16_grouped_gemm(q.FPROP, experts.x, experts.w, ends))
+        assert torch.equal(experts.dx, q.nvfp4_bf16_grouped_gemm(q.DGRAD, experts.dy, experts.w, ends))
+        assert torch.equal(experts.dw, q.nvfp4_bf16_grouped_gemm(q.WGRAD, experts.dy, experts.x, ends, torch.float32))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_training_learns_the_maps(env, bits):
+    """From zero weights the loss starts at the targets' variance (1) and has
+    to fall to a twentieth of it; the int8 answers stay near the bf16 ones:
+    codes of 127 steps put an error of about 1 / (127 sqrt(12) / 3) = 0.7 % of a
+    typical value on each factor, 2 % leaves twice both."""
+    torch, q, ex = env
+    print(f"expert layer training, {bits}-bit states", flush=True)
+    losses, master, task = ex.train(steps=60, bits=bits)
+    assert 0.8 < losses[0] < 1.25
+    assert losses[-1] < 0.05, losses[::10]
+    x, ends, _ = task.batch()
+    bf16 = q.nvfp4_bf16_grouped_gemm(q.FPROP, x, master.bfloat16(), ends, torch.float32)
+    int8 = ex.answer_in_int8(master, x, ends)
+    assert ((int8 - bf16).norm() / bf16.norm()).item() < 0.02

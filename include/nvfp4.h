@@ -545,12 +545,28 @@ int nvfp4_mfma_sustain(int64_t blocks, int64_t iters, int32_t operands, float* o
  *   c, ldc, c_dtype  as for nvfp4_gemm; WGRAD: expert e at c + e * stride_c
  *             elements (a multiple of 4), its rows ldc apart; otherwise
  *             stride_c is ignored.
+ *   workspace optional device memory, 16-byte aligned.  With at least the
+ *             bytes that nvfp4_bf16_grouped_gemm_workspace reports, a long
+ *             contraction of few output tiles is taken in parts over equal
+ *             runs of it, whose fp32 sums go to the workspace and are added
+ *             in order by a second kernel (deterministic; the last bits may
+ *             differ from the whole sum's).  NULL or less: it is not split.
+ *             Its contents on entry do not matter; calls that share it must
+ *             not overlap.
  * Returns NVFP4_OK or a negative status; nothing is enqueued on failure.
  */
 int nvfp4_bf16_grouped_gemm(int32_t pass, const void* a, int64_t lda, const void* b, int64_t ldb,
                             int64_t stride_b, const int32_t* ends, int64_t E, int64_t T, int64_t N,
                             int64_t K, void* c, int64_t ldc, int64_t stride_c, int32_t c_dtype,
-                            void* stream);
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * nvfp4_bf16_grouped_gemm_workspace -- host query: the workspace bytes with
+ * which nvfp4_bf16_grouped_gemm splits a product of this pass and size on the
+ * current device (0: it does not split it; at most 64 KB per compute unit).
+ * *bytes is written only on NVFP4_OK.
+ */
+int nvfp4_bf16_grouped_gemm_workspace(int32_t pass, int64_t E, int64_t T, int64_t N, int64_t K, int64_t* bytes);
 
 /* One tensor of an AdamW step (device pointers; n elements each, contiguous). */
 typedef struct nvfp4_adamw_tensor {

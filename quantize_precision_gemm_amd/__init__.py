@@ -23,7 +23,7 @@ __all__ = [
     "nvfp4_rht_sign_mask", "nvfp4_amax", "nvfp4_bf16_gemm", "nvfp4_mx_quantize",
     "nvfp4_mx_gemm", "nvfp4_rht_quantize_sized", "nvfp4_rht_signs64", "nvfp4_quantize_rht_rows", "BLOCK_MX32", "MX_ROWS", "MX_COLS", "MX_COLS_RHT", "nvfp4_gemm_fp8blk", "nvfp4_gemm_amax", "nvfp4_gemm_split", "nvfp4_gemm_split_workspace", "nvfp4_gemm_split_noalloc",
     "nvfp4_mfma_sustain", "MFMA_SUSTAIN_DECODED", "MFMA_SUSTAIN_RANDOM", "MFMA_SUSTAIN_FP4",
-    "nvfp4_bf16_grouped_gemm", "AdamWGroup", "nvfp4_adamw", "I8Tensor", "nvfp4_i8_quantize", "nvfp4_i8_gemm",
+    "nvfp4_bf16_grouped_gemm", "nvfp4_bf16_grouped_gemm_workspace", "AdamWGroup", "nvfp4_adamw", "I8Tensor", "nvfp4_i8_quantize", "nvfp4_i8_gemm",
     "LAYOUT_ROW_MAJOR", "LAYOUT_INTERLEAVED", "interleave_codes", "deinterleave_codes",
     "lib_path", "load_library",
 ]
@@ -125,8 +125,10 @@ def load_library():
         L.nvfp4_mfma_sustain.argtypes = [i64, i64, i32, P, P]
         L.nvfp4_mfma_sustain.restype = ctypes.c_int
         L.nvfp4_bf16_grouped_gemm.argtypes = [i32, P, i64, P, i64, i64, P, i64, i64, i64, i64, P, i64, i64,
-                                              i32, P]
+                                              i32, P, i64, P]
         L.nvfp4_bf16_grouped_gemm.restype = ctypes.c_int
+        L.nvfp4_bf16_grouped_gemm_workspace.argtypes = [i32, i64, i64, i64, i64, ctypes.POINTER(i64)]
+        L.nvfp4_bf16_grouped_gemm_workspace.restype = ctypes.c_int
         f64 = ctypes.c_double
         L.nvfp4_adamw.argtypes = [P, i64, i32, i32, i32, i64, f64, f64, f64, f64, f64, P, P]
         L.nvfp4_adamw.restype = ctypes.c_int
@@ -702,7 +704,18 @@ def _check_bf16_experts(w, what):
         raise ValueError(f"{what}: the last dimension must be contiguous")
 
 
-def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=None, stream=None):
+def nvfp4_bf16_grouped_gemm_workspace(pass_, E, T, N, K):
+    """Bytes with which nvfp4_bf16_grouped_gemm splits the contraction (0: it does not)."""
+    need = ctypes.c_int64(0)
+    st = load_library().nvfp4_bf16_grouped_gemm_workspace(pass_, E, T, N, K, ctypes.byref(need))
+    _check(st, "nvfp4_bf16_grouped_gemm_workspace")
+    return need.value
+
+
+_SPLIT_FROM = 512  # shortest contraction that is worth asking about
+
+
+def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """GEMM of a linear layer of E experts kept in bf16, its rows sorted by
     expert (see nvfp4_bf16_grouped_gemm in nvfp4.h).
 
@@ -710,6 +723,9 @@ def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=Non
     DGRAD: a = dY (T x N), b = W (E x N x K) -> T x K
     WGRAD: a = dY (T x N), b = X (T x K) -> E x N x K
     ends: int32 device tensor (E): one past the last row of each expert.
+    workspace: uint8 device tensor for a split contraction; without one, what
+    nvfp4_bf16_grouped_gemm_workspace asks for is allocated (an empty one: no
+    split).
     """
     _check_bf16(a)
     index = a.get_device()
@@ -761,9 +777,16 @@ def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=Non
         _check_gemm_out(out, shape, a.device)
         code = _out_code(out.dtype)
         ldc = _pitch(out, 4)
+    if workspace is not None:
+        _check_buf(workspace, "workspace", a.device, torch.uint8, (0,))
+    elif (T if pass_ == WGRAD else a_cols) >= _SPLIT_FROM:
+        need = nvfp4_bf16_grouped_gemm_workspace(pass_, E, T, N, K)
+        if need:
+            workspace = _for_stream(torch.empty(need, dtype=torch.uint8, device=a.device), stream)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     st = load_library().nvfp4_bf16_grouped_gemm(pass_, a.data_ptr(), _pitch(a), b.data_ptr(), ldb, stride_b,
                                                 ends.data_ptr(), E, T, N, K, out.data_ptr(), ldc, stride_c, code,
-                                                _raw_stream(stream))
+                                                ws, ws_bytes, _raw_stream(stream))
     if st:
         _check(st, "nvfp4_bf16_grouped_gemm")
     return out

@@ -655,6 +655,18 @@ bool adamw_vec(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight
            aligned(t.v, eight ? 4 : 16) && aligned(t.copy, 8);
 }
 
+// Pass and sizes of a grouped product.
+int check_grouped(int32_t pass, int64_t E, int64_t T, int64_t N, int64_t K)
+{
+    if (pass != NVFP4_FPROP && pass != NVFP4_DGRAD && pass != NVFP4_WGRAD) return NVFP4_ERR_MODE;
+    if (E < 0 || T < 0 || N < 0 || K < 0 || N % 8 || K % 8) return NVFP4_ERR_SHAPE;
+    const int64_t lim = int64_t(1) << 31;
+    if (E >= lim || T >= lim || N >= lim || K >= lim) return NVFP4_ERR_SHAPE;
+    const int64_t cols = pass == NVFP4_FPROP ? N : K;
+    const int64_t tiles = (pass == NVFP4_WGRAD ? E * ((N + 255) / 256) : T / 256 + E + 1) * ((cols + 255) / 256);
+    return tiles < kMostBigTiles ? NVFP4_OK : NVFP4_ERR_SHAPE;
+}
+
 int check_adamw(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight)
 {
     if (t.n < 0) return NVFP4_ERR_SHAPE;
@@ -754,15 +766,30 @@ int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int
     return launch_status();
 }
 
+int nvfp4_bf16_grouped_gemm_workspace(int32_t pass, int64_t E, int64_t T, int64_t N, int64_t K, int64_t* bytes)
+{
+    if (!bytes) return NVFP4_ERR_NULL;
+    const int st = check_grouped(pass, E, T, N, K);
+    if (st != NVFP4_OK) return st;
+    nvfp4::GroupedArgs g{};
+    g.E = E;
+    g.T = T;
+    g.N = N;
+    g.K = K;
+    g.cus = std::max(device_cus(), 1);
+    *bytes = nvfp4::grouped_workspace(pass, g);
+    return NVFP4_OK;
+}
+
 int nvfp4_bf16_grouped_gemm(int32_t pass, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t stride_b,
                             const int32_t* ends, int64_t E, int64_t T, int64_t N, int64_t K, void* c, int64_t ldc,
-                            int64_t stride_c, int32_t c_dtype, void* stream)
+                            int64_t stride_c, int32_t c_dtype, void* workspace, int64_t workspace_bytes, void* stream)
 {
-    if (pass != NVFP4_FPROP && pass != NVFP4_DGRAD && pass != NVFP4_WGRAD) return NVFP4_ERR_MODE;
     if (c_dtype != NVFP4_OUT_BF16 && c_dtype != NVFP4_OUT_FP32) return NVFP4_ERR_MODE;
-    if (E < 0 || T < 0 || N < 0 || K < 0 || N % 8 || K % 8) return NVFP4_ERR_SHAPE;
-    const int64_t lim = int64_t(1) << 31;
-    if (E >= lim || T >= lim || N >= lim || K >= lim) return NVFP4_ERR_SHAPE;
+    const int st = check_grouped(pass, E, T, N, K);
+    if (st != NVFP4_OK) return st;
+    if (workspace_bytes < 0) return NVFP4_ERR_SHAPE;
+    if (!aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
     const bool wgrad = pass == NVFP4_WGRAD;
     const int64_t a_cols = pass == NVFP4_FPROP ? K : N;
     const int64_t c_cols = pass == NVFP4_FPROP ? N : K;
@@ -783,11 +810,10 @@ int nvfp4_bf16_grouped_gemm(int32_t pass, const void* a, int64_t lda, const void
     // a tile's 256 rows (or 64 k rows) are addressed with 32-bit offsets
     const int64_t span = int64_t(1) << 22;
     if (lda >= span || ldb >= span) return NVFP4_ERR_SHAPE;
-    const int64_t tiles = (wgrad ? E * ((N + 255) / 256) : T / 256 + E + 1) * ((c_cols + 255) / 256);
-    if (tiles >= kMostBigTiles) return NVFP4_ERR_SHAPE;
     const nvfp4::GroupedArgs g{static_cast<const uint16_t*>(a), lda, static_cast<const uint16_t*>(b), ldb, stride_b,
-                               ends, E, T, N, K, c, ldc, stride_c, std::max(device_cus(), 1)};
-    nvfp4::launch_grouped(pass, g, c_dtype == NVFP4_OUT_FP32, static_cast<hipStream_t>(stream));
+                               ends, E, T, N, K, c, ldc, stride_c, std::max(device_cus(), 1),
+                               static_cast<float*>(workspace), 1};
+    nvfp4::launch_grouped(pass, g, workspace_bytes, c_dtype == NVFP4_OUT_FP32, static_cast<hipStream_t>(stream));
     return launch_status();
 }
 

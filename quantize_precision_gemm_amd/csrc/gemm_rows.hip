@@ -894,8 +894,7 @@ __device__ __forceinline__ bool xcd_order(int64_t hw, int64_t total, int64_t& at
     return hw < total;
 }
 
-// The tile of this workgroup among `total`, and which of its row halves (-1:
-// both).  Whole rounds of one tile per compute unit come first, each round
+// The hw-th tile of `total`, and which of its row halves (-1: both).  Whole rounds of one tile per compute unit come first, each round
 // dealt so that an XCD gets neighbouring tiles of it (dealt over all rounds
 // at once, the XCD of the largest experts would finish last: 468 against
 // 354 us for a wgrad of 16 uneven experts, 8192 x 2560 x 5120).  If what
@@ -903,9 +902,9 @@ __device__ __forceinline__ bool xcd_order(int64_t hw, int64_t total, int64_t& at
 // of 128 rows each (a step of up to 160 halves takes 0.71 us, of 256 about
 // 1.0, a whole tile's 1.15 to 1.6).
 template <bool kBig>
-__device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, int& half)
+__device__ __forceinline__ bool tile_order(int64_t hw, int64_t total, int cus, int64_t& at, int& half)
 {
-    const int64_t hw = blockIdx.x, rest = total % cus, full = total - rest;
+    const int64_t rest = total % cus, full = total - rest;
     half = -1;
     if (hw < full) {
         if (!xcd_order(hw % cus, cus, at)) return false;
@@ -927,51 +926,116 @@ __device__ __forceinline__ bool tile_order(int64_t total, int cus, int64_t& at, 
 // 2 and 2 24.4 (more waves on a compute unit do more than more loads in one).
 constexpr int kThinN = 1, kThinU = 2;
 
+// One tile of a grouped product: its operands, place and steps.
+struct Place {
+    View A, B;
+    int64_t m0, n0, mend, Ka, Kb, c_at, at;
+    int steps;
+};
+
+// The hw-th tile's; false: there is none.
+template <bool kBig, int kPass>
+__device__ __forceinline__ bool place_tile(const GroupedArgs& g, int64_t hw, Place& t)
+{
+    constexpr int kTile = kBig ? 256 : 128;
+    const int64_t cols = kPass == 0 ? g.N : g.K;
+    const int tn = (int)((cols + kTile - 1) / kTile);
+    int im, in_, half;
+    if constexpr (kPass == 2) {
+        const int tm = (int)((g.N + kTile - 1) / kTile);
+        if (!tile_order<kBig>(hw, g.E * tm * tn, g.cus, t.at, half)) return false;
+        const int64_t e = t.at / (tm * tn);
+        grouped_order((int)(t.at % (tm * tn)), tm, tn, im, in_);
+        int64_t begin, end;
+        expert_rows(g.ends, e, g.T, begin, end);
+        t.A = View{reinterpret_cast<const uint8_t*>(g.a + begin * g.lda), 2 * g.lda, g.N};
+        t.B = View{reinterpret_cast<const uint8_t*>(g.b + begin * g.ldb), 2 * g.ldb, g.K};
+        t.Ka = t.Kb = end - begin;
+        t.steps = (int)((end - begin + 63) / 64);
+        t.c_at = e * g.c_expert;
+    } else {
+        Slice s;
+        const auto order = [&](int64_t total, int64_t& tile) {
+            if (!tile_order<kBig>(hw, total, g.cus, tile, half)) return false;
+            t.at = tile;
+            return true;
+        };
+        if (!find_tile<kTile>(g.ends, g.E, g.T, tn, order, s)) return false;
+        grouped_order((int)s.tile, (int)((s.end - s.begin + kTile - 1) / kTile), tn, im, in_);
+        const bool none = s.e >= g.E;  // rows of no expert: zeros
+        t.A = View{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
+        t.B = View{reinterpret_cast<const uint8_t*>(g.b + (none ? 0 : s.e) * g.b_expert), 2 * g.ldb, cols};
+        const int64_t K = none ? 0 : kPass == 0 ? g.K : g.N;
+        t.Ka = 2 * K;
+        t.Kb = kPass == 0 ? 2 * K : K;
+        t.steps = (int)((K + 63) / 64);
+        t.c_at = s.begin * g.ldc;
+    }
+    t.m0 = (int64_t)kTile * im + (half == 1 ? 128 : 0);
+    t.n0 = (int64_t)kTile * in_;
+    t.mend = half >= 0 ? min(t.m0 + 128, t.A.rows) : t.A.rows;
+    return t.m0 < t.mend;
+}
+
+constexpr int kPart = 128 * 128;  // floats of a partial tile
+
 }  // namespace
 
 template <bool kBig, int kPass, bool kF32>
 __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_grouped(GroupedArgs g)
 {
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLdsBytes];
-    constexpr int kTile = kBig ? 256 : 128;
-    const int64_t cols = kPass == 0 ? g.N : g.K;
-    const int tn = (int)((cols + kTile - 1) / kTile);
-    View A, B;
-    int64_t m0, n0, mend, Ka, Kb, c_at = 0;
-    int steps, im, in_, half;
-    if constexpr (kPass == 2) {
-        int64_t at;
-        const int tm = (int)((g.N + kTile - 1) / kTile);
-        if (!tile_order<kBig>(g.E * tm * tn, g.cus, at, half)) return;
-        const int64_t e = at / (tm * tn);
-        grouped_order((int)(at % (tm * tn)), tm, tn, im, in_);
-        int64_t begin, end;
-        expert_rows(g.ends, e, g.T, begin, end);
-        A = View{reinterpret_cast<const uint8_t*>(g.a + begin * g.lda), 2 * g.lda, g.N};
-        B = View{reinterpret_cast<const uint8_t*>(g.b + begin * g.ldb), 2 * g.ldb, g.K};
-        Ka = Kb = end - begin;
-        steps = (int)((end - begin + 63) / 64);
-        c_at = e * g.c_expert;
-    } else {
-        Slice s;
-        const auto order = [&](int64_t total, int64_t& tile) { return tile_order<kBig>(total, g.cus, tile, half); };
-        if (!find_tile<kTile>(g.ends, g.E, g.T, tn, order, s)) return;
-        grouped_order((int)s.tile, (int)((s.end - s.begin + kTile - 1) / kTile), tn, im, in_);
-        const bool none = s.e >= g.E;  // rows of no expert: zeros
-        A = View{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
-        B = View{reinterpret_cast<const uint8_t*>(g.b + (none ? 0 : s.e) * g.b_expert), 2 * g.ldb, cols};
-        const int64_t K = none ? 0 : kPass == 0 ? g.K : g.N;
-        Ka = 2 * K;
-        Kb = kPass == 0 ? 2 * K : K;
-        steps = (int)((K + 63) / 64);
-        c_at = s.begin * g.ldc;
+    Place t;
+    if (!place_tile<kBig, kPass>(g, blockIdx.x, t)) return;
+    tile<kBig, f32x16_t, kPass == 2, kPass != 0, kF32, kPass == 2>(t.A, t.B, t.m0, t.n0, t.Ka, t.Kb, t.mend, t.steps, lds,
+                                                                   g.c, t.c_at, g.ldc, Plain());
+}
+
+// Few tiles and a long contraction: g.split workgroups per 128 x 128 tile,
+// each over an equal run of the tile's steps, leave fp32 partial tiles in the
+// workspace; k_grouped_join adds them in order.  (Whole -> split, us: wgrad of
+// 16384 tokens and one expert of 1280 x 1280, 100 tiles, 123 -> 75, of 4096
+// and 512 x 512 34.7 -> 24.0; dgrad of 300 tokens, 1280 of 5120, 42.4 -> 21.0;
+// fprop of 128 tokens, 1024 of 4096, 32.7 -> 16.9.  The partial tiles are 64 KB
+// each way for 4 steps of 32 KB or more.)
+template <int kPass>
+__global__ __launch_bounds__(256, 1) void k_grouped_part(GroupedArgs g)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLdsBytes];
+    Place t;
+    if (!place_tile<false, kPass>(g, blockIdx.x / g.split, t)) return;
+    const int part = blockIdx.x % g.split;
+    const int first = (int)((int64_t)t.steps * part / g.split), last = (int)((int64_t)t.steps * (part + 1) / g.split);
+    // a step is 128 bytes of a row, or 64 k rows
+    const auto cut = [&](View& v, int64_t& K, bool k_rows) {
+        const int64_t unit = k_rows ? 64 : 128;
+        v.p += k_rows ? first * unit * v.ld : first * unit;
+        K = min(K, last * unit) - first * unit;
+    };
+    cut(t.A, t.Ka, kPass == 2);
+    cut(t.B, t.Kb, kPass != 0);
+    tile<false, f32x16_t, kPass == 2, kPass != 0, true, false>(t.A, t.B, t.m0, t.n0, t.Ka, t.Kb, t.mend, last - first, lds,
+                                                               g.ws, (t.at * g.split + part) * kPart - t.m0 * 128 - t.n0,
+                                                               128, Plain());
+}
+
+constexpr int kJoinRows = 8;  // rows of a tile that one workgroup joins
+
+template <int kPass, bool kF32>
+__global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs g)
+{
+    Place t;
+    if (!place_tile<false, kPass>(g, blockIdx.x / (128 / kJoinRows), t)) return;
+    const int r = blockIdx.x % (128 / kJoinRows) * kJoinRows + (threadIdx.x >> 5), c = 4 * (threadIdx.x & 31);
+    const int64_t m = t.m0 + r, n = t.n0 + c;
+    if (m >= t.mend || n >= t.B.rows) return;
+    const float* part = g.ws + t.at * g.split * kPart + r * 128 + c;
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < g.split; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)i * kPart);
+        y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
     }
-    m0 = (int64_t)kTile * im + (half == 1 ? 128 : 0);
-    n0 = (int64_t)kTile * in_;
-    mend = half >= 0 ? min(m0 + 128, A.rows) : A.rows;
-    if (m0 >= mend) return;
-    tile<kBig, f32x16_t, kPass == 2, kPass != 0, kF32, kPass == 2>(A, B, m0, n0, Ka, Kb, mend, steps, lds, g.c, c_at, g.ldc,
-                                                                   Plain());
+    store_cols<kF32>(g.c, t.c_at + m * g.ldc + n, n, t.B.rows, y);
 }
 
 template <bool kBig, bool kF32>
@@ -984,7 +1048,7 @@ __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_i8(
     const int tm = (int)((M + kTile - 1) / kTile), tn = (int)((N + kTile - 1) / kTile);
     int64_t at;
     int im, in_, half;
-    if (!tile_order<kBig>((int64_t)tm * tn, cus, at, half)) return;
+    if (!tile_order<kBig>(blockIdx.x, (int64_t)tm * tn, cus, at, half)) return;
     grouped_order((int)at, tm, tn, im, in_);
     const View A{reinterpret_cast<const uint8_t*>(a), lda, M}, B{reinterpret_cast<const uint8_t*>(b), ldb, N};
     const int64_t m0 = (int64_t)kTile * im + (half == 1 ? 128 : 0), n0 = (int64_t)kTile * in_;
@@ -1051,7 +1115,8 @@ enum class Tiles { kThin, kMid, kBig };
 // 21.2 / 26.1, 777 rows - / 43.1 / 36.3, 2048 rows - / 75.5 / 54.4; N = 1024,
 // K = 2048, 256 rows 10.8 / 13.5 / 18.1.
 // thin_grid, mid_grid: their workgroups; a grid holds fewer than 2^32 threads.
-Tiles choose(double traffic, int64_t thin_grid, double mid, int64_t mid_grid, double big, double steps, int cus)
+Tiles choose(double traffic, int64_t thin_grid, double mid, int64_t mid_grid, double big, double steps, int cus,
+             double* time = nullptr)
 {
     constexpr int64_t most = int64_t(1) << 24;  // workgroups of 256 threads
     const double thin = traffic > 0 && thin_grid < most ? 6.0 + traffic / 8.5e6 : 1e30;
@@ -1059,6 +1124,7 @@ Tiles choose(double traffic, int64_t thin_grid, double mid, int64_t mid_grid, do
     const double whole = std::floor(big / cus), rest = big - whole * cus;
     const double b = 1.5 + whole * (9.0 + 1.15 * steps) +
                      (rest == 0 ? 0.0 : 2 * rest <= cus ? 7.0 + (8 * rest <= 3 * cus ? 0.72 : 1.0) * steps : 9.0 + 1.15 * steps);
+    if (time) *time = std::min(thin, std::min(m, b));
     return thin <= m && thin <= b ? Tiles::kThin : m <= b ? Tiles::kMid : Tiles::kBig;
 }
 
@@ -1116,8 +1182,15 @@ void launch_i8_thin(const int8_t* a, int64_t lda, const float* sa, const int8_t*
         hipLaunchKernelGGL((k_i8_thin<kM, false>), grid, dim3(256), 0, s, a, lda, sa, b, ldb, sb, M, N, K, c, ldc);
 }
 
+// How a grouped product is done: its kernel, the rows / 16 of a thin tile, and
+// in how many parts the contraction is taken (1: whole).
+struct Plan {
+    Tiles tiles;
+    int m, split;
+};
+
 template <int kPass>
-void launch_grouped_pass(const GroupedArgs& g, bool out_fp32, hipStream_t s)
+Plan plan_grouped(const GroupedArgs& g)
 {
     const int64_t cols = kPass == 0 ? g.N : g.K;
     const double T = (double)g.T, experts = (double)std::max<int64_t>(1, std::min(g.E, g.T)), each = T / experts;
@@ -1127,21 +1200,62 @@ void launch_grouped_pass(const GroupedArgs& g, bool out_fp32, hipStream_t s)
         return kPass == 2 ? (double)(g.E * ceil_div(g.N, (int64_t)t)) : std::max(experts, T / t + experts / 2);
     };
     const auto tiles = [&](int64_t t) { return row_tiles((double)t) * ceil_div(cols, t); };
-    const double K = kPass == 0 ? (double)g.K : kPass == 1 ? (double)g.N : each;
+    const double K = kPass == 0 ? (double)g.K : kPass == 1 ? (double)g.N : each, steps = std::ceil(K / 64);
+    // (thin: not below 2.4 ns per element of the contraction at 64 rows, its
+    // loads' latency; a workgroup takes the whole of it)
     const double traffic =
-        kPass == 0 ? row_tiles(16.0 * m) * ceil_div(cols, 16) * (std::min(each, 16.0 * m) + 16) * 2 * K : 0.0;
-    const Tiles t = choose(traffic, grouped_grid<kPass>(g, 16 * m, 16 * kThinN), tiles(128),
-                           grouped_grid<kPass>(g, 128, 128), tiles(256), std::ceil(K / 64), g.cus);
-    if (kPass == 0 && t == Tiles::kThin)
-        return m == 1 ? launch_grouped_thin<1>(g, out_fp32, s)
-               : m == 2 ? launch_grouped_thin<2>(g, out_fp32, s) : launch_grouped_thin<4>(g, out_fp32, s);
-    if (t == Tiles::kBig)
+        kPass == 0 ? std::max(row_tiles(16.0 * m) * ceil_div(cols, 16) * (std::min(each, 16.0 * m) + 16) * 2,
+                              0.6e-3 * 8.5e6 * m) * K : 0.0;
+    const int64_t grid = grouped_grid<kPass>(g, 128, 128);
+    double time;
+    const Tiles t = choose(traffic, grouped_grid<kPass>(g, 16 * m, 16 * kThinN), tiles(128), grid, tiles(256), steps, g.cus,
+                           &time);
+    // parts of 4 steps at least, a compute unit for each; 7 us to join them
+    const int split = (int)std::min(std::min(32.0, std::floor((double)g.cus / grid)), std::floor(steps / 4));
+    if (split > 1 && 1.5 + 4.0 + 0.47 * std::ceil(steps / split) + 7.0 < time) return Plan{Tiles::kMid, m, split};
+    return Plan{t, m, 1};
+}
+
+template <int kPass>
+int64_t plan_bytes(const GroupedArgs& g)
+{
+    const int split = plan_grouped<kPass>(g).split;
+    return split > 1 ? grouped_grid<kPass>(g, 128, 128) * split * kPart * (int64_t)sizeof(float) : 0;
+}
+
+template <int kPass>
+void launch_grouped_pass(const GroupedArgs& g0, int64_t ws_bytes, bool out_fp32, hipStream_t s)
+{
+    GroupedArgs g = g0;
+    Plan p = plan_grouped<kPass>(g);
+    const int64_t grid = grouped_grid<kPass>(g, 128, 128);
+    if (p.split > 1 && g.ws && ws_bytes >= plan_bytes<kPass>(g)) {
+        g.split = p.split;
+        hipLaunchKernelGGL(k_grouped_part<kPass>, dim3((uint32_t)(grid * p.split)), dim3(256), 0, s, g);
+        const dim3 join((uint32_t)(grid * (128 / kJoinRows)));
+        if (out_fp32)
+            hipLaunchKernelGGL((k_grouped_join<kPass, true>), join, dim3(256), 0, s, g);
+        else
+            hipLaunchKernelGGL((k_grouped_join<kPass, false>), join, dim3(256), 0, s, g);
+        return;
+    }
+    if (kPass == 0 && p.tiles == Tiles::kThin)
+        return p.m == 1 ? launch_grouped_thin<1>(g, out_fp32, s)
+               : p.m == 2 ? launch_grouped_thin<2>(g, out_fp32, s) : launch_grouped_thin<4>(g, out_fp32, s);
+    if (p.tiles == Tiles::kBig)
         launch_grouped_tiles<true, kPass>(g, out_fp32, s);
     else
         launch_grouped_tiles<false, kPass>(g, out_fp32, s);
 }
 
 }  // namespace
+
+int64_t grouped_workspace(int pass, const GroupedArgs& g)
+{
+    const int64_t rows = pass == 2 ? g.E * g.N : g.T, cols = pass == 0 ? g.N : g.K;
+    if (rows == 0 || cols == 0) return 0;
+    return pass == 0 ? plan_bytes<0>(g) : pass == 1 ? plan_bytes<1>(g) : plan_bytes<2>(g);
+}
 
 void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb, const float* sb,
                     int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, int cus, hipStream_t s)
@@ -1163,13 +1277,13 @@ void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t*
     launch(a, lda, sa, b, ldb, sb, M, N, K, c, ldc, cus, s);
 }
 
-void launch_grouped(int pass, const GroupedArgs& g, bool out_fp32, hipStream_t s)
+void launch_grouped(int pass, const GroupedArgs& g, int64_t ws_bytes, bool out_fp32, hipStream_t s)
 {
     const int64_t rows = pass == 2 ? g.E * g.N : g.T, cols = pass == 0 ? g.N : g.K;
     if (rows == 0 || cols == 0) return;  // (an empty contraction still writes zeros)
-    if (pass == 0) launch_grouped_pass<0>(g, out_fp32, s);
-    else if (pass == 1) launch_grouped_pass<1>(g, out_fp32, s);
-    else launch_grouped_pass<2>(g, out_fp32, s);
+    if (pass == 0) launch_grouped_pass<0>(g, ws_bytes, out_fp32, s);
+    else if (pass == 1) launch_grouped_pass<1>(g, ws_bytes, out_fp32, s);
+    else launch_grouped_pass<2>(g, ws_bytes, out_fp32, s);
 }
 
 }  // namespace nvfp4

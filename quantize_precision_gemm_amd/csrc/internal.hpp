@@ -165,9 +165,14 @@ struct GroupedArgs {
     void* c;
     int64_t ldc, c_expert;
     int cus;             // compute units of the device
+    float* ws;           // workspace of ws_bytes, or null
+    int split;           // parts of the contraction (the launch sets it)
 };
 
-void launch_grouped(int pass, const GroupedArgs& g, bool out_fp32, hipStream_t s);
+// The workspace with which launch_grouped may split the contraction (0: it
+// would not); without one, or with less, it does not split.
+int64_t grouped_workspace(int pass, const GroupedArgs& g);
+void launch_grouped(int pass, const GroupedArgs& g, int64_t ws_bytes, bool out_fp32, hipStream_t s);
 
 // Register-only stream of matrix instructions: `blocks` workgroups of 512
 // threads, `iters` rounds of 64 instructions per wave; operands 0 = fp16

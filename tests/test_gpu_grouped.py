@@ -277,6 +277,72 @@ def test_another_stream_and_a_captured_graph(env):
             assert torch.equal(outs[p], q.nvfp4_bf16_grouped_gemm(p, *ops[p], ends)), f"replay {i} pass {p}"
 
 
+SPLITS = {
+    # rows of each expert, rows behind the last, N, K: few tiles, a long contraction
+    FPROP: [([90, 0, 130], 5, 72, 4104), ([200], 0, 264, 8200), ([140, 3], 0, 1032, 4104)],
+    DGRAD: [([90, 0, 130], 5, 4104, 72), ([200], 0, 8200, 264), ([140, 3], 0, 4104, 1032)],
+    WGRAD: [([4097], 0, 200, 136), ([6000, 0, 1, 2999], 7, 264, 72), ([20, 9000], 300, 8, 1032)],
+}
+
+
+@pytest.mark.parametrize("pass_", [FPROP, DGRAD, WGRAD])
+@pytest.mark.parametrize("case", range(3))
+def test_split_contraction(env, pass_, case):
+    """In parts with the workspace that the query names, whole without one or
+    with too little; the parts' sums do not depend on what the workspace held,
+    and the output's surroundings stay."""
+    torch, q, dev = env
+    rows, tail, N, K = SPLITS[pass_][case]
+    E, T = len(rows), sum(rows) + tail
+    ends = torch.tensor(ends_of(rows), dtype=torch.int32, device=dev)
+    a, b = operands(torch, dev, pass_, T, E, N, K, 60 + case)
+    want, size, C = reference(torch, pass_, a, b, ends_of(rows), E)
+    need = q.nvfp4_bf16_grouped_gemm_workspace(pass_, E, T, N, K)
+    assert need > 0
+    for dt in (torch.float32, torch.bfloat16):
+        results = []
+        for fill, size_ws in ((0, need), (255, need), (255, need + 48), (255, need - 16), (255, 0)):
+            print(f"grouped split pass {pass_} rows {rows} N {N} K {K} {dt} workspace {size_ws}", flush=True)
+            buf = torch.full((size_ws + 64,), fill, dtype=torch.uint8, device=dev)  # 255: NaN
+            shape = list(want.shape)
+            shape[-1] += 12
+            shape[-2] += 2
+            held = torch.full(shape, -7.0, dtype=dt, device=dev)
+            out = held[..., : want.shape[-2], : want.shape[-1]]
+            q.nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out=out, workspace=buf[:size_ws])
+            torch.cuda.synchronize()
+            check(torch, out, want, size, C, f"workspace {size_ws}")
+            mask = torch.ones_like(held, dtype=torch.bool)
+            mask[..., : want.shape[-2], : want.shape[-1]] = False
+            assert (held[mask] == -7.0).all().item(), "written outside the output"
+            assert (buf[size_ws:] == fill).all().item(), "written behind the workspace"
+            assert size_ws >= need or (buf == fill).all().item(), "a workspace that is too small was used"
+            results.append(out.clone())
+        assert torch.equal(results[0], results[1]) and torch.equal(results[0], results[2])
+        assert torch.equal(results[3], results[4])
+        assert torch.equal(results[0], q.nvfp4_bf16_grouped_gemm(pass_, a, b, ends, dt))
+
+
+def test_split_contraction_in_a_captured_graph(env):
+    torch, q, dev = env
+    T, E, N, K = 4096, 2, 136, 72
+    a, b = operands(torch, dev, WGRAD, T, E, N, K, 71)
+    ends = torch.tensor([1000, T], dtype=torch.int32, device=dev)
+    assert q.nvfp4_bf16_grouped_gemm_workspace(WGRAD, E, T, N, K) > 0
+    q.nvfp4_bf16_grouped_gemm(WGRAD, a, b, ends)
+    out = torch.zeros(E, N, K, dtype=torch.bfloat16, device=dev)
+    graph = torch.cuda.CUDAGraph()
+    print("grouped split capture", flush=True)
+    with torch.cuda.graph(graph):
+        q.nvfp4_bf16_grouped_gemm(WGRAD, a, b, ends, out=out)
+    for i in range(3):
+        ends.copy_(torch.tensor([1500 * i, T - 100 * i], dtype=torch.int32, device=dev))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, q.nvfp4_bf16_grouped_gemm(WGRAD, a, b, ends)), f"replay {i}"
+
+
 def test_gradients_are_those_of_the_forward_product(env):
     """dX and dW against central differences of sum(Y * dY): the product is
     linear in each operand, so a step of 1/2 in one element (exact in bf16 for

@@ -23,7 +23,7 @@ def lib():
 
 
 GROUPED = dict(pass_=0, a=FAKE, lda=64, b=FAKE, ldb=64, sb=64 * 32, ends=FAKE, E=4, T=10, N=32, K=64, c=FAKE, ldc=64,
-               sc=64 * 32, dtype=0)
+               sc=64 * 32, dtype=0, ws=None, wb=0)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -37,13 +37,25 @@ GROUPED = dict(pass_=0, a=FAKE, lda=64, b=FAKE, ldb=64, sb=64 * 32, ends=FAKE, E
     ({"pass_": 1, "lda": 24}, -2), ({"pass_": 1, "ldc": 60}, -2),
     ({"pass_": 2, "sc": 64 * 31}, -2), ({"pass_": 2, "sc": 64 * 32 + 2}, -3),
     ({"T": (1 << 31) - 8, "N": 1 << 20, "ldc": 1 << 20, "sb": 1 << 26}, -2),  # more tiles than a grid holds
+    ({"ws": FAKE + 8, "wb": 1 << 20}, -3), ({"ws": FAKE, "wb": -1}, -2),
     ({"lda": 1 << 22}, -2), ({"ldb": 1 << 22, "sb": 1 << 28}, -2),  # rows further apart than 32-bit offsets reach
 ])
 def test_grouped_validation(lib, change, status):
     d = dict(GROUPED, **change)
     got = lib.nvfp4_bf16_grouped_gemm(d["pass_"], d["a"], d["lda"], d["b"], d["ldb"], d["sb"], d["ends"], d["E"], d["T"],
-                                      d["N"], d["K"], d["c"], d["ldc"], d["sc"], d["dtype"], None)
+                                      d["N"], d["K"], d["c"], d["ldc"], d["sc"], d["dtype"], d["ws"], d["wb"], None)
     assert got == status
+
+
+@pytest.mark.parametrize("args,status", [
+    ((0, 4, 10, 32, 64), 0), ((3, 4, 10, 32, 64), -4), ((0, -1, 10, 32, 64), -2), ((0, 4, -1, 32, 64), -2),
+    ((1, 4, 10, 36, 64), -2), ((2, 4, 10, 32, 60), -2), ((2, 0, 0, 0, 0), 0),
+])
+def test_grouped_workspace_query(lib, args, status):
+    n = ctypes.c_int64(-7)
+    assert lib.nvfp4_bf16_grouped_gemm_workspace(*args, ctypes.byref(n)) == status
+    assert (n.value >= 0) if status == 0 else (n.value == -7)
+    assert lib.nvfp4_bf16_grouped_gemm_workspace(*args, None) == -1
 
 
 ADAMW = dict(p=FAKE, g=FAKE, m=FAKE, v=FAKE, m_scale=FAKE, v_scale=FAKE, copy=FAKE, n=10, count=1, pd=1, gd=1, bits=8,

@@ -713,12 +713,11 @@ __device__ __forceinline__ void wide_tile(const View& A, const View& B, int64_t 
     barrier();  // nothing is on its way into LDS or being read any more
 }
 
-// kStream: past the caches (a weight gradient is larger than they are).
 template <bool kStream>
-__device__ __forceinline__ void store16(void* d, uint4 v)
+__device__ __forceinline__ void store16(void* d, uint4 v, bool stream)
 {
     typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-    if constexpr (kStream)
+    if (kStream && stream)
         __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, static_cast<u32x4_t*>(d));
     else
         *static_cast<uint4*>(d) = v;
@@ -729,14 +728,15 @@ __device__ __forceinline__ void store16(void* d, uint4 v)
 // k as a float.  The wave stages 64 rows of 128 bytes in its own 8 KB of LDS
 // (16-byte piece c of row r at c ^ r % 8, and the 8-byte halves of the bf16
 // pieces of every other 8 rows exchanged: the writes, a row per lane, then
-// meet no bank twice within the 128 bytes that the LDS takes at a time) and stores 8 row
-// pieces of 128 bytes at a time.
+// meet no bank twice within the 128 bytes that the LDS takes at a time) and
+// stores 8 row pieces of 128 bytes at a time.
 template <bool kF32, bool kStream, class Value>
 __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const int64_t (&col)[2], int64_t mend, int64_t N,
                                            void* c, int64_t c_at, int64_t ldc, const Value& value)
 {
     const int lane = threadIdx.x & 63, g = lane >> 5;
     const bool wide = (reinterpret_cast<uintptr_t>(c) & 15) == 0 && (kF32 || ((ldc | c_at) & 7) == 0);
+    const bool stream = kStream && ((reinterpret_cast<uintptr_t>(c) | (c_at | ldc) * (kF32 ? 4 : 2)) & 127) == 0;
     constexpr int kUnits = kF32 ? 2 : 1;  // stagings for the 64 columns
     if (row0 >= mend) return;
 #pragma unroll
@@ -774,7 +774,7 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
             if constexpr (kF32) {
                 float* d = static_cast<float*>(c) + at;
                 if (n + 4 <= N) {
-                    store16<kStream>(d, v);
+                    store16<kStream>(d, v, stream);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -783,7 +783,7 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
             } else {
                 uint16_t* d = static_cast<uint16_t*>(c) + at;
                 if (wide && n + 8 <= N) {
-                    store16<kStream>(d, v);
+                    store16<kStream>(d, v, stream);
                 } else {  // rows are 8-byte aligned at least
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -987,7 +987,7 @@ __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_grouped(Grou
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLdsBytes];
     Place t;
     if (!place_tile<kBig, kPass>(g, blockIdx.x, t)) return;
-    tile<kBig, f32x16_t, kPass == 2, kPass != 0, kF32, kPass == 2>(t.A, t.B, t.m0, t.n0, t.Ka, t.Kb, t.mend, t.steps, lds,
+    tile<kBig, f32x16_t, kPass == 2, kPass != 0, kF32, kPass == 2 && kF32>(t.A, t.B, t.m0, t.n0, t.Ka, t.Kb, t.mend, t.steps, lds,
                                                                    g.c, t.c_at, g.ldc, Plain());
 }
 

@@ -8,12 +8,20 @@
 //   wgrad  dW[e, n, k] = sum_{t in e} dY[t, n] X[t, k]
 // Integer product: Y[m, n] = sa[m] sb[n] sum_k a[m, k] b[n, k].
 //
-// v_mfma_f32_16x16x32_bf16 and v_mfma_i32_16x16x64_i8 both take 16 bytes of
-// a row per lane, so one loop serves both types: lane l supplies row l % 16
-// and the 16-byte piece l / 16 of a 64-byte step, and accumulator j of lane l
-// is row 4 (l / 16) + j of the first operand, column l % 16 of the second.
-// The output's columns are passed as the first operand, so that a lane holds
-// 4 neighbouring columns of one output row.
+// The bf16 and the int8 matrix instructions (16 x 16 and 32 x 32 outputs) take
+// 16 bytes of a row per lane and give one accumulator layout, so the loops
+// serve both types: in a 16 x 16 instruction lane l supplies row l % 16 and
+// the 16-byte piece l / 16 of 64 bytes, and accumulator j of lane l is row
+// 4 (l / 16) + j of the first operand, column l % 16 of the second; in a
+// 32 x 32 one row l % 32 and piece l / 32 of 32 bytes, and accumulator j is
+// row 8 (j / 4) + 4 (l / 32) + j % 4, column l % 32.  The output's columns are
+// passed as the first operand, so that a lane holds 4 neighbouring columns of
+// one output row.
+//
+// Three kernels, chosen from estimates of their time (see choose()): thin
+// tiles (few rows, bound by the weights' bytes), 128 x 128 tiles (fewer of
+// them than compute units: bound by latency, with their contraction split
+// when it is long) and 256 x 256 tiles (bound by the matrix and LDS pipes).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -894,10 +902,11 @@ __device__ __forceinline__ bool xcd_order(int64_t hw, int64_t total, int64_t& at
     return hw < total;
 }
 
-// The hw-th tile of `total`, and which of its row halves (-1: both).  Whole rounds of one tile per compute unit come first, each round
-// dealt so that an XCD gets neighbouring tiles of it (dealt over all rounds
-// at once, the XCD of the largest experts would finish last: 468 against
-// 354 us for a wgrad of 16 uneven experts, 8192 x 2560 x 5120).  If what
+// The hw-th tile of `total`, and which of its row halves (-1: both).  Whole
+// rounds of one tile per compute unit come first, each round dealt so that an
+// XCD gets neighbouring tiles of it (dealt over all rounds at once, the XCD of
+// the largest experts would finish last: 468 against 354 us for a wgrad of 16
+// uneven experts, 8192 x 2560 x 5120).  If what
 // remains is at most half the compute units, its tiles are done as two halves
 // of 128 rows each (a step of up to 160 halves takes 0.71 us, of 256 about
 // 1.0, a whole tile's 1.15 to 1.6).

@@ -690,10 +690,23 @@ def _pitch(x, multiple=8):
     return x.stride(0) if rows > 1 and cols > 0 else _round_up(cols, multiple)
 
 
-def _for_stream(t, stream):
-    """A tensor made here for work on `stream` keeps its memory until that work is done."""
-    if stream is not None:
-        t.record_stream(stream)
+def _empty(shape, dtype, device, stream, strides=None):
+    """A tensor made here for work on `stream`: from that stream's memory, which
+    no unfinished work of the current one can still use, and not reused before
+    what the current one does with it is done."""
+    if strides is not None:
+        def make():
+            return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    else:
+        def make():
+            return torch.empty(shape, dtype=dtype, device=device)
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    current = torch.cuda.current_stream(device)
+    if current != stream:
+        t.record_stream(current)
     return t
 
 
@@ -760,7 +773,7 @@ def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=Non
     stride_c = 0
     if out is None:
         code = _out_code(out_dtype)
-        out = _for_stream(torch.empty(shape, dtype=out_dtype, device=a.device), stream)
+        out = _empty(shape, out_dtype, a.device, stream)
         ldc = shape[-1]
         stride_c = N * K
     elif pass_ == WGRAD:
@@ -782,7 +795,7 @@ def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=Non
     elif (T if pass_ == WGRAD else a_cols) >= _SPLIT_FROM:
         need = nvfp4_bf16_grouped_gemm_workspace(pass_, E, T, N, K)
         if need:
-            workspace = _for_stream(torch.empty(need, dtype=torch.uint8, device=a.device), stream)
+            workspace = _empty(need, torch.uint8, a.device, stream)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     st = load_library().nvfp4_bf16_grouped_gemm(pass_, a.data_ptr(), _pitch(a), b.data_ptr(), ldb, stride_b,
                                                 ends.data_ptr(), E, T, N, K, out.data_ptr(), ldc, stride_c, code,
@@ -944,8 +957,8 @@ def nvfp4_i8_quantize(x, out=None, stream=None):
     _check_bf16(x)
     rows, cols = x.shape
     if out is None:
-        codes = _for_stream(torch.empty((rows, cols), dtype=torch.int8, device=x.device), stream)
-        scales = _for_stream(torch.empty(rows, dtype=torch.float32, device=x.device), stream)
+        codes = _empty((rows, cols), torch.int8, x.device, stream)
+        scales = _empty(rows, torch.float32, x.device, stream)
         out = I8Tensor(codes, scales)
     else:
         codes, scales = _check_i8(out, "out")
@@ -972,7 +985,7 @@ def nvfp4_i8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
     if out is None:
         code = _out_code(out_dtype)
         ldc = _round_up(N, 4)  # (the ABI's rule)
-        out = _for_stream(torch.empty_strided((M, N), (ldc, 1), dtype=out_dtype, device=ac.device), stream)
+        out = _empty((M, N), out_dtype, ac.device, stream, (ldc, 1))
     else:
         _check_gemm_out(out, (M, N), ac.device)
         code = _out_code(out.dtype)

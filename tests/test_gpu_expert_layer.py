@@ -61,3 +61,43 @@ def test_training_learns_the_maps(env, bits):
     bf16 = q.nvfp4_bf16_grouped_gemm(q.FPROP, x, master.bfloat16(), ends, torch.float32)
     int8 = ex.answer_in_int8(master, x, ends)
     assert ((int8 - bf16).norm() / bf16.norm()).item() < 0.02
+
+
+@pytest.mark.parametrize("what", ["grouped", "split", "quantize", "int8"])
+def test_outputs_made_for_another_stream_are_its_own(env, what):
+    """Memory freed on the current stream, where work on it is still waiting,
+    is not given to a call on another stream."""
+    torch, q, _ = env
+    dev = torch.device("cuda:0")
+    T, E, N, K = (4096, 1, 256, 128) if what == "split" else (512, 2, 256, 128)
+    x = torch.randn(T, K, device=dev).bfloat16()
+    dy = torch.randn(T, N, device=dev).bfloat16()
+    ends = torch.tensor([T] * E, dtype=torch.int32, device=dev)
+    xq, wq = q.nvfp4_i8_quantize(x), q.nvfp4_i8_quantize(dy[:N, :K].contiguous())
+    if what == "split":
+        assert q.nvfp4_bf16_grouped_gemm_workspace(q.WGRAD, E, T, N, K) > 0
+
+    def call(stream):
+        if what in ("grouped", "split"):
+            return [q.nvfp4_bf16_grouped_gemm(q.WGRAD, dy, x, ends, torch.float32, stream=stream)]
+        if what == "quantize":
+            t = q.nvfp4_i8_quantize(x, stream=stream)
+            return [t.codes, t.scales]
+        return [q.nvfp4_i8_gemm(xq, wq, torch.float32, stream=stream)]
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    sizes = [t.numel() * t.element_size() for t in want]
+    if what == "split":
+        sizes.append(q.nvfp4_bf16_grouped_gemm_workspace(q.WGRAD, E, T, N, K))
+    print(f"another stream: {what} {sizes}", flush=True)
+    held = [torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes]
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    for t in held:
+        t.fill_(255)
+    del held, t
+    got = call(side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

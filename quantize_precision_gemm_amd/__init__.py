@@ -710,6 +710,14 @@ def _empty(shape, dtype, device, stream, strides=None):
     return t
 
 
+def _used_on(stream, *tensors):
+    """The caller may drop these before the work on `stream` has read them."""
+    if stream != torch.cuda.current_stream(tensors[0].device):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _check_bf16_experts(w, what):
     if not (isinstance(w, torch.Tensor) and w.is_cuda and w.dtype == torch.bfloat16 and w.dim() == 3):
         raise TypeError(f"{what}: expected a 3-D bfloat16 CUDA tensor (experts, rows, columns)")
@@ -800,6 +808,8 @@ def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=Non
     st = load_library().nvfp4_bf16_grouped_gemm(pass_, a.data_ptr(), _pitch(a), b.data_ptr(), ldb, stride_b,
                                                 ends.data_ptr(), E, T, N, K, out.data_ptr(), ldc, stride_c, code,
                                                 ws, ws_bytes, _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, a, b, ends, out, workspace)
     if st:
         _check(st, "nvfp4_bf16_grouped_gemm")
     return out
@@ -904,6 +914,7 @@ def nvfp4_adamw(group, step, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0
 
     step counts from 1; grad_scale: optional one-element float32 device tensor
     that every gradient is multiplied by (not finite: the step writes nothing).
+    With `stream`, the group and grad_scale have to live until the step is done.
     """
     if not isinstance(group, AdamWGroup):
         raise TypeError("group: expected an AdamWGroup")
@@ -968,6 +979,8 @@ def nvfp4_i8_quantize(x, out=None, stream=None):
             raise ValueError(f"out: on {codes.device}, expected {x.device}")
     st = load_library().nvfp4_i8_quantize(x.data_ptr(), rows, cols, _pitch(x), codes.data_ptr(), _pitch(codes, 16),
                                           scales.data_ptr(), _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, x, codes, scales)
     if st:
         _check(st, "nvfp4_i8_quantize")
     return out
@@ -992,6 +1005,8 @@ def nvfp4_i8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
         ldc = _pitch(out, 4)
     st = load_library().nvfp4_i8_gemm(ac.data_ptr(), _pitch(ac, 16), sa.data_ptr(), bc.data_ptr(), _pitch(bc, 16),
                                       sb.data_ptr(), M, N, K, out.data_ptr(), ldc, code, _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, ac, sa, bc, sb, out)
     if st:
         _check(st, "nvfp4_i8_gemm")
     return out

@@ -101,3 +101,34 @@ def test_outputs_made_for_another_stream_are_its_own(env, what):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_inputs_dropped_before_another_stream_has_read_them(env):
+    """Inputs that are freed and overwritten on the current stream while the
+    work that reads them waits on another one."""
+    torch, q, _ = env
+    dev = torch.device("cuda:0")
+    T, E, N, K = 512, 2, 256, 128
+    x, dy = torch.randn(T, K, device=dev).bfloat16(), torch.randn(T, N, device=dev).bfloat16()
+    ends = torch.tensor([100, T], dtype=torch.int32, device=dev)
+    w = q.nvfp4_i8_quantize(dy[:N, :K].contiguous())
+    want = [q.nvfp4_bf16_grouped_gemm(q.WGRAD, dy, x, ends), q.nvfp4_i8_gemm(q.nvfp4_i8_quantize(x), w)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for which in range(2):
+        print(f"inputs dropped {which}", flush=True)
+        torch.cuda.empty_cache()
+        copies = [t.clone() for t in (x, dy, ends)]
+        sizes = [t.numel() * t.element_size() for t in copies]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+        if which == 0:
+            got = q.nvfp4_bf16_grouped_gemm(q.WGRAD, copies[1], copies[0], copies[2], stream=side)
+        else:
+            got = q.nvfp4_i8_gemm(q.nvfp4_i8_quantize(copies[0], stream=side), w, stream=side)
+        del copies
+        over = [torch.zeros(n, dtype=torch.uint8, device=dev) for n in sizes]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want[which])
+        del over

@@ -581,6 +581,16 @@ typedef struct nvfp4_adamw_tensor {
 } nvfp4_adamw_tensor;
 
 /*
+ * nvfp4_adamw_table -- host function: writes the table of a list of tensors
+ * that nvfp4_adamw reads, which is copied to the device once for all steps.
+ * *bytes: its size (0: the step takes none; 48 tensors travel in a launch's
+ * arguments, and a few more large ones are as fast so).  table: HOST memory of table_bytes, 8-byte aligned, or
+ * NULL to ask for the size alone; NVFP4_ERR_WORKSPACE if it is too small.
+ */
+int nvfp4_adamw_table(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t p_dtype, int32_t g_dtype,
+                      int32_t state_bits, void* table, int64_t table_bytes, int64_t* bytes);
+
+/*
  * nvfp4_adamw -- one step of AdamW over `count` tensors, in place:
  *   g' = g * grad_scale
  *   m  = beta1 m + (1 - beta1) g'
@@ -607,6 +617,10 @@ typedef struct nvfp4_adamw_tensor {
  *   grad_scale  optional device float that every gradient is multiplied by
  *               (clipping, loss scaling).  If it is not finite the step
  *               writes nothing.
+ *   table       optional device copy (8-byte aligned) of what
+ *               nvfp4_adamw_table wrote for the same arguments (if that was
+ *               anything): the tensors are then updated by one launch instead
+ *               of one for every 48, with the same results.
  * A gradient that is not finite makes its own element NaN (in 8 bits its
  * block's scale too grows to its largest).  Pointers need the alignment of
  * their type; with 16 bytes for fp32, 8 for bf16 and 4 for codes the wide
@@ -616,7 +630,7 @@ typedef struct nvfp4_adamw_tensor {
  */
 int nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t p_dtype, int32_t g_dtype,
                 int32_t state_bits, int64_t step, double lr, double beta1, double beta2, double eps,
-                double weight_decay, const float* grad_scale, void* stream);
+                double weight_decay, const float* grad_scale, const void* table, void* stream);
 
 /*
  * nvfp4_i8_quantize -- symmetric 8-bit integer quantisation of the rows of a

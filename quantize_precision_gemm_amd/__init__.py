@@ -130,7 +130,9 @@ def load_library():
         L.nvfp4_bf16_grouped_gemm_workspace.argtypes = [i32, i64, i64, i64, i64, ctypes.POINTER(i64)]
         L.nvfp4_bf16_grouped_gemm_workspace.restype = ctypes.c_int
         f64 = ctypes.c_double
-        L.nvfp4_adamw.argtypes = [P, i64, i32, i32, i32, i64, f64, f64, f64, f64, f64, P, P]
+        L.nvfp4_adamw_table.argtypes = [P, i64, i32, i32, i32, P, i64, ctypes.POINTER(i64)]
+        L.nvfp4_adamw_table.restype = ctypes.c_int
+        L.nvfp4_adamw.argtypes = [P, i64, i32, i32, i32, i64, f64, f64, f64, f64, f64, P, P, P]
         L.nvfp4_adamw.restype = ctypes.c_int
         L.nvfp4_i8_quantize.argtypes = [P, i64, i64, i64, P, i64, P, P]
         L.nvfp4_i8_quantize.restype = ctypes.c_int
@@ -877,6 +879,18 @@ class AdamWGroup:
         if len(set(seen)) != len(seen):
             raise ValueError("params: the same tensor twice in one group")
         self.count = k
+        self._device_table = self._make_device_table()
+
+    def _make_device_table(self):
+        """What nvfp4_adamw_table writes, on the device; None: the step needs no table."""
+        L, need = load_library(), ctypes.c_int64(0)
+        args = (self._table, self.count, self.p_dtype, self.g_dtype, self.bits)
+        _check(L.nvfp4_adamw_table(*args, None, 0, ctypes.byref(need)), "nvfp4_adamw_table")
+        if not need.value:
+            return None
+        host = torch.empty(need.value // 8, dtype=torch.int64)
+        _check(L.nvfp4_adamw_table(*args, host.data_ptr(), need.value, ctypes.byref(need)), "nvfp4_adamw_table")
+        return host.to(self.device)
 
     def _check_tensor(self, what, i, t, dtype, count):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -926,8 +940,10 @@ def nvfp4_adamw(group, step, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0
         grad_scale = grad_scale.data_ptr()
     if group.count == 0:
         return
+    table = group._device_table
     st = load_library().nvfp4_adamw(group._table, group.count, group.p_dtype, group.g_dtype, group.bits, step, lr,
-                                    beta1, beta2, eps, weight_decay, grad_scale, _raw_stream(stream))
+                                    beta1, beta2, eps, weight_decay, grad_scale,
+                                    table.data_ptr() if table is not None else None, _raw_stream(stream))
     if st:
         _check(st, "nvfp4_adamw")
 

@@ -20,6 +20,8 @@
 // launch moves more than the last-level cache holds twice (512 MB): 139.8M
 // elements in 32 bits 747 -> 693 us (6.05 TB/s), 106.2M in 8 bits 328 -> 311 us
 // (6.2 TB/s); of 405 MB that the cache does hold, such loads cost 9 us of 58.
+#include <type_traits>
+
 #include "internal.hpp"
 #include "nvfp4_device.hpp"
 
@@ -179,26 +181,21 @@ __device__ __forceinline__ uint32_t encode4(const float (&y)[4], float& scale)
     return (uint32_t)w;
 }
 
-}  // namespace
-
-// One workgroup updates one chunk of 1024 elements of one tensor; the tensor
-// is found from the first chunk of each, held in the kernel's arguments.
-template <class P, class G, bool k8, bool kStream>
-__global__ __launch_bounds__(kThreads) void k_adamw(AdamWArgs a)
+// The factor of the gradients; false: it is not finite, the step is left out.
+__device__ __forceinline__ bool gradient_scale(const AdamWStep& a, float& gs)
 {
-    float gs = 1.0f;
-    if (a.grad_scale) {
-        gs = *a.grad_scale;
-        if ((__float_as_uint(gs) & 0x7F800000u) == 0x7F800000u) return;  // not finite: the step is left out
-    }
+    gs = a.grad_scale ? *a.grad_scale : 1.0f;
+    return (__float_as_uint(gs) & 0x7F800000u) != 0x7F800000u;
+}
+
+// A workgroup's 1024 elements, the chunk-th of tensor t.
+template <class P, class G, bool k8, bool kStream>
+__device__ __forceinline__ void update(const AdamWStep& a, float gs, const AdamWTensor& t, uint32_t chunk)
+{
     const int lane = threadIdx.x & 63;
-    const uint32_t mine = a.first[min(lane, a.count)];
-    const int at = __builtin_amdgcn_readfirstlane(
-        (int)__popcll(__ballot(lane < a.count && mine <= blockIdx.x)) - 1);
-    const AdamWTensor t = a.t[at];
     const int64_t n = t.n;
     const bool vec = t.vec != 0;
-    const int64_t i = (int64_t)(blockIdx.x - a.first[at]) * kChunk + 4 * threadIdx.x;
+    const int64_t i = (int64_t)chunk * kChunk + 4 * threadIdx.x;
 
     float p[4], g[4], m[4], v[4], r[4];
     load4<kStream>(p, t.p, i, n, vec, P());
@@ -240,23 +237,71 @@ __global__ __launch_bounds__(kThreads) void k_adamw(AdamWArgs a)
     }
 }
 
+}  // namespace
+
+// One workgroup updates one chunk of one tensor; the tensor is found from the
+// first chunk of each, held in the kernel's arguments.
+template <class P, class G, bool k8, bool kStream>
+__global__ __launch_bounds__(kThreads) void k_adamw(AdamWArgs a)
+{
+    float gs;
+    if (!gradient_scale(a.step, gs)) return;
+    const int lane = threadIdx.x & 63;
+    const uint32_t mine = a.first[min(lane, a.count)];
+    const int at = __builtin_amdgcn_readfirstlane(
+        (int)__popcll(__ballot(lane < a.count && mine <= blockIdx.x)) - 1);
+    update<P, G, k8, kStream>(a.step, gs, a.t[at], blockIdx.x - a.first[at]);
+}
+
+// The same for more tensors than the arguments hold, in one launch (96 small
+// tensors 8.5 -> 4.9 us, 1000 of 100000 elements 626 -> 443).  The wave looks at 64 tensors, evenly
+// spaced, at a time (96 tensors: twice, 4097: three times).
+template <class P, class G, bool k8, bool kStream>
+__global__ __launch_bounds__(kThreads) void k_adamw_table(AdamWStep step, const AdamWTensor* __restrict__ t,
+                                                          const uint32_t* __restrict__ first, int count)
+{
+    float gs;
+    if (!gradient_scale(step, gs)) return;
+    const int lane = threadIdx.x & 63;
+    int at = 0;  // the chunk's tensor is one of at .. at + len - 1
+    for (int len = count; len > 1;) {
+        const int stride = (len + 63) / 64, off = lane * stride;
+        const bool past = off < len && first[at + off] <= blockIdx.x;
+        const int k = (__builtin_amdgcn_readfirstlane((int)__popcll(__ballot(past))) - 1) * stride;
+        at += k;
+        len = min(stride, len - k);
+    }
+    update<P, G, k8, kStream>(step, gs, t[at], blockIdx.x - first[at]);
+}
+
 namespace {
 
-template <class P, class G, bool k8>
-void launch_bits(const AdamWArgs& a, uint32_t chunks, hipStream_t s)
+// launch(kernel's types): the update past the caches if it moves more than they hold.
+template <class P, class G, bool k8, class Launch>
+void launch_bits(uint32_t chunks, const Launch& launch)
 {
     const int64_t bytes = 2 * sizeof(P) + sizeof(G) + (k8 ? 4 : 16);
     if ((int64_t)chunks * kChunk * bytes > (int64_t)512 << 20)
-        hipLaunchKernelGGL((k_adamw<P, G, k8, true>), dim3(chunks), dim3(kThreads), 0, s, a);
+        launch(P(), G(), std::integral_constant<bool, k8>(), std::true_type());
     else
-        hipLaunchKernelGGL((k_adamw<P, G, k8, false>), dim3(chunks), dim3(kThreads), 0, s, a);
+        launch(P(), G(), std::integral_constant<bool, k8>(), std::false_type());
 }
 
-template <class P, class G>
-void launch_types(const AdamWArgs& a, uint32_t chunks, bool eight, hipStream_t s)
+template <class P, class G, class Launch>
+void launch_types(uint32_t chunks, bool eight, const Launch& launch)
 {
-    if (eight) launch_bits<P, G, true>(a, chunks, s);
-    else launch_bits<P, G, false>(a, chunks, s);
+    if (eight) launch_bits<P, G, true>(chunks, launch);
+    else launch_bits<P, G, false>(chunks, launch);
+}
+
+template <class Launch>
+void launch_kind(uint32_t chunks, bool p_bf16, bool g_bf16, bool eight, const Launch& launch)
+{
+    if (chunks == 0) return;
+    if (p_bf16 && g_bf16) launch_types<uint16_t, uint16_t>(chunks, eight, launch);
+    else if (p_bf16) launch_types<uint16_t, float>(chunks, eight, launch);
+    else if (g_bf16) launch_types<float, uint16_t>(chunks, eight, launch);
+    else launch_types<float, float>(chunks, eight, launch);
 }
 
 }  // namespace
@@ -266,11 +311,19 @@ int64_t adamw_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
 void launch_adamw(const AdamWArgs& a, bool p_bf16, bool g_bf16, bool eight, hipStream_t s)
 {
     const uint32_t chunks = a.first[a.count];
-    if (chunks == 0) return;
-    if (p_bf16 && g_bf16) launch_types<uint16_t, uint16_t>(a, chunks, eight, s);
-    else if (p_bf16) launch_types<uint16_t, float>(a, chunks, eight, s);
-    else if (g_bf16) launch_types<float, uint16_t>(a, chunks, eight, s);
-    else launch_types<float, float>(a, chunks, eight, s);
+    launch_kind(chunks, p_bf16, g_bf16, eight, [&](auto p, auto g, auto k8, auto stream) {
+        hipLaunchKernelGGL((k_adamw<decltype(p), decltype(g), decltype(k8)::value, decltype(stream)::value>), dim3(chunks),
+                           dim3(kThreads), 0, s, a);
+    });
+}
+
+void launch_adamw_table(const AdamWStep& step, const AdamWTensor* t, const uint32_t* first, int64_t count,
+                        uint32_t chunks, bool p_bf16, bool g_bf16, bool eight, hipStream_t s)
+{
+    launch_kind(chunks, p_bf16, g_bf16, eight, [&](auto p, auto g, auto k8, auto stream) {
+        hipLaunchKernelGGL((k_adamw_table<decltype(p), decltype(g), decltype(k8)::value, decltype(stream)::value>),
+                           dim3(chunks), dim3(kThreads), 0, s, step, t, first, (int)count);
+    });
 }
 
 }  // namespace nvfp4

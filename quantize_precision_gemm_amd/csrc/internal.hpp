@@ -116,7 +116,7 @@ void launch_bf16_gemm(const uint16_t* a, int64_t lda, bool a_t, const uint16_t* 
                       bool out_fp32, hipStream_t s);
 
 // ---- AdamW ----
-constexpr int kAdamWTensors = 48;  // tensors of one launch (they travel in its arguments)
+constexpr int kAdamWTensors = 48;  // tensors that travel in the arguments of a launch
 
 struct AdamWTensor {
     void* p;
@@ -130,17 +130,25 @@ struct AdamWTensor {
     int64_t vec;     // every pointer suits accesses of 4 elements
 };
 
+struct AdamWStep {
+    float beta1, rest1, beta2, rest2;  // rest: 1 - beta
+    float keep, rate, root_corr, eps;  // 1 - lr decay, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+    const float* grad_scale;           // or null
+};
+
 struct AdamWArgs {
+    AdamWStep step;
     AdamWTensor t[kAdamWTensors];
     uint32_t first[kAdamWTensors + 1];  // first workgroup of each tensor; [count]: all of them
     int count;
-    float beta1, rest1, beta2, rest2;   // rest: 1 - beta
-    float keep, rate, root_corr, eps;   // 1 - lr decay, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
-    const float* grad_scale;            // or null
 };
 
 int64_t adamw_chunks(int64_t n);  // workgroups for a tensor of n elements
 void launch_adamw(const AdamWArgs& a, bool p_bf16, bool g_bf16, bool eight, hipStream_t s);
+// The same for any number of tensors, whose table lies in device memory;
+// first[count] = chunks.
+void launch_adamw_table(const AdamWStep& step, const AdamWTensor* t, const uint32_t* first, int64_t count,
+                        uint32_t chunks, bool p_bf16, bool g_bf16, bool eight, hipStream_t s);
 
 // ---- 8-bit integers ----
 void launch_i8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int8_t* codes, int64_t ld_codes,

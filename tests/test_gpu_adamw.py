@@ -311,6 +311,56 @@ def test_extreme_gradients(env):
         assert torch.isfinite(grp.v[0].float()).all().item()
 
 
+@pytest.mark.parametrize("p_dtype,g_dtype", [("float32", "bfloat16"), ("bfloat16", "float32"),
+                                             ("bfloat16", "bfloat16"), ("float32", "float32")])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("count", [49, 65, 128, 129, 4099])
+def test_table_equals_launches_of_a_few(env, p_dtype, g_dtype, bits, count):
+    """One launch from the device table, each tensor as in a group of few."""
+    torch, q, dev = env
+    sizes = [(613 * i) % 2111 for i in range(count)]  # (the first is empty)
+    d = tensors(torch, dev, sizes, getattr(torch, p_dtype), getattr(torch, g_dtype), bits, p_dtype == "float32", 6)
+    few = clone(d)
+    print(f"adamw table {count} {p_dtype} {g_dtype} {bits}", flush=True)
+    whole = q.AdamWGroup(**d)
+    assert (whole._device_table is not None) == (count > 49)
+    q.nvfp4_adamw(whole, 2, **HYPER)
+    for i in range(0, count, 40):
+        q.nvfp4_adamw(q.AdamWGroup(**{k: None if v is None else v[i:i + 40] for k, v in few.items()}), 2, **HYPER)
+    torch.cuda.synchronize()
+    for k, v in d.items():
+        if v is not None:
+            for i, t in enumerate(v):
+                assert t is None or torch.equal(t.view(torch.uint8), few[k][i].view(torch.uint8)), f"{k} of tensor {i}"
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_table_of_large_tensors_and_a_captured_graph(env, bits):
+    torch, q, dev = env
+    count = 49 if bits == 32 else 98
+    sizes = [1_000_003 if bits == 32 else 400_003] * count
+    d = tensors(torch, dev, sizes, torch.float32, torch.float32, bits, False, 7)
+    few = clone(d)
+    print(f"adamw large table {bits}", flush=True)
+    whole, parts = q.AdamWGroup(**d), [q.AdamWGroup(**{k: None if v is None else v[i:i + 7] for k, v in few.items()})
+                                       for i in range(0, count, 7)]
+    assert whole._device_table is not None
+    q.nvfp4_adamw(whole, 1, **HYPER)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.nvfp4_adamw(whole, 2, **HYPER)
+    for p in parts:
+        q.nvfp4_adamw(p, 1, **HYPER)
+    for i in range(3):
+        graph.replay()
+        for p in parts:
+            q.nvfp4_adamw(p, 2, **HYPER)
+        torch.cuda.synchronize()
+        for k in ("params", "m", "v"):
+            for a, b in zip(d[k], few[k]):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), f"replay {i}: {k}"
+
+
 def test_another_stream_and_a_captured_graph(env):
     torch, q, dev = env
     for bits in (32, 8):

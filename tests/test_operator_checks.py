@@ -5,6 +5,7 @@ dereferenced, no compute call is made."""
 import ctypes
 import os
 
+import numpy as np
 import pytest
 import torch
 
@@ -59,7 +60,7 @@ def test_grouped_workspace_query(lib, args, status):
 
 
 ADAMW = dict(p=FAKE, g=FAKE, m=FAKE, v=FAKE, m_scale=FAKE, v_scale=FAKE, copy=FAKE, n=10, count=1, pd=1, gd=1, bits=8,
-             step=1, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, wd=0.1, gs=FAKE)
+             step=1, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, wd=0.1, gs=FAKE, table=None)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -71,6 +72,7 @@ ADAMW = dict(p=FAKE, g=FAKE, m=FAKE, v=FAKE, m_scale=FAKE, v_scale=FAKE, copy=FA
     ({"pd": 0}, -4),  # a copy of bf16 parameters
     ({"p": FAKE + 2}, -3), ({"g": FAKE + 2}, -3), ({"copy": FAKE + 1}, -3), ({"m_scale": FAKE + 2}, -3),
     ({"m": FAKE + 2, "bits": 32}, -3), ({"v": FAKE + 1, "bits": 32}, -3), ({"gs": FAKE + 2}, -3),
+    ({"table": FAKE + 4}, -3),
     ({"n": 1 << 60}, -2), ({"n": (1 << 33) + 1}, -2),
 ])
 def test_adamw_validation(lib, change, status):
@@ -79,12 +81,41 @@ def test_adamw_validation(lib, change, status):
     for k in ("p", "g", "m", "v", "m_scale", "v_scale", "copy", "n"):
         setattr(t[0], k, d[k])
     got = lib.nvfp4_adamw(t, d["count"], d["pd"], d["gd"], d["bits"], d["step"], d["lr"], d["b1"], d["b2"], d["eps"],
-                          d["wd"], d["gs"], None)
+                          d["wd"], d["gs"], d["table"], None)
     assert got == status
 
 
+def test_adamw_table(lib):
+    """The size, the entries (those with elements) and their first chunks, and its refusals."""
+    k = 61
+    t = (q._AdamWTensor * k)()
+    for i in range(k):
+        t[i].n = 0 if i in (0, 7) else 700 * i
+        t[i].p = t[i].g = t[i].m = t[i].v = FAKE + 4096 * i
+    n = ctypes.c_int64(-7)
+    args = (t, k, 1, 1, 32)
+    assert lib.nvfp4_adamw_table(*args, None, 0, None) == -1
+    assert lib.nvfp4_adamw_table(None, k, 1, 1, 32, None, 0, ctypes.byref(n)) == -1 and n.value == -7
+    assert lib.nvfp4_adamw_table(t, k, 1, 1, 16, None, 0, ctypes.byref(n)) == -4 and n.value == -7
+    assert lib.nvfp4_adamw_table(t, 48, 1, 1, 32, None, 0, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.nvfp4_adamw_table(*args, None, 0, ctypes.byref(n)) == 0 and n.value == -(-59 * 76 // 8) * 8
+    buf = np.full(n.value // 8 + 1, -1, dtype=np.int64)
+    assert buf.ctypes.data % 8 == 0
+    assert lib.nvfp4_adamw_table(*args, buf.ctypes.data, n.value - 8, ctypes.byref(n)) == -7
+    assert lib.nvfp4_adamw_table(*args, buf.ctypes.data + 4, n.value, ctypes.byref(n)) == -3
+    assert (buf == -1).all()
+    assert lib.nvfp4_adamw_table(*args, buf.ctypes.data, n.value, ctypes.byref(n)) == 0
+    entries, first = buf[:59 * 9].reshape(59, 9), buf[59 * 9:].view(np.int32)
+    used = [i for i in range(k) if t[i].n]
+    chunk = 0
+    for row, i in enumerate(used):
+        assert entries[row, 0] == t[i].p and entries[row, 7] == t[i].n and first[row] == chunk
+        chunk += -(-t[i].n // 1024)
+    assert buf[-1] == -1
+
+
 def test_adamw_null_table_and_empty_calls(lib):
-    args = (1, 1, 32, 1, 1e-3, 0.9, 0.99, 1e-8, 0.0, None, None)
+    args = (1, 1, 32, 1, 1e-3, 0.9, 0.99, 1e-8, 0.0, None, None, None)
     assert lib.nvfp4_adamw(None, 1, *args) == -1
     t = (q._AdamWTensor * 3)()  # tensors of no elements need no pointers and launch nothing
     assert lib.nvfp4_adamw(t, 3, *args) in (0, -6)  # (-6: no GPU in this process)

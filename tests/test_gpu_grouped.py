@@ -323,6 +323,20 @@ def test_split_contraction(env, pass_, case):
         assert torch.equal(results[0], q.nvfp4_bf16_grouped_gemm(pass_, a, b, ends, dt))
 
 
+def test_refuses_workspaces_that_do_not_fit(env):
+    torch, q, dev = env
+    a, b = operands(torch, dev, WGRAD, 2048, 1, 64, 64, 72)
+    ends = torch.tensor([2048], dtype=torch.int32, device=dev)
+    for bad in (torch.empty(1 << 20), torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 18, device=dev),
+                torch.empty(2, 1 << 19, dtype=torch.uint8, device=dev)):
+        with pytest.raises(ValueError):
+            q.nvfp4_bf16_grouped_gemm(WGRAD, a, b, ends, workspace=bad)
+    with pytest.raises(TypeError):
+        q.nvfp4_bf16_grouped_gemm(WGRAD, a, b, ends, workspace=1 << 20)
+    with pytest.raises(RuntimeError):
+        q.nvfp4_bf16_grouped_gemm(WGRAD, a, b, ends, workspace=torch.empty(1 << 20, dtype=torch.uint8, device=dev)[8:])
+
+
 def test_split_contraction_in_a_captured_graph(env):
     torch, q, dev = env
     T, E, N, K = 4096, 2, 136, 72

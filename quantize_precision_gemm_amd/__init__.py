@@ -696,16 +696,12 @@ def _empty(shape, dtype, device, stream, strides=None):
     """A tensor made here for work on `stream`: from that stream's memory, which
     no unfinished work of the current one can still use, and not reused before
     what the current one does with it is done."""
-    if strides is not None:
-        def make():
-            return torch.empty_strided(shape, strides, dtype=dtype, device=device)
-    else:
-        def make():
-            return torch.empty(shape, dtype=dtype, device=device)
     if stream is None:
-        return make()
+        if strides is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        t = make()
+        t = _empty(shape, dtype, device, None, strides)
     current = torch.cuda.current_stream(device)
     if current != stream:
         t.record_stream(current)
@@ -967,15 +963,17 @@ def _check_i8(t, what):
     c, s = t.codes, t.scales
     if not (isinstance(c, torch.Tensor) and c.is_cuda and c.dtype == torch.int8 and c.dim() == 2):
         raise TypeError(f"{what}.codes: expected a 2-D int8 CUDA tensor")
-    if c.stride(1) != 1 and c.numel() > 0:
+    rows, cols = c.shape
+    pitch, step = c.stride()
+    if step != 1 and rows > 0 and cols > 0:
         raise ValueError(f"{what}.codes: the last dimension must be contiguous")
     if not isinstance(s, torch.Tensor) or s.dtype != torch.float32 or s.dim() != 1 or not s.is_contiguous():
         raise TypeError(f"{what}.scales: expected a contiguous 1-D float32 tensor")
-    if s.shape[0] != c.shape[0]:
-        raise ValueError(f"{what}.scales: {s.shape[0]} values for {c.shape[0]} rows")
-    if not s.is_cuda or s.get_device() != c.get_device():
+    if s.numel() != rows:
+        raise ValueError(f"{what}.scales: {s.numel()} values for {rows} rows")
+    if s.get_device() != c.get_device():  # (of a CPU tensor: -1)
         raise ValueError(f"{what}.scales: on {s.device}, expected {c.device}")
-    return c, s
+    return c, s, rows, cols, pitch if rows > 1 and cols > 0 else _round_up(cols, 16)
 
 
 def nvfp4_i8_quantize(x, out=None, stream=None):
@@ -986,15 +984,16 @@ def nvfp4_i8_quantize(x, out=None, stream=None):
     if out is None:
         codes = _empty((rows, cols), torch.int8, x.device, stream)
         scales = _empty(rows, torch.float32, x.device, stream)
+        ldq = cols if rows > 1 else _round_up(cols, 16)
         out = I8Tensor(codes, scales)
     else:
-        codes, scales = _check_i8(out, "out")
-        if tuple(codes.shape) != (rows, cols):
-            raise ValueError(f"out: shape {tuple(codes.shape)}, expected {(rows, cols)}")
+        codes, scales, *shape, ldq = _check_i8(out, "out")
+        if shape != [rows, cols]:
+            raise ValueError(f"out: shape {tuple(shape)}, expected {(rows, cols)}")
         if codes.get_device() != x.get_device():
             raise ValueError(f"out: on {codes.device}, expected {x.device}")
-    st = load_library().nvfp4_i8_quantize(x.data_ptr(), rows, cols, _pitch(x), codes.data_ptr(), _pitch(codes, 16),
-                                          scales.data_ptr(), _raw_stream(stream))
+    st = load_library().nvfp4_i8_quantize(x.data_ptr(), rows, cols, _pitch(x), codes.data_ptr(), ldq, scales.data_ptr(),
+                                          _raw_stream(stream))
     if stream is not None:
         _used_on(stream, x, codes, scales)
     if st:
@@ -1005,8 +1004,8 @@ def nvfp4_i8_quantize(x, out=None, stream=None):
 def nvfp4_i8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
     """a (M x K) times b (N x K) transposed, both I8Tensors (see nvfp4_i8_gemm
     in nvfp4.h): M x N, float32 or bfloat16."""
-    (ac, sa), (bc, sb) = _check_i8(a, "a"), _check_i8(b, "b")
-    (M, K), (N, b_cols) = ac.shape, bc.shape
+    ac, sa, M, K, lda = _check_i8(a, "a")
+    bc, sb, N, b_cols, ldb = _check_i8(b, "b")
     if b_cols != K:
         raise ValueError(f"b: {b_cols} columns, a has {K}")
     if bc.get_device() != ac.get_device():
@@ -1019,8 +1018,8 @@ def nvfp4_i8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
         _check_gemm_out(out, (M, N), ac.device)
         code = _out_code(out.dtype)
         ldc = _pitch(out, 4)
-    st = load_library().nvfp4_i8_gemm(ac.data_ptr(), _pitch(ac, 16), sa.data_ptr(), bc.data_ptr(), _pitch(bc, 16),
-                                      sb.data_ptr(), M, N, K, out.data_ptr(), ldc, code, _raw_stream(stream))
+    st = load_library().nvfp4_i8_gemm(ac.data_ptr(), lda, sa.data_ptr(), bc.data_ptr(), ldb, sb.data_ptr(),
+                                      M, N, K, out.data_ptr(), ldc, code, _raw_stream(stream))
     if stream is not None:
         _used_on(stream, ac, sa, bc, sb, out)
     if st:

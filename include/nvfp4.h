@@ -606,9 +606,11 @@ int nvfp4_adamw_table(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t 
  *   state_bits  32: m and v are fp32.
  *               8: m and r = sqrt(v) are OCP E4M3 codes times their block's
  *               scale, blocks of 128 consecutive elements of the tensor.  The
- *               scale is the smallest power of two (not below 2^-126) for
- *               which no value of the block passes 448; codes are rounded to
- *               nearest even, and a nonzero r to at least 2^-9 of the scale.
+ *               scale is the smallest power of two for which no value of the
+ *               block passes 448 (from 2^-126 to 2^119 for m and to 2^55 for r,
+ *               whose square has to be finite; larger values are held as
+ *               448); codes are rounded to nearest even, and a nonzero r to at
+ *               least 2^-9 of the scale.
  *               The update uses m and v before they are rounded to 8 bits.
  *               All-zero codes with any finite scale are the initial state.
  *   step        >= 1, the number of this step (the bias corrections).
@@ -621,8 +623,11 @@ int nvfp4_adamw_table(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t 
  *               nvfp4_adamw_table wrote for the same arguments (if that was
  *               anything): the tensors are then updated by one launch instead
  *               of one for every 48, with the same results.
- * A gradient that is not finite makes its own element NaN (in 8 bits its
- * block's scale too grows to its largest).  Pointers need the alignment of
+ * A gradient that is not finite makes its own element NaN.  One whose square
+ * alone overflows leaves v infinite, and its element without updates; in 8
+ * bits that element's m and r are held as 448 of their scales and it goes on
+ * from there.  Neither counts for its block's scales at that step: the other
+ * elements keep theirs.  Pointers need the alignment of
  * their type; with 16 bytes for fp32, 8 for bf16 and 4 for codes the wide
  * accesses are used.  A captured call replays the scalars it was captured
  * with.  Returns NVFP4_OK or a negative status; nothing is enqueued on

@@ -615,7 +615,9 @@ int nvfp4_adamw_table(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t 
  *               All-zero codes with any finite scale are the initial state.
  *   step        >= 1, the number of this step (the bias corrections).
  *   beta1, beta2 in [0, 1), eps >= 0, lr and weight_decay finite
- *               (NVFP4_ERR_MODE otherwise).
+ *               (NVFP4_ERR_MODE otherwise).  An eps below fp32's smallest value
+ *               counts as that; with eps = 0 a parameter that never had a
+ *               gradient becomes 0 / 0.
  *   grad_scale  optional device float that every gradient is multiplied by
  *               (clipping, loss scaling).  If it is not finite the step
  *               writes nothing.

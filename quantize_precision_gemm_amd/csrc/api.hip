@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 
@@ -784,6 +785,7 @@ int nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t p_dtyp
     a.step.rate = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
     a.step.root_corr = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
     a.step.eps = (float)eps;
+    if (eps > 0.0 && a.step.eps == 0.0f) a.step.eps = FLT_TRUE_MIN;  // 0 / eps stays 0
     a.step.grad_scale = grad_scale;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const AdamWTotal total = adamw_total(tensors, count);

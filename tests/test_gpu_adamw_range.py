@@ -1,4 +1,4 @@
-"""GPU tests of AdamW steps whose gradients or moments leave fp32's range
+"""GPU tests of AdamW steps whose gradients, moments or eps leave fp32's range
 or 8-bit states' (nvfp4_adamw): what the other elements of a block keep, and
 what the element itself is held as.
 
@@ -142,3 +142,17 @@ def test_states_out_of_range_from_elsewhere(env):
         assert torch.isfinite(m.float()).all().item() and torch.isfinite(v.float()).all().item()
         assert torch.isfinite(ms).all().item() and (vs <= 2.0 ** 55).all().item()
     assert torch.equal(p, torch.ones(256, device=dev))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_an_eps_below_fp32_is_not_zero(env, bits):
+    """A parameter that never had a gradient is not divided 0 by 0."""
+    torch, q, dev = env
+    p, g = torch.ones(200, device=dev), torch.zeros(200, device=dev)
+    g[::2] = 0.5
+    group = q.AdamWGroup.with_states([p], [g], bits=bits)
+    print(f"adamw eps 1e-60 bits {bits}", flush=True)
+    for step in (1, 2):
+        q.nvfp4_adamw(group, step, lr=1e-3, eps=1e-60, weight_decay=0.0)
+    assert torch.equal(p[1::2], torch.ones(100, device=dev))
+    assert (p[::2] < 1).all().item() and torch.isfinite(p).all().item()

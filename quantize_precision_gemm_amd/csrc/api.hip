@@ -664,8 +664,9 @@ int check_grouped(int32_t pass, int64_t E, int64_t T, int64_t N, int64_t K)
     const int64_t lim = int64_t(1) << 31;
     if (E >= lim || T >= lim || N >= lim || K >= lim) return NVFP4_ERR_SHAPE;
     const int64_t cols = pass == NVFP4_FPROP ? N : K;
-    const int64_t tiles = (pass == NVFP4_WGRAD ? E * ((N + 255) / 256) : T / 256 + E + 1) * ((cols + 255) / 256);
-    return tiles < kMostBigTiles ? NVFP4_OK : NVFP4_ERR_SHAPE;
+    const int64_t row_tiles = pass == NVFP4_WGRAD ? E * ((N + 255) / 256) : T / 256 + E + 1;
+    const int64_t col_tiles = (cols + 255) / 256;  // (the product of the two may pass 64 bits)
+    return col_tiles == 0 || row_tiles <= (kMostBigTiles - 1) / col_tiles ? NVFP4_OK : NVFP4_ERR_SHAPE;
 }
 
 int check_adamw(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight)

@@ -19,7 +19,8 @@ sys.path.insert(0, ROOT)
 
 TESTS = ["tests/test_oracle_codecs.py", "tests/test_oracle_quant.py", "tests/test_oracle_philox.py",
          "tests/test_oracle_rht_gemm.py", "tests/test_oracle_rht_sized.py", "tests/test_oracle_mx.py",
-         "tests/test_abi.py", "tests/test_binding_checks.py"]
+         "tests/test_abi.py", "tests/test_binding_checks.py", "tests/test_operator_checks.py",
+         "tests/test_operator_ranges.py"]
 
 
 def main():

@@ -1,0 +1,37 @@
+"""Sizes next to what 64-bit integers hold, in the host checks of the expert
+products and the AdamW step (include/nvfp4.h): refused before any of their
+products leaves that range.  CPU only: no pointer is dereferenced, no compute
+call is made."""
+import ctypes
+import os
+
+import pytest
+
+import quantize_precision_gemm_amd as q
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(q.lib_path()):
+        from quantize_precision_gemm_amd import build as hip_build
+        hip_build.build()
+    return q.load_library()
+
+
+MOST = (1 << 31) - 8
+
+
+@pytest.mark.parametrize("sizes,status", [
+    # pass, E, T, N, K: more output tiles than a grid holds
+    ((2, 1 << 30, 10, 1 << 25, 1 << 25), -2),  # 2^64 tiles
+    ((2, 1 << 29, 10, 1 << 25, 1 << 25), -2),  # 2^63
+    ((2, MOST, 10, MOST, MOST), -2), ((0, MOST, MOST, MOST, 64), -2), ((1, MOST, MOST, 64, MOST), -2),
+    ((2, 1 << 11, 10, 1 << 8, 1 << 19), -2),   # 2^22, one too many
+    ((2, 1 << 11, 10, 1 << 8, (1 << 19) - 256), 0),
+    ((0, (1 << 22) - 1, 0, 256, 8), -2), ((0, (1 << 22) - 2, 0, 256, 8), 0),
+    ((2, MOST, 10, 0, MOST), 0), ((2, 0, 10, MOST, MOST), 0), ((0, MOST, 10, 0, 8), 0),  # no output
+])
+def test_grouped_sizes(lib, sizes, status):
+    n = ctypes.c_int64(-7)
+    assert lib.nvfp4_bf16_grouped_gemm_workspace(*sizes, ctypes.byref(n)) == status
+    assert (n.value >= 0) if status == 0 else (n.value == -7)

@@ -649,6 +649,7 @@ constexpr int64_t kMostBigTiles = int64_t(1) << 22;
 // nvfp4_adamw: one launch takes up to kAdamWTensors tensors and 2^23
 // workgroups (a tensor has at most 2^33 elements, that many workgroups).
 constexpr int64_t kMostChunks = int64_t(1) << 23;
+constexpr int64_t kMostElements = int64_t(1) << 33;
 
 bool adamw_vec(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight)
 {
@@ -671,7 +672,7 @@ int check_grouped(int32_t pass, int64_t E, int64_t T, int64_t N, int64_t K)
 
 int check_adamw(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight)
 {
-    if (t.n < 0) return NVFP4_ERR_SHAPE;
+    if (t.n < 0 || t.n > kMostElements) return NVFP4_ERR_SHAPE;
     if (t.n > 0 && (!t.p || !t.g || !t.m || !t.v)) return NVFP4_ERR_NULL;
     if (t.n > 0 && eight && (!t.m_scale || !t.v_scale)) return NVFP4_ERR_NULL;
     if (t.copy && p_bf16) return NVFP4_ERR_MODE;
@@ -679,7 +680,6 @@ int check_adamw(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eigh
         return NVFP4_ERR_ALIGN;
     if (!eight && (!aligned(t.m, 4) || !aligned(t.v, 4))) return NVFP4_ERR_ALIGN;
     if (eight && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))) return NVFP4_ERR_ALIGN;
-    if (nvfp4::adamw_chunks(t.n) > kMostChunks) return NVFP4_ERR_SHAPE;
     return NVFP4_OK;
 }
 

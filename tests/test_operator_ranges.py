@@ -8,6 +8,7 @@ import os
 import pytest
 
 import quantize_precision_gemm_amd as q
+from tests.test_operator_checks import ADAMW, FAKE
 
 
 @pytest.fixture(scope="module")
@@ -35,3 +36,16 @@ def test_grouped_sizes(lib, sizes, status):
     n = ctypes.c_int64(-7)
     assert lib.nvfp4_bf16_grouped_gemm_workspace(*sizes, ctypes.byref(n)) == status
     assert (n.value >= 0) if status == 0 else (n.value == -7)
+
+
+@pytest.mark.parametrize("n", [(1 << 63) - 1, (1 << 63) - 1024, (1 << 33) + 1, 1 << 62])
+def test_adamw_sizes(lib, n):
+    t = (q._AdamWTensor * 1)()
+    for k in ("p", "g", "m", "v", "m_scale", "v_scale", "copy"):
+        setattr(t[0], k, ADAMW[k])
+    t[0].n = n
+    size = ctypes.c_int64(-7)
+    assert lib.nvfp4_adamw_table(t, 1, 1, 1, 8, None, 0, ctypes.byref(size)) == -2 and size.value == -7
+    assert lib.nvfp4_adamw(t, 1, 1, 1, 8, 1, 1e-3, 0.9, 0.99, 1e-8, 0.1, FAKE, None, None) == -2
+    t[0].n = 1 << 33
+    assert lib.nvfp4_adamw_table(t, 1, 1, 1, 8, None, 0, ctypes.byref(size)) == 0 and size.value == 0

@@ -657,6 +657,14 @@ bool adamw_vec(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight
            aligned(t.v, eight ? 4 : 16) && aligned(t.copy, 8);
 }
 
+// Whether `stride` elements hold `rows` rows of `cols`, `ld` apart (ld >= cols
+// >= 0; ld * rows may pass 64 bits).
+bool holds(int64_t stride, int64_t rows, int64_t ld, int64_t cols)
+{
+    if (rows == 0) return stride >= 0;
+    return stride >= cols && (rows == 1 || (stride - cols) / (rows - 1) >= ld);
+}
+
 // Pass and sizes of a grouped product.
 int check_grouped(int32_t pass, int64_t E, int64_t T, int64_t N, int64_t K)
 {
@@ -883,10 +891,10 @@ int nvfp4_bf16_grouped_gemm(int32_t pass, const void* a, int64_t lda, const void
     if (lda < a_cols || ldb < K || ldc < c_cols) return NVFP4_ERR_SHAPE;
     if (wgrad) {
         if (stride_c % 4 != 0) return NVFP4_ERR_ALIGN;
-        if (stride_c < (N > 0 ? (N - 1) * ldc + c_cols : 0)) return NVFP4_ERR_SHAPE;
+        if (!holds(stride_c, N, ldc, c_cols)) return NVFP4_ERR_SHAPE;
     } else {
         if (stride_b % 8 != 0) return NVFP4_ERR_ALIGN;
-        if (stride_b < (N > 0 ? (N - 1) * ldb + K : 0)) return NVFP4_ERR_SHAPE;
+        if (!holds(stride_b, N, ldb, K)) return NVFP4_ERR_SHAPE;
     }
     // a tile's 256 rows (or 64 k rows) are addressed with 32-bit offsets
     const int64_t span = int64_t(1) << 22;

@@ -8,7 +8,7 @@ import os
 import pytest
 
 import quantize_precision_gemm_amd as q
-from tests.test_operator_checks import ADAMW, FAKE
+from tests.test_operator_checks import ADAMW, FAKE, GROUPED
 
 
 @pytest.fixture(scope="module")
@@ -49,3 +49,16 @@ def test_adamw_sizes(lib, n):
     assert lib.nvfp4_adamw(t, 1, 1, 1, 8, 1, 1e-3, 0.9, 0.99, 1e-8, 0.1, FAKE, None, None) == -2
     t[0].n = 1 << 33
     assert lib.nvfp4_adamw_table(t, 1, 1, 1, 8, None, 0, ctypes.byref(size)) == 0 and size.value == 0
+
+
+@pytest.mark.parametrize("change", [
+    {"ldb": 1 << 60, "sb": 0}, {"ldb": (1 << 63) - 8, "sb": (1 << 63) - 8}, {"ldb": 1 << 59, "sb": 0, "N": 16},
+    {"pass_": 2, "ldc": 1 << 60, "sc": 0}, {"pass_": 2, "ldc": 1 << 62, "sc": (1 << 63) - 4},
+    {"pass_": 2, "ldc": (1 << 63) - 4, "sc": 1 << 62},
+    {"pass_": 2, "sc": -(1 << 40)}, {"sb": -(1 << 40)}, {"sb": -64, "N": 0, "lda": 64}, {"pass_": 2, "sc": 60, "N": 8},
+])
+def test_grouped_strides(lib, change):
+    d = dict(GROUPED, **change)
+    got = lib.nvfp4_bf16_grouped_gemm(d["pass_"], d["a"], d["lda"], d["b"], d["ldb"], d["sb"], d["ends"], d["E"], d["T"],
+                                      d["N"], d["K"], d["c"], d["ldc"], d["sc"], d["dtype"], d["ws"], d["wb"], None)
+    assert got == -2

@@ -9,6 +9,7 @@ drawn anew for each step, so the experts' shares change from step to step.
     python examples/expert_layer.py [--steps 60] [--bits 8]
 """
 import argparse
+import math
 import os
 import sys
 
@@ -43,9 +44,10 @@ class ExpertTask:
 
 
 def clip_factor(grads, limit):
-    """limit / norm where the norm is above it (a device scalar: no step waits for the host)."""
+    """limit / norm where the norm is above it (a device scalar: no step waits
+    for the host); NaN where the norm is not finite, which leaves the step out."""
     norm = torch.linalg.vector_norm(torch.stack([torch.linalg.vector_norm(g) for g in grads]))
-    return (limit / norm.clamp(min=limit)).reshape(1)
+    return torch.where(torch.isfinite(norm), limit / norm.clamp(min=limit), math.nan).reshape(1)
 
 
 def train(steps=60, bits=8, tokens=4096, experts=6, outputs=512, inputs=256, lr=5e-3, seed=0, device="cuda:0", log=None):

@@ -271,6 +271,10 @@ class BF16Experts:
         self.y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
         self.dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
         self.dw = torch.empty((E, N, K), dtype=torch.float32, device=dev)
+        # for contractions that are split (empty where they are not), one for
+        # each pass: wgrad runs beside dgrad, and beside another layer's
+        self.ws = {p: torch.empty(q.nvfp4_bf16_grouped_gemm_workspace(p, E, T, N, K), dtype=torch.uint8, device=dev)
+                   for p in (q.FPROP, q.DGRAD, q.WGRAD)}
 
     def flops(self):
         return 3 * 2.0 * self.T * self.N * self.K
@@ -278,9 +282,11 @@ class BF16Experts:
     def weight_ops(self):
         return []
 
+    def _product(self, pass_, a, b, out):
+        self.q.nvfp4_bf16_grouped_gemm(pass_, a, b, self.ends, out=out, workspace=self.ws[pass_])
+
     def forward_ops(self):
-        q = self.q
-        return [("experts_fprop", lambda: q.nvfp4_bf16_grouped_gemm(q.FPROP, self.x, self.w, self.ends, out=self.y))]
+        return [("experts_fprop", lambda: self._product(self.q.FPROP, self.x, self.w, self.y))]
 
     def backward_shared_ops(self):
         return []
@@ -289,12 +295,10 @@ class BF16Experts:
         return []
 
     def dgrad_ops(self):
-        q = self.q
-        return [("experts_dgrad", lambda: q.nvfp4_bf16_grouped_gemm(q.DGRAD, self.dy, self.w, self.ends, out=self.dx))]
+        return [("experts_dgrad", lambda: self._product(self.q.DGRAD, self.dy, self.w, self.dx))]
 
     def wgrad_ops(self):
-        q = self.q
-        return [("experts_wgrad", lambda: q.nvfp4_bf16_grouped_gemm(q.WGRAD, self.dy, self.x, self.ends, out=self.dw))]
+        return [("experts_wgrad", lambda: self._product(self.q.WGRAD, self.dy, self.x, self.dw))]
 
 
 class TrainingStep:

@@ -1,10 +1,13 @@
-"""The example's gradient clipping (examples/expert_layer.py), on the CPU."""
+"""The training-step driver's layer of experts and the example's gradient
+clipping (examples/expert_layer.py), on the CPU."""
 import math
 import os
 import sys
 
 import pytest
 import torch
+
+import quantize_precision_gemm_amd as q
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -22,3 +25,37 @@ def test_the_example_leaves_a_step_out_whose_gradients_are_not_finite(value):
     assert abs(big * 0.25 * math.sqrt(50 * 257) / 0.5 - 1) <= 104 * 2.0 ** -24
     g[7] = value
     assert not math.isfinite(expert_layer.clip_factor([g], 10.0).item())
+
+
+class Recorder:
+    """Stands in for the package: the calls a layer makes, and their workspaces."""
+    FPROP, DGRAD, WGRAD = q.FPROP, q.DGRAD, q.WGRAD
+    need = {q.FPROP: 48, q.DGRAD: 1 << 20, q.WGRAD: 0}
+
+    def __init__(self):
+        self.calls = []
+
+    def nvfp4_bf16_grouped_gemm_workspace(self, pass_, E, T, N, K):
+        assert (E, T, N, K) == (2, 6, 16, 24)
+        return self.need[pass_]
+
+    def nvfp4_bf16_grouped_gemm(self, pass_, a, b, ends, out_dtype=None, out=None, workspace=None, stream=None):
+        self.calls.append((pass_, workspace))
+
+
+def test_a_layer_of_experts_holds_its_workspaces():
+    """One for each pass (dgrad and wgrad run beside each other), the same in
+    every step."""
+    from quantize_precision_gemm_amd.step import BF16Experts
+    r = Recorder()
+    bf16 = torch.bfloat16
+    layer = BF16Experts(r, torch, torch.zeros(6, 24, dtype=bf16), torch.zeros(2, 16, 24, dtype=bf16),
+                        torch.zeros(6, 16, dtype=bf16), torch.zeros(2, dtype=torch.int32))
+    for _ in range(2):
+        for _, op in layer.forward_ops() + layer.dgrad_ops() + layer.wgrad_ops():
+            op()
+    assert [p for p, _ in r.calls] == [q.FPROP, q.DGRAD, q.WGRAD] * 2
+    for p, ws in r.calls:
+        assert ws is not None and ws.dtype == torch.uint8 and ws.dim() == 1 and ws.numel() == r.need[p]
+    assert all(r.calls[i][1] is r.calls[i + 3][1] for i in range(3))
+    assert r.calls[0][1].data_ptr() != r.calls[1][1].data_ptr()

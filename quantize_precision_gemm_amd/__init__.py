@@ -813,6 +813,19 @@ def nvfp4_bf16_grouped_gemm(pass_, a, b, ends, out_dtype=torch.bfloat16, out=Non
     return out
 
 
+def _overlapping(written, read):
+    """Whether a range [start, end) of `written` shares bytes with any other range."""
+    most_written = most_read = 0  # the largest ends so far
+    for start, end, writes in sorted([(s, e, True) for s, e in written if s < e] + [(s, e, False) for s, e in read if s < e]):
+        if start < most_written or (writes and start < most_read):
+            return True
+        if writes:
+            most_written = end
+        else:
+            most_read = max(most_read, end)
+    return False
+
+
 class AdamWGroup:
     """The tensors of one AdamW step and where their states lie, made once.
 
@@ -826,7 +839,8 @@ class AdamWGroup:
              entry may be None
 
     The group holds its tensors and their addresses; all of one kind have one
-    dtype.  A tensor that gets other memory (t.data = ...) needs a new group.
+    dtype.  nvfp4_adamw refuses a group in which a buffer that the step writes
+    shares memory with another one (gradients may be shared).  A tensor that gets other memory (t.data = ...) needs a new group.
     """
 
     BLOCK = 128  # elements that share the scale of an 8-bit state
@@ -860,20 +874,29 @@ class AdamWGroup:
         if eight:
             kinds += [("m_scale", "m_scales", self.m_scales, torch.float32),
                       ("v_scale", "v_scales", self.v_scales, torch.float32)]
-        for i, p in enumerate(self.params):
-            table[i].n = p.numel() if isinstance(p, torch.Tensor) else 0
+        entries = [table[i] for i in range(k)]
+        counts = [p.numel() if isinstance(p, torch.Tensor) else 0 for p in self.params]
+        blocks = [-(-n // self.BLOCK) for n in counts]
+        index, written, read = self.params[0].get_device(), [], []
         for field, what, tensors, dtype in kinds:
+            ranges, size = read if what == "grads" else written, dtype.itemsize
             if what == "copies" and any(t is not None for t in tensors) and self.p_dtype != OUT_FP32:
                 raise ValueError("copies are made of float32 params")
-            for i, t in enumerate(tensors):
+            for i, (entry, t, n) in enumerate(zip(entries, tensors, blocks if what.endswith("scales") else counts)):
                 if t is None and what == "copies":
                     continue
-                n = table[i].n
-                self._check_tensor(what, i, t, dtype, -(-n // self.BLOCK) if what.endswith("scales") else n)
-                setattr(table[i], field, t.data_ptr())
-        seen = [table[i].p for i in range(k) if table[i].n]
+                if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.get_device() == index and
+                        t.numel() == n and t.is_contiguous()):
+                    self._refuse_tensor(what, i, t, dtype, n)
+                at = t.data_ptr()
+                setattr(entry, field, at)
+                ranges.append((at, at + n * size))
+        for entry, n in zip(entries, counts):
+            entry.n = n
+        seen = [entry.p for entry, n in zip(entries, counts) if n]
         if len(set(seen)) != len(seen):
             raise ValueError("params: the same tensor twice in one group")
+        self._overlaps = _overlapping(written, read)
         self.count = k
         self._device_table = self._make_device_table()
 
@@ -888,7 +911,7 @@ class AdamWGroup:
         _check(L.nvfp4_adamw_table(*args, host.data_ptr(), need.value, ctypes.byref(need)), "nvfp4_adamw_table")
         return host.to(self.device)
 
-    def _check_tensor(self, what, i, t, dtype, count):
+    def _refuse_tensor(self, what, i, t, dtype, count):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{what}[{i}]: expected a CUDA tensor")
         if t.dtype != dtype:
@@ -897,8 +920,7 @@ class AdamWGroup:
             raise ValueError(f"{what}[{i}]: on {t.device}, expected {self.device}")
         if t.numel() != count:
             raise ValueError(f"{what}[{i}]: {t.numel()} elements, expected {count}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}[{i}]: must be contiguous")
+        raise ValueError(f"{what}[{i}]: must be contiguous")
 
     @classmethod
     def with_states(cls, params, grads, bits=32, copies=None):
@@ -936,6 +958,8 @@ def nvfp4_adamw(group, step, lr, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0
         grad_scale = grad_scale.data_ptr()
     if group.count == 0:
         return
+    if group._overlaps:
+        raise ValueError("group: params, states or copies overlap in memory, with each other or with grads")
     table = group._device_table
     st = load_library().nvfp4_adamw(group._table, group.count, group.p_dtype, group.g_dtype, group.bits, step, lr,
                                     beta1, beta2, eps, weight_decay, grad_scale,

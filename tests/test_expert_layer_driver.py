@@ -1,5 +1,6 @@
-"""The training-step driver's layer of experts and the example's gradient
-clipping (examples/expert_layer.py), on the CPU."""
+"""The training-step driver's layer of experts, the example's gradient clipping
+(examples/expert_layer.py) and the search for overlaps among an AdamWGroup's
+buffers, on the CPU."""
 import math
 import os
 import sys
@@ -59,3 +60,23 @@ def test_a_layer_of_experts_holds_its_workspaces():
         assert ws is not None and ws.dtype == torch.uint8 and ws.dim() == 1 and ws.numel() == r.need[p]
     assert all(r.calls[i][1] is r.calls[i + 3][1] for i in range(3))
     assert r.calls[0][1].data_ptr() != r.calls[1][1].data_ptr()
+
+
+@pytest.mark.parametrize("written,read,found", [
+    ([], [], False),
+    ([(0, 16)], [(0, 16)], True),
+    ([(0, 16), (16, 32)], [(32, 48), (32, 48)], False),            # neighbours; gradients may be shared
+    ([(0, 16), (12, 20)], [], True),
+    ([(40, 48), (0, 100)], [], True),                              # one inside another
+    ([(0, 16), (64, 80)], [(20, 60), (10, 11)], True),
+    ([(0, 16), (64, 80)], [(20, 60), (16, 64)], False),
+    ([(0, 16), (64, 80)], [(80, 96), (8, 100)], True),
+    ([(8, 8), (0, 16)], [(12, 12)], False),                        # tensors without elements
+    ([(0, 4), (4, 8), (8, 12), (11, 16)], [], True),
+    ([(100, 200)], [(0, 50), (20, 101)], True),
+    ([(100, 200)], [(0, 300), (10, 20)], True),
+])
+def test_overlaps_of_written_buffers(written, read, found):
+    for w in (written, written[::-1]):
+        for r in (read, read[::-1]):
+            assert q._overlapping(w, r) == found

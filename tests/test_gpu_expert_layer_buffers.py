@@ -1,6 +1,6 @@
 """GPU tests of what the expert-layer calls do to memory: the training-step
 driver's layer of experts allocates nothing in a step, also where its
-contractions are split."""
+contractions are split, and no step runs over buffers that share memory."""
 import pytest
 
 from tests.gpu_util import ensure_built
@@ -49,3 +49,51 @@ def test_a_step_of_experts_allocates_nothing(env, serial):
         assert torch.equal(x.y, q.nvfp4_bf16_grouped_gemm(q.FPROP, x.x, x.w, ends))
         assert torch.equal(x.dx, q.nvfp4_bf16_grouped_gemm(q.DGRAD, x.dy, x.w, ends))
         assert torch.equal(x.dw, q.nvfp4_bf16_grouped_gemm(q.WGRAD, x.dy, x.x, ends, torch.float32))
+
+
+def group_tensors(torch, dev, bits, n=70_000):
+    d = {"params": [torch.ones(n, device=dev)], "grads": [torch.ones(n, device=dev)]}
+    if bits == 8:
+        for k in ("m", "v"):
+            d[k] = [torch.zeros(n, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)]
+            d[k + "_scales"] = [torch.zeros(-(-n // 128), device=dev)]
+    else:
+        d.update(m=[torch.zeros(n, device=dev)], v=[torch.zeros(n, device=dev)])
+    d["copies"] = [torch.zeros(n, dtype=torch.bfloat16, device=dev)]
+    return d
+
+
+OVERLAPS = [
+    ("m and v", lambda d, t: d.update(v=d["m"])),
+    ("m and v in part", lambda d, t: d.update(m=[t[0:1000]], v=[t[996:1996]])),
+    ("params in part", lambda d, t: d.update(params=[t[0:1000]], m=[t[999:1999]])),
+    ("params and grads", lambda d, t: d.update(grads=d["params"])),
+    ("copies and grads", lambda d, t: d.update(grads=[t[0:1000]], copies=[t[500:1000].view(d["copies"][0].dtype)])),
+]
+
+
+@pytest.mark.parametrize("what", range(len(OVERLAPS)))
+def test_refuses_a_step_over_buffers_that_overlap(env, what):
+    torch, q, dev = env
+    name, change = OVERLAPS[what]
+    d = group_tensors(torch, dev, 32, 1000)
+    change(d, torch.zeros(4000, device=dev))
+    before = {k: v[0].clone() for k, v in d.items()}
+    print(f"overlap of {name}", flush=True)
+    with pytest.raises(ValueError, match="overlap"):
+        q.nvfp4_adamw(q.AdamWGroup(**d), 1, 1e-3)
+    torch.cuda.synchronize()
+    for k, v in d.items():
+        assert torch.equal(v[0], before[k]), k
+
+
+def test_takes_neighbours_and_shared_gradients(env):
+    """Pieces of one buffer that touch, gradients read by two tensors, and
+    tensors without elements are no overlap."""
+    torch, q, dev = env
+    flat, g = torch.zeros(8 * 128, device=dev), torch.ones(128, device=dev)
+    cut = [flat[128 * i:128 * (i + 1)] for i in range(6)]
+    empty = flat[100:100]
+    print("neighbours", flush=True)
+    q.nvfp4_adamw(q.AdamWGroup(cut[0:2] + [empty], [g, g, empty], cut[2:4] + [empty], cut[4:6] + [empty]), 1, 1e-3)
+    assert not flat[768:].any().item() and flat[:768].all().item()

@@ -840,7 +840,12 @@ class AdamWGroup:
 
     The group holds its tensors and their addresses; all of one kind have one
     dtype.  nvfp4_adamw refuses a group in which a buffer that the step writes
-    shares memory with another one (gradients may be shared).  A tensor that gets other memory (t.data = ...) needs a new group.
+    shares memory with another one (gradients may be shared).  A tensor that
+    gets other memory (t.data = ..., module.to) needs a new group: the steps of
+    this one go on in the old memory, which it keeps from being freed.  (Asking
+    96 tensors and their states for their addresses takes 19 us, the step of
+    such small ones 6.)  Storages that are resized in place (t.resize_) free
+    what the group points to; do not resize the tensors of a group in use.
     """
 
     BLOCK = 128  # elements that share the scale of an 8-bit state
@@ -878,6 +883,7 @@ class AdamWGroup:
         counts = [p.numel() if isinstance(p, torch.Tensor) else 0 for p in self.params]
         blocks = [-(-n // self.BLOCK) for n in counts]
         index, written, read = self.params[0].get_device(), [], []
+        self._storages = storages = []
         for field, what, tensors, dtype in kinds:
             ranges, size = read if what == "grads" else written, dtype.itemsize
             if what == "copies" and any(t is not None for t in tensors) and self.p_dtype != OUT_FP32:
@@ -891,6 +897,7 @@ class AdamWGroup:
                 at = t.data_ptr()
                 setattr(entry, field, at)
                 ranges.append((at, at + n * size))
+                storages.append(t.untyped_storage())
         for entry, n in zip(entries, counts):
             entry.n = n
         seen = [entry.p for entry, n in zip(entries, counts) if n]

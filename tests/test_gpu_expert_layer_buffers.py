@@ -1,6 +1,7 @@
 """GPU tests of what the expert-layer calls do to memory: the training-step
 driver's layer of experts allocates nothing in a step, also where its
-contractions are split, and no step runs over buffers that share memory."""
+contractions are split; no step runs over buffers that share memory; an
+AdamWGroup does not let go of its tensors' memory."""
 import pytest
 
 from tests.gpu_util import ensure_built
@@ -97,3 +98,21 @@ def test_takes_neighbours_and_shared_gradients(env):
     print("neighbours", flush=True)
     q.nvfp4_adamw(q.AdamWGroup(cut[0:2] + [empty], [g, g, empty], cut[2:4] + [empty], cut[4:6] + [empty]), 1, 1e-3)
     assert not flat[768:].any().item() and flat[:768].all().item()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_memory_of_a_group_is_not_given_to_others(env, bits):
+    """A tensor of a group that is pointed to other memory: the old memory,
+    which the next step still writes, stays the group's."""
+    torch, q, dev = env
+    d = group_tensors(torch, dev, bits)
+    group = q.AdamWGroup(**d)
+    for kind, (t,) in d.items():
+        old, size = t.data_ptr(), t.numel() * t.element_size()
+        torch.cuda.synchronize()
+        t.data = torch.zeros_like(t)
+        others = [torch.empty(size, dtype=torch.uint8, device=dev) for _ in range(8)]
+        print(f"group keeps {kind}, bits {bits}", flush=True)
+        for o in others:
+            assert not (o.data_ptr() < old + size and old < o.data_ptr() + o.numel()), kind
+    del group

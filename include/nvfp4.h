@@ -644,7 +644,8 @@ int nvfp4_adamw(const nvfp4_adamw_tensor* tensors, int64_t count, int32_t p_dtyp
  * bf16 matrix (the tokens of an activation, the output channels of a weight):
  *   scale[r] = max_k |x[r, k]| / 127
  *   code[r, k] = 127 x[r, k] / max_k |x[r, k]| rounded to nearest even
- * A row of zeros has scale 0 and codes 0.
+ * A row of zeros has scale 0 and codes 0.  A row with an infinity or NaN has
+ * scale infinity or NaN and codes 0: its products are NaN.
  *   x         device bf16, rows x ld_x elements; 16-byte aligned, ld_x >= cols
  *             and a multiple of 8.
  *   cols      >= 0 and a multiple of 16.

@@ -4,6 +4,8 @@
 //
 //   amax_r = max_k |x[r, k]|,  scale_r = amax_r / 127,
 //   code[r, k] = rint(127 x[r, k] / amax_r), ties to even, in [-127, 127].
+// A row whose maximum is not finite keeps that as its scale; its codes are 0
+// (the factor is 0, and an element that is not finite times 0 is NaN).
 // 127 x is exact in fp32 for a bf16 x and the quotient is rounded once, so a
 // code is the one that exact arithmetic gives: with significands X and A of 8
 // bits, 127 X / (A 2^d) that is no tie differs from one by at least
@@ -40,7 +42,11 @@ __device__ __forceinline__ uint32_t code_of(float x, float scale)
     const float y = x * scale;
     const float t = y * 65.0f;              // y to 18 bits: 24 - 6
     const float y18 = t - (t - y);
-    return (uint32_t)(int)__builtin_rintf(y18) & 0xFFu;
+    // the instruction takes NaN as 0, a C++ conversion leaves it undefined (a
+    // mask that clears such a row first cost 20.8 -> 21.1 us for 8192 x 5120)
+    uint32_t code;
+    asm("v_cvt_i32_f32 %0, %1" : "=v"(code) : "v"(__builtin_rintf(y18)));
+    return code & 0xFFu;
 }
 
 __device__ __forceinline__ uint2 codes_of(const uint4& v, float lift, float scale)
@@ -89,7 +95,7 @@ __global__ __launch_bounds__(256) void k_i8_quant(const uint16_t* __restrict__ x
             __syncthreads();  // part is written again for the next row
         }
         const float amax = __uint_as_float(top << 16);
-        if (lane == 0) scales[row] = amax / 127.0f;
+        if (lane == 0) scales[row] = amax / 127.0f;  // infinity or NaN if amax is
         // a power of two on both sides of the quotient keeps 127 / amax finite
         const float lift = amax < 0x1p-100f ? 0x1p64f : 1.0f;
         const float scale = amax > 0.0f ? 127.0f / (amax * lift) : 0.0f;

@@ -309,7 +309,10 @@ constexpr int kLdsBytes = 9 * kHalfBytes;
 
 __device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
 
-// 16 bytes a lane from `src` to LDS byte `lds` + 16 * lane.
+// 16 bytes a lane from `src` to LDS byte `lds` + 16 * lane.  (m0 is written
+// and read within the statement; the compiler reserves it and warns of its name in a
+// clobber list, which changes no instruction here.  Its own uses, LDS DMA by
+// builtins, indexed registers and messages, must not be added to these kernels.)
 __device__ __forceinline__ void dma16(const uint8_t* src, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");

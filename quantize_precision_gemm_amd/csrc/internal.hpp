@@ -155,7 +155,7 @@ void launch_i8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, 
                      float* scales, hipStream_t s);
 
 // C[m, n] = sa[m] sb[n] sum_k a[m, k] b[n, k], the sum exact in int32 (K a
-// multiple of 16, K > 0).
+// multiple of 16; 0: zeros).
 void launch_i8_gemm(const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb, const float* sb,
                     int64_t M, int64_t N, int64_t K, void* c, int64_t ldc, bool out_fp32, int cus, hipStream_t s);
 

@@ -301,7 +301,7 @@ __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t 
 // keep the LDS busy for about as long as the MFMAs take, and under full load
 // the power limit lowers the clock (1.5 to 1.7 GHz): 16384 rows of 8 experts,
 // N = K = 5120, 710 to 760 us (1130 to 1210 TFLOP/s, MFMAs 0.70 of the cycles), int8
-// 8192 x 20480 x 5120 720 us (2390 TOP/s).  A tile alone: 1.15 us a step and 9
+// 8192 x 20480 x 5120 690 to 735 us (2340 to 2490 TOP/s).  A tile alone: 1.15 us a step and 9
 // us for its start and end.
 // ---------------------------------------------------------------------------
 constexpr int kHalfBytes = 128 * 128;
@@ -565,7 +565,7 @@ __device__ __forceinline__ void big_tile(const View& A, const View& B, int64_t m
 // t + 4 starts when every wave's reads of step t have come back.  Wave
 // (wm, wn) of 2 x 2 owns 64 x 64; it reads the fragments of the next step
 // while it multiplies those of this one.  0.47 us a step (int8, 64 x 5120 x
-// 5120: 21.2 us, by 256 x 256 tiles 26.1).
+// 5120: 20.6 us, by 256 x 256 tiles 25.4).
 // ---------------------------------------------------------------------------
 template <class Acc, bool kTA, bool kTB>
 __device__ __forceinline__ void mid_tile(const View& A, const View& B, int64_t m0, int64_t n0, int64_t Ka, int64_t Kb,
@@ -646,7 +646,8 @@ __device__ __forceinline__ void mid_tile(const View& A, const View& B, int64_t m
 // The 128 x 256 products of a 256 x 256 tile of which no more rows are
 // wanted: the same loop with the 8 waves of the big tile, 2 x 4 of 64 x 64
 // outputs each, and three buffers of 48 KB.  0.72 us a step, 1.15 for the whole
-// tile (int8, 777 x 5120 x 5120, 80 tiles as halves: 36.3 us).
+// tile (int8, 777 x 5120 x 5120, 80 tiles as halves: 36.3 us back to back,
+// 37.2 behind its quantiser).
 template <class Acc, bool kTA, bool kTB>
 __device__ __forceinline__ void wide_tile(const View& A, const View& B, int64_t m0, int64_t n0, int64_t Ka, int64_t Kb,
                                           int64_t mend, int steps, uint8_t* lds, Acc (&acc)[2][2])
@@ -1133,9 +1134,10 @@ enum class Tiles { kThin, kMid, kBig };
 //   mid   1.5, and 4 and 0.47 per step for each round of its tiles
 //   big   1.5, and 9 and 1.15 per step for each round (7 and 0.72 to 1.0 in a
 //         last round of halves)
-// For example int8, N = K = 5120: 16 rows 12.4 / 20.4 / 25.0, 64 rows 25.0 /
-// 21.2 / 26.1, 777 rows - / 43.1 / 36.3, 2048 rows - / 75.5 / 54.4; N = 1024,
-// K = 2048, 256 rows 10.8 / 13.5 / 18.1.
+// For example int8 (products alone, back to back), N = K = 5120: 16 rows 10.9 /
+// 19.9 / 24.0, 64 rows 24.4 / 20.6 / 25.4 (where thin is taken: the estimate is
+// 3 us short of its time), 777 rows - / 44.6 / 36.3, 2048 rows - / 71.6 / 53.7;
+// N = 1024, K = 2048, 256 rows 6.6 / 12.0 / 17.5.
 // thin_grid, mid_grid: their workgroups; a grid holds fewer than 2^32 threads.
 Tiles choose(double traffic, int64_t thin_grid, double mid, int64_t mid_grid, double big, double steps, int cus,
              double* time = nullptr)
@@ -1181,9 +1183,11 @@ void launch_grouped_tiles(const GroupedArgs& g, bool out_fp32, hipStream_t s)
 }
 
 // Row tiles of a thin product of about `rows` rows: 16, 32 or 64.  (int8,
-// N = K = 5120, us with 16 / 32 / 64: one row 8.1 / 9.1 / 11.4, 16 rows 11.4 /
-// 12.4 / 14.8, 24 rows 16.0 / 14.1 / 16.5, 33 rows 18.7 / 22.3 / 18.2, 48 rows
-// 20.4 / 22.3 / 21.4.)
+// N = K = 5120, us with 16 / 32 / 64: one row 7.5 / 8.6 / 11.0, 16 rows 10.8 /
+// 12.1 / 14.4, 24 rows 15.9 / 13.7 / 16.1, 33 rows 18.6 / 22.3 / 17.8, 48 rows
+// 20.4 / 22.3 / 21.0.)  A grouped product takes the mean load for it, since the
+// host does not see the routing: 256 rows of one expert, 5120 -> 2560, take
+// 24.6 us alone and 41.7 among 64 experts.
 int thin_rows(double rows) { return rows <= 16.0 ? 1 : rows <= 32.0 ? 2 : 4; }
 
 template <int kM>

@@ -79,6 +79,16 @@ extern "C" {
 #define NVFP4_OUT_BF16 0
 #define NVFP4_OUT_FP32 1
 
+/* Scores of a router (nvfp4_route). */
+#define NVFP4_SOFTMAX 0
+#define NVFP4_SIGMOID 1
+
+/* Activations of a linear layer (nvfp4_bf16_linear). */
+#define NVFP4_ACT_NONE 0
+#define NVFP4_ACT_RELU2 1       /* max(z, 0)^2 */
+#define NVFP4_ACT_SILU 2        /* z / (1 + e^-z) */
+#define NVFP4_ACT_GELU 3        /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+
 /* Code layouts (nvfp4_tensor.layout; the scales are row-major in both). */
 #define NVFP4_LAYOUT_ROW_MAJOR 0   /* byte j of code row r at r * ld + j */
 #define NVFP4_LAYOUT_INTERLEAVED 1 /* rows interleaved by 4 in 32-byte pieces (below) */
@@ -674,6 +684,166 @@ int nvfp4_i8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld_x, i
 int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int8_t* b, int64_t ldb,
                   const float* b_scales, int64_t M, int64_t N, int64_t K, void* c, int64_t ldc,
                   int32_t c_dtype, void* stream);
+
+/*
+ * nvfp4_route -- routing of T tokens to k of E experts each, and the order of
+ * the rows by expert that nvfp4_bf16_grouped_gemm takes.
+ *   s = softmax(l) or 1 / (1 + e^-l) of a token's logits l;  c = s + bias.
+ *   groups > groups_kept: groups of E / groups neighbours; a group counts the
+ *   sum of its two largest c (of its only one), and the experts outside of the
+ *   groups_kept best groups are not chosen.
+ *   Chosen are the k largest c in falling order; without a bias the k largest
+ *   l (the same order).  Equal ones, of experts and of groups: the lowest index first.
+ *   weight = scale s, or with renormalise scale s / (sum of the chosen s).
+ * The choices are those of 64-bit arithmetic on the given logits and biases,
+ * whatever their type.  An expert whose logit or c is not finite is not
+ * chosen; a token with fewer than k to choose from has experts and rows -1 and
+ * weights 0 in its last slots (all of them where every logit is minus
+ * infinity: a padded token).  A token with a logit that is NaN or plus
+ * infinity has weights NaN.
+ *   logits    device fp32 or bf16 (l_dtype), T rows of E, ld apart (any ld >= E;
+ *             multiples of 4 from 16-byte aligned logits (bf16: 8) are read faster).
+ *   bias      device float, E values, or NULL; it enters the choice alone.
+ *   T         0 to 2^27; E 1 to 1024; k 1 to min(16, E / groups * groups_kept);
+ *             T k below 2^31; groups 1 to 64, a divisor of E.
+ *   experts, weights  device, T x k.
+ *   rows, ends  device int32, T x k and E, or both NULL: slot (t, j)'s place
+ *             when the slots are sorted by expert, then token (-1: none), and one past each
+ *             expert's last row.  With fewer than T k rows the rest belong to no expert.
+ *   scores    device float, T x E, or NULL: all s (of a token with a logit
+ *             that is NaN or plus infinity: NaN).
+ *   workspace device, 16-byte aligned, the bytes of nvfp4_route_workspace
+ *             (0 for up to 64 tokens); not needed without rows.  Calls that share it must not overlap.
+ */
+int nvfp4_route(const void* logits, int32_t l_dtype, int64_t ld, int64_t T, int64_t E, int64_t k, const float* bias,
+                int64_t groups, int64_t groups_kept, int32_t score, int32_t renormalise, float scale,
+                int32_t* experts, float* weights, int32_t* rows, int32_t* ends, float* scores, void* workspace,
+                int64_t workspace_bytes, void* stream);
+
+/* Host query: the workspace bytes of nvfp4_route. */
+int nvfp4_route_workspace(int64_t T, int64_t E, int64_t* bytes);
+
+/*
+ * nvfp4_route_backward -- gradients of the logits (T x E, all written) from
+ * those of the weights, and optionally of the scores (a balance loss).  The
+ * choice has no gradient.  g = scale dweights of the chosen, p their scores over the sum of them:
+ *   renormalised: softmax p (g - sum g p), sigmoid p (g - sum g p) (1 - s);
+ *   otherwise     softmax s (g - sum g s), sigmoid g s (1 - s);
+ *   dscores d:    softmax s (d - sum d s), sigmoid d s (1 - s).
+ *   experts, dweights  T x k (an expert outside [0, E) takes no part, one that
+ *             is there twice counts twice); dscores float T x E or NULL.
+ *   dlogits   fp32 or bf16, rows ld_out apart (any ld_out >= E).
+ */
+int nvfp4_route_backward(const void* logits, int32_t l_dtype, int64_t ld, int64_t T, int64_t E, int64_t k,
+                         const int32_t* experts, const float* dweights, const float* dscores, int32_t score,
+                         int32_t renormalise, float scale, void* dlogits, int64_t ld_out, int32_t out_dtype,
+                         void* stream);
+
+/*
+ * nvfp4_dispatch -- tokens into the experts' order: out[rows[t, j]] = x[t].
+ *   x, out    bf16, T and R rows of cols, a multiple of 8, 16-byte aligned,
+ *             pitches multiples of 8.  rows: T x k int32 (k 1 to 64), as nvfp4_route writes them; a place
+ *             outside [0, R) is skipped, and rows that no slot names are left
+ *             as they are.  A place named twice gets either token.
+ * Its gradient is nvfp4_combine without weights.
+ */
+int nvfp4_dispatch(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int64_t k, int64_t cols, int64_t R,
+                   void* out, int64_t ld_out, void* stream);
+
+/*
+ * nvfp4_combine -- the experts' answers back to the tokens:
+ *   y[t] = residual[t] + sum_j weights[t, j] o[rows[t, j]]
+ * in fp32, over j in order, rounded once.  A place outside [0, R) counts as a row of zeros.
+ *   o         R rows, fp32 or bf16; weights float T x k, or NULL: 1.
+ *   y         T rows, fp32 or bf16; residual of the same type, or NULL (it may be y itself).
+ *   Bases 16-byte aligned; pitches multiples of 8 (bf16) or 4 (fp32); cols a multiple of 8.
+ */
+int nvfp4_combine(const void* o, int32_t o_dtype, int64_t ld_o, int64_t R, const int32_t* rows, const float* weights,
+                  int64_t T, int64_t k, int64_t cols, const void* residual, int64_t ld_r, void* y, int64_t ld_y,
+                  int32_t y_dtype, void* stream);
+
+/*
+ * nvfp4_combine_backward -- do[rows[t, j]] = weights[t, j] dy[t] (bf16) and
+ * dweights[t, j] = sum_c dy[t, c] o[rows[t, j], c] (fp32; 0 for a place outside [0, R)).
+ * Rows of do that no slot names are left as they are.  (residual's gradient is dy.)
+ */
+int nvfp4_combine_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* o, int32_t o_dtype,
+                           int64_t ld_o, int64_t R, const int32_t* rows, const float* weights, int64_t T, int64_t k,
+                           int64_t cols, void* d_o, int64_t ld_do, float* dweights, void* stream);
+
+/*
+ * nvfp4_rmsnorm -- root-mean-square norm of rows, with a residual added first:
+ *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight
+ * in fp32; y comes from the unrounded h.  Out: y as bf16, or as int8 with one scale
+ * per row (what nvfp4_i8_gemm takes: scale = max|y| / 127, code = rint(127 y /
+ * max|y|)), or both, from one pass.  A row whose largest |y| is not finite keeps that as its scale, with codes 0.
+ *   x         fp32 or bf16; residual, h: both fp32 or both bf16 (s_dtype); h
+ *             may be NULL, and may be residual or x itself (same type and pitch); residual may be NULL.
+ *   weight    fp32 or bf16, cols values, or NULL: 1.
+ *   cols      a multiple of 8 (with codes: 16); eps finite, >= 0 (with 0 a row of zeros gives NaN).
+ *   Bases 16-byte aligned; pitches multiples of 8 (bf16), 4 (fp32), 16 (codes).
+ */
+int nvfp4_rmsnorm(const void* x, int32_t x_dtype, int64_t ld_x, const void* residual, int64_t ld_r, int32_t s_dtype,
+                  const void* weight, int32_t w_dtype, double eps, int64_t rows, int64_t cols, void* h, int64_t ld_h,
+                  void* y, int64_t ld_y, int8_t* codes, int64_t ld_codes, float* scales, void* stream);
+
+/*
+ * nvfp4_rmsnorm_backward -- with u = dy weight and r = 1 / sqrt(mean(h^2) + eps):
+ *   dx = r (u - h r^2 mean(u h)) + dh     (x's gradient, and the residual's)
+ *   dweight = sum over the rows of dy h r (fp32, the same bits in every call)
+ *   h         as the forward pass wrote it (its x, without a residual); dh the
+ *             gradient that reached h by the residual stream, or NULL; both of
+ *             s_dtype.  dx fp32 or bf16; it may be dy or dh itself (same type and pitch).
+ *   dweight   NULL: not wanted.  cols a multiple of 8, up to 16384.
+ *   workspace with dweight: nvfp4_rmsnorm_backward_workspace bytes, 16-byte
+ *             aligned; calls that share it must not overlap.
+ */
+int nvfp4_rmsnorm_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* h, int64_t ld_h,
+                           const void* dh, int64_t ld_dh, int32_t s_dtype, const void* weight, int32_t w_dtype,
+                           double eps, int64_t rows, int64_t cols, void* dx, int64_t ld_dx, int32_t dx_dtype,
+                           float* dweight, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Host query: the workspace bytes of nvfp4_rmsnorm_backward with dweight. */
+int nvfp4_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+
+/*
+ * nvfp4_bf16_linear -- the forward product of a linear layer kept in bf16, with
+ * bias, activation and residual in its epilogue, dense or grouped by expert:
+ *   pre = x w^T + bias,  c = act(pre) + residual
+ * in fp32; pre (bf16) and c are each rounded once, c from the unrounded pre.
+ *   x, w, ends, E, T, N, K, c, ldc, c_dtype, workspace  as a, b, ... of
+ *             nvfp4_bf16_grouped_gemm's FPROP (workspace bytes:
+ *             nvfp4_bf16_grouped_gemm_workspace); ends NULL: one dense layer,
+ *             w N x K, E = 1.  Rows of no expert get zeros in c and pre.
+ *   bias      fp32 (16-byte aligned) or bf16 (8), N values, expert e's stride_bias
+ *             (a multiple of 4) from the next; or NULL.
+ *   residual  T x N of c's type and alignment, ld_r a multiple of 4, or NULL; it may be c itself.
+ *   pre       bf16 T x N, 8-byte aligned, ld_pre a multiple of 4, or NULL: what the backward pass takes.
+ */
+int nvfp4_bf16_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t stride_w, const int32_t* ends,
+                      int64_t E, int64_t T, int64_t N, int64_t K, const void* bias, int64_t stride_bias,
+                      int32_t bias_dtype, int32_t act, const void* residual, int64_t ld_r, void* pre, int64_t ld_pre,
+                      void* c, int64_t ldc, int32_t c_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * nvfp4_bf16_linear_backward -- gradients through that epilogue:
+ *   dpre = dy act'(pre) (bf16: what the DGRAD and WGRAD products take),
+ *   dbias = sum of the unrounded dpre over the rows, expert by expert (fp32 E x N; 0 without rows)
+ *   dy        T x N fp32 or bf16; pre, dpre bf16 (dpre may be pre, or a bf16 dy itself);
+ *             pre NULL with NVFP4_ACT_NONE: dpre is dy, and only dbias is computed.
+ *             Rows of no expert are left as they are.
+ *   dbias     or NULL (then pre is needed).  N a multiple of 8, E below 65536.
+ *   workspace with dbias: nvfp4_bf16_linear_backward_workspace bytes, 16-byte
+ *             aligned; calls that share it must not overlap.
+ *   Bases 16-byte aligned; pitches multiples of 8 (bf16) or 4 (fp32).
+ * (residual's gradient is dy.)
+ */
+int nvfp4_bf16_linear_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* pre, int64_t ld_pre,
+                               int32_t act, const int32_t* ends, int64_t E, int64_t T, int64_t N, void* dpre,
+                               int64_t ld_dpre, float* dbias, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Host query: the workspace bytes of nvfp4_bf16_linear_backward with dbias. */
+int nvfp4_bf16_linear_backward_workspace(int64_t E, int64_t T, int64_t N, int64_t* bytes);
 
 /* Human-readable name of a status code (static string). */
 const char* nvfp4_status_string(int32_t status);

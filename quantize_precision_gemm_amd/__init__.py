@@ -24,6 +24,11 @@ __all__ = [
     "nvfp4_mx_gemm", "nvfp4_rht_quantize_sized", "nvfp4_rht_signs64", "nvfp4_quantize_rht_rows", "BLOCK_MX32", "MX_ROWS", "MX_COLS", "MX_COLS_RHT", "nvfp4_gemm_fp8blk", "nvfp4_gemm_amax", "nvfp4_gemm_split", "nvfp4_gemm_split_workspace", "nvfp4_gemm_split_noalloc",
     "nvfp4_mfma_sustain", "MFMA_SUSTAIN_DECODED", "MFMA_SUSTAIN_RANDOM", "MFMA_SUSTAIN_FP4",
     "nvfp4_bf16_grouped_gemm", "nvfp4_bf16_grouped_gemm_workspace", "AdamWGroup", "nvfp4_adamw", "I8Tensor", "nvfp4_i8_quantize", "nvfp4_i8_gemm",
+    "SOFTMAX", "SIGMOID", "Routing", "nvfp4_route", "nvfp4_route_workspace", "nvfp4_route_backward",
+    "nvfp4_dispatch", "nvfp4_combine", "nvfp4_combine_backward",
+    "nvfp4_rmsnorm", "nvfp4_rmsnorm_i8", "nvfp4_rmsnorm_backward", "nvfp4_rmsnorm_backward_workspace",
+    "ACT_NONE", "ACT_RELU2", "ACT_SILU", "ACT_GELU", "nvfp4_bf16_linear", "nvfp4_bf16_linear_backward",
+    "nvfp4_bf16_linear_backward_workspace",
     "LAYOUT_ROW_MAJOR", "LAYOUT_INTERLEAVED", "interleave_codes", "deinterleave_codes",
     "lib_path", "load_library",
 ]
@@ -45,6 +50,12 @@ DGRAD = 1
 WGRAD = 2
 OUT_BF16 = 0
 OUT_FP32 = 1
+SOFTMAX = 0        # scores of a router
+SIGMOID = 1
+ACT_NONE = 0       # activations of a linear layer
+ACT_RELU2 = 1
+ACT_SILU = 2
+ACT_GELU = 3
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libnvfp4.so"
@@ -138,6 +149,25 @@ def load_library():
         L.nvfp4_i8_quantize.restype = ctypes.c_int
         L.nvfp4_i8_gemm.argtypes = [P, i64, P, P, i64, P, i64, i64, i64, P, i64, i32, P]
         L.nvfp4_i8_gemm.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        L.nvfp4_route.argtypes = [P, i32, i64, i64, i64, i64, P, i64, i64, i32, i32, f32, P, P, P, P, P, P, i64, P]
+        L.nvfp4_route_workspace.argtypes = [i64, i64, ctypes.POINTER(i64)]
+        L.nvfp4_route_backward.argtypes = [P, i32, i64, i64, i64, i64, P, P, P, i32, i32, f32, P, i64, i32, P]
+        L.nvfp4_dispatch.argtypes = [P, i64, P, i64, i64, i64, i64, P, i64, P]
+        L.nvfp4_combine.argtypes = [P, i32, i64, i64, P, P, i64, i64, i64, P, i64, P, i64, i32, P]
+        L.nvfp4_combine_backward.argtypes = [P, i32, i64, P, i32, i64, i64, P, P, i64, i64, i64, P, i64, P, P]
+        L.nvfp4_rmsnorm.argtypes = [P, i32, i64, P, i64, i32, P, i32, f64, i64, i64, P, i64, P, i64, P, i64, P, P]
+        L.nvfp4_rmsnorm_backward.argtypes = [P, i32, i64, P, i64, P, i64, i32, P, i32, f64, i64, i64, P, i64, i32, P, P,
+                                             i64, P]
+        L.nvfp4_rmsnorm_backward_workspace.argtypes = [i64, i64, ctypes.POINTER(i64)]
+        L.nvfp4_bf16_linear.argtypes = [P, i64, P, i64, i64, P, i64, i64, i64, i64, P, i64, i32, i32, P, i64, P, i64, P, i64,
+                                        i32, P, i64, P]
+        L.nvfp4_bf16_linear_backward.argtypes = [P, i32, i64, P, i64, i32, P, i64, i64, i64, P, i64, P, P, i64, P]
+        L.nvfp4_bf16_linear_backward_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+        for name in ("route", "route_workspace", "route_backward", "dispatch", "combine", "combine_backward", "rmsnorm",
+                     "rmsnorm_backward", "rmsnorm_backward_workspace", "bf16_linear", "bf16_linear_backward",
+                     "bf16_linear_backward_workspace"):
+            getattr(L, "nvfp4_" + name).restype = ctypes.c_int
         L.nvfp4_status_string.argtypes = [i32]
         L.nvfp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -1056,6 +1086,453 @@ def nvfp4_i8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
     if st:
         _check(st, "nvfp4_i8_gemm")
     return out
+
+
+# ---- what stands around the expert products ----
+
+def _check_matrix(t, what, index, shape=None, dtypes=(torch.bfloat16, torch.float32)):
+    """A 2-D device tensor with a contiguous last dimension: its address, row
+    pitch and dtype code (index None: any device)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
+        raise TypeError(f"{what}: expected a 2-D CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{what}: on {t.device}, expected cuda:{index}")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{what}: shape {(rows, cols)}, expected {shape}")
+    pitch, step = t.stride()
+    if rows == 0 or cols == 0 or rows == 1:  # the stride of a dimension of one element or none means nothing
+        if step != 1 and cols > 1 and rows > 0:
+            raise ValueError(f"{what}: the last dimension must be contiguous")
+        pitch = _round_up(cols, 16)
+    elif step != 1 and cols > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    elif pitch < cols:
+        raise ValueError(f"{what}: rows overlap")
+    return t.data_ptr(), pitch, OUT_FP32 if t.dtype == torch.float32 else OUT_BF16
+
+
+def _check_dense(t, what, index, dtype, shape):
+    """A contiguous device tensor of one dtype and shape: its address."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype):
+        raise TypeError(f"{what}: expected a {dtype} CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{what}: on {t.device}, expected cuda:{index}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    return t.data_ptr()
+
+
+def _workspace(given, need, device, stream):
+    """The caller's workspace (uint8), or a new one of `need` bytes: (tensor, address, bytes)."""
+    if given is not None:
+        _check_buf(given, "workspace", device, torch.uint8, (need,))
+    elif need:
+        given = _empty(need, torch.uint8, device, stream)
+    return (None, None, 0) if given is None else (given, given.data_ptr(), given.numel())
+
+
+def _asked(query, *args):
+    """What a workspace query of the library answers."""
+    need = ctypes.c_int64(0)
+    st = getattr(load_library(), query)(*args, ctypes.byref(need))
+    if st:
+        _check(st, query)
+    return need.value
+
+
+def nvfp4_route_workspace(T, E):
+    """Workspace bytes of nvfp4_route (0 for up to 64 tokens)."""
+    return _asked("nvfp4_route_workspace", T, E)
+
+
+class Routing:
+    """What a router decided for T tokens, k of E experts each.
+
+    experts  int32 [T, k]    the chosen, best first; -1: none
+    weights  float32 [T, k]
+    rows     int32 [T, k]    each slot's row in the experts' order; -1: none
+    ends     int32 [E]       one past each expert's last row (what the grouped products take)
+    scores   float32 [T, E] or None
+    workspace  uint8, or None (what nvfp4_route needs for as many tokens)
+    """
+
+    def __init__(self, experts, weights, rows, ends, scores=None, workspace=None):
+        self.experts, self.weights, self.rows, self.ends = experts, weights, rows, ends
+        self.scores, self.workspace = scores, workspace
+
+    @classmethod
+    def empty(cls, T, E, k, device, with_scores=False, stream=None):
+        """Buffers for nvfp4_route(..., out=), which a layer may keep from batch to batch."""
+        need = nvfp4_route_workspace(T, E)
+        return cls(_empty((T, k), torch.int32, device, stream), _empty((T, k), torch.float32, device, stream),
+                   _empty((T, k), torch.int32, device, stream), _empty(E, torch.int32, device, stream),
+                   _empty((T, E), torch.float32, device, stream) if with_scores else None,
+                   _empty(need, torch.uint8, device, stream) if need else None)
+
+
+def nvfp4_route(logits, k, score=SOFTMAX, bias=None, groups=1, groups_kept=None, renormalise=True, scale=1.0,
+                with_scores=False, out=None, stream=None):
+    """Experts, weights and row order of T tokens from their logits T x E (see
+    nvfp4_route in nvfp4.h): a Routing.
+
+    bias: float32 [E], for the choice alone.  groups_kept: None keeps all groups.
+    out: a Routing to write (its scores too, if it has them); its workspace is used.
+    """
+    ptr, ld, code = _check_matrix(logits, "logits", None)
+    (T, E), index, device = logits.shape, logits.get_device(), logits.device
+    if bias is not None:
+        bias_ptr = _check_dense(bias, "bias", index, torch.float32, (E,))
+    if out is None:
+        out = Routing.empty(T, E, k, device, with_scores, stream)
+        workspace = out.workspace
+    else:
+        if not isinstance(out, Routing):
+            raise TypeError("out: expected a Routing")
+        _check_dense(out.experts, "out.experts", index, torch.int32, (T, k))
+        _check_dense(out.weights, "out.weights", index, torch.float32, (T, k))
+        _check_dense(out.rows, "out.rows", index, torch.int32, (T, k))
+        _check_dense(out.ends, "out.ends", index, torch.int32, (E,))
+        if out.scores is not None:
+            _check_dense(out.scores, "out.scores", index, torch.float32, (T, E))
+        elif with_scores:
+            raise ValueError("out: a Routing without scores")
+        workspace = out.workspace
+        if workspace is not None or T > 64:
+            workspace = _workspace(workspace, nvfp4_route_workspace(T, E), device, stream)[0]
+    scores = out.scores
+    st = load_library().nvfp4_route(ptr, code, ld, T, E, k, None if bias is None else bias_ptr, groups,
+                                    groups if groups_kept is None else groups_kept, score, 1 if renormalise else 0, scale,
+                                    out.experts.data_ptr(), out.weights.data_ptr(), out.rows.data_ptr(),
+                                    out.ends.data_ptr(), None if scores is None else scores.data_ptr(),
+                                    None if workspace is None else workspace.data_ptr(),
+                                    0 if workspace is None else workspace.numel(), _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, logits, bias, out.experts, out.weights, out.rows, out.ends, scores, workspace)
+    if st:
+        _check(st, "nvfp4_route")
+    return out
+
+
+def nvfp4_route_backward(logits, experts, dweights, score=SOFTMAX, renormalise=True, scale=1.0, dscores=None,
+                         out_dtype=torch.float32, out=None, stream=None):
+    """Gradients of the logits T x E from those of the chosen weights T x k and,
+    optionally, of all scores (see nvfp4_route_backward in nvfp4.h)."""
+    ptr, ld, code = _check_matrix(logits, "logits", None)
+    (T, E), index = logits.shape, logits.get_device()
+    if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
+        raise TypeError("experts: expected a 2-D int32 CUDA tensor")
+    k = experts.shape[1]
+    experts_ptr = _check_dense(experts, "experts", index, torch.int32, (T, k))
+    dweights_ptr = _check_dense(dweights, "dweights", index, torch.float32, (T, k))
+    dscores_ptr = None if dscores is None else _check_dense(dscores, "dscores", index, torch.float32, (T, E))
+    if out is None:
+        out_code, ld_out = _out_code(out_dtype), E
+        out = _empty((T, E), out_dtype, logits.device, stream)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr, ld_out, out_code = _check_matrix(out, "out", index, (T, E))
+    st = load_library().nvfp4_route_backward(ptr, code, ld, T, E, k, experts_ptr, dweights_ptr, dscores_ptr, score,
+                                             1 if renormalise else 0, scale, out_ptr, ld_out, out_code,
+                                             _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, logits, experts, dweights, dscores, out)
+    if st:
+        _check(st, "nvfp4_route_backward")
+    return out
+
+
+def _check_places(rows, index):
+    if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
+        raise TypeError("rows: expected a 2-D int32 CUDA tensor")
+    return _check_dense(rows, "rows", index, torch.int32, rows.shape)
+
+
+def nvfp4_dispatch(x, rows, out=None, stream=None):
+    """Tokens (bf16 T x cols) into the experts' order, out[rows[t, j]] = x[t]
+    (see nvfp4_dispatch in nvfp4.h): bf16, T k rows, or as many as `out` has.
+    Rows that no slot names are left as they are (in a new tensor: undefined)."""
+    ptr, ld, _ = _check_matrix(x, "x", None, dtypes=(torch.bfloat16,))
+    (T, cols), index = x.shape, x.get_device()
+    rows_ptr = _check_places(rows, index)
+    if rows.shape[0] != T:
+        raise ValueError(f"rows: {rows.shape[0]} tokens, x has {T}")
+    k = rows.shape[1]
+    if out is None:
+        out = _empty((T * k, cols), torch.bfloat16, x.device, stream)
+    out_ptr, ld_out, _ = _check_matrix(out, "out", index, dtypes=(torch.bfloat16,))
+    if out.shape[1] != cols:
+        raise ValueError(f"out: {out.shape[1]} columns, x has {cols}")
+    st = load_library().nvfp4_dispatch(ptr, ld, rows_ptr, T, k, cols, out.shape[0], out_ptr, ld_out, _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, x, rows, out)
+    if st:
+        _check(st, "nvfp4_dispatch")
+    return out
+
+
+def nvfp4_combine(o, rows, weights=None, residual=None, out_dtype=torch.bfloat16, out=None, stream=None):
+    """The experts' rows back to the tokens, residual[t] + sum_j weights[t, j]
+    o[rows[t, j]] (see nvfp4_combine in nvfp4.h): T x cols.  Without weights it is
+    also the gradient of nvfp4_dispatch."""
+    ptr, ld, code = _check_matrix(o, "o", None)
+    (R, cols), index = o.shape, o.get_device()
+    rows_ptr = _check_places(rows, index)
+    T, k = rows.shape
+    weights_ptr = None if weights is None else _check_dense(weights, "weights", index, torch.float32, (T, k))
+    if out is None:
+        out = _empty((T, cols), out_dtype, o.device, stream)
+    out_ptr, ld_out, out_code = _check_matrix(out, "out", index, (T, cols))
+    r_ptr, ld_r = None, 0
+    if residual is not None:
+        r_ptr, ld_r, _ = _check_matrix(residual, "residual", index, (T, cols), (out.dtype,))
+    st = load_library().nvfp4_combine(ptr, code, ld, R, rows_ptr, weights_ptr, T, k, cols, r_ptr, ld_r, out_ptr, ld_out,
+                                      out_code, _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, o, rows, weights, residual, out)
+    if st:
+        _check(st, "nvfp4_combine")
+    return out
+
+
+def nvfp4_combine_backward(dy, o, rows, weights, out=None, dweights=None, stream=None):
+    """Gradients of nvfp4_combine: of the experts' rows (bf16, as many as o has;
+    rows that no slot names are left as they are, in a new tensor undefined) and
+    of the weights (float32 T x k).  See nvfp4_combine_backward in nvfp4.h."""
+    ptr, ld, code = _check_matrix(dy, "dy", None)
+    (T, cols), index = dy.shape, dy.get_device()
+    o_ptr, ld_o, o_code = _check_matrix(o, "o", index)
+    R = o.shape[0]
+    rows_ptr = _check_places(rows, index)
+    if rows.shape[0] != T or o.shape[1] != cols:
+        raise ValueError(f"dy: shape {(T, cols)} does not fit rows {tuple(rows.shape)} and o {tuple(o.shape)}")
+    k = rows.shape[1]
+    weights_ptr = _check_dense(weights, "weights", index, torch.float32, (T, k))
+    if out is None:
+        out = _empty((R, cols), torch.bfloat16, dy.device, stream)
+    out_ptr, ld_out, _ = _check_matrix(out, "out", index, (R, cols), (torch.bfloat16,))
+    if dweights is None:
+        dweights = _empty((T, k), torch.float32, dy.device, stream)
+    dweights_ptr = _check_dense(dweights, "dweights", index, torch.float32, (T, k))
+    st = load_library().nvfp4_combine_backward(ptr, code, ld, o_ptr, o_code, ld_o, R, rows_ptr, weights_ptr, T, k, cols,
+                                               out_ptr, ld_out, dweights_ptr, _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, dy, o, rows, weights, out, dweights)
+    if st:
+        _check(st, "nvfp4_combine_backward")
+    return out, dweights
+
+
+def _check_norm_weight(weight, index, cols):
+    if weight is None:
+        return None, OUT_FP32
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("weight: expected a float32 or bfloat16 CUDA tensor")
+    return _check_dense(weight, "weight", index, weight.dtype, (cols,)), _out_code(weight.dtype)
+
+
+def _rmsnorm(x, weight, eps, residual, h, y, codes, scales, stream, what):
+    ptr, ld, code = _check_matrix(x, "x", None)
+    (rows, cols), index = x.shape, x.get_device()
+    weight_ptr, w_code = _check_norm_weight(weight, index, cols)
+    r_ptr, ld_r, h_ptr, ld_h, s_code = None, 0, None, 0, code
+    if residual is not None:
+        r_ptr, ld_r, s_code = _check_matrix(residual, "residual", index, (rows, cols))
+        if h is None:
+            h = _empty((rows, cols), residual.dtype, x.device, stream)
+    if h is not None:
+        h_ptr, ld_h, h_code = _check_matrix(h, "h", index, (rows, cols))
+        if residual is not None and h_code != s_code:
+            raise TypeError(f"h: dtype {h.dtype}, residual has {residual.dtype}")
+        s_code = h_code
+    y_ptr, ld_y, codes_ptr, ld_codes, scales_ptr = None, 0, None, 0, None
+    if y is not None:
+        y_ptr, ld_y, _ = _check_matrix(y, "out", index, (rows, cols), (torch.bfloat16,))
+    if codes is not None:
+        codes_ptr, ld_codes, _ = _check_matrix(codes, "out.codes", index, (rows, cols), (torch.int8,))
+        scales_ptr = _check_dense(scales, "out.scales", index, torch.float32, (rows,))
+    st = load_library().nvfp4_rmsnorm(ptr, code, ld, r_ptr, ld_r, s_code, weight_ptr, w_code, eps, rows, cols, h_ptr, ld_h,
+                                      y_ptr, ld_y, codes_ptr, ld_codes, scales_ptr, _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, x, weight, residual, h, y, codes, scales)
+    if st:
+        _check(st, what)
+    return h
+
+
+def nvfp4_rmsnorm(x, weight=None, eps=1e-6, residual=None, h=None, out=None, stream=None):
+    """Root-mean-square norm of x + residual (see nvfp4_rmsnorm in nvfp4.h):
+    (bf16 rows, h).  h is the sum, of the residual's dtype: a new tensor, or the
+    one given (which may be residual); None without a residual (unless given)."""
+    if out is None and isinstance(x, torch.Tensor) and x.is_cuda:
+        out = _empty(x.shape, torch.bfloat16, x.device, stream)
+    h = _rmsnorm(x, weight, eps, residual, h, out, None, None, stream, "nvfp4_rmsnorm")
+    return out, h
+
+
+def nvfp4_rmsnorm_i8(x, weight=None, eps=1e-6, residual=None, h=None, out=None, stream=None):
+    """nvfp4_rmsnorm with the normalised rows as int8 and one scale per row: (an
+    I8Tensor, which nvfp4_i8_gemm takes, h)."""
+    if out is None and isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2:
+        out = I8Tensor(_empty(x.shape, torch.int8, x.device, stream), _empty(x.shape[0], torch.float32, x.device, stream))
+    if not isinstance(out, I8Tensor):
+        raise TypeError("out: expected an I8Tensor" if out is not None else "x: expected a 2-D CUDA tensor")
+    h = _rmsnorm(x, weight, eps, residual, h, None, out.codes, out.scales, stream, "nvfp4_rmsnorm")
+    return out, h
+
+
+def nvfp4_rmsnorm_backward_workspace(rows, cols):
+    """Workspace bytes of nvfp4_rmsnorm_backward with a gradient of the weight."""
+    return _asked("nvfp4_rmsnorm_backward_workspace", rows, cols)
+
+
+def nvfp4_rmsnorm_backward(dy, h, weight=None, eps=1e-6, dh=None, out_dtype=torch.bfloat16, out=None, dweight=None,
+                           workspace=None, stream=None):
+    """Gradients of nvfp4_rmsnorm (see nvfp4_rmsnorm_backward in nvfp4.h): (dx,
+    dweight), dx that of x and of the residual alike, dweight float32 [cols]
+    (None without a weight).  h: what the norm was taken of; dh: the gradient
+    that reaches h otherwise, of h's dtype."""
+    ptr, ld, code = _check_matrix(dy, "dy", None)
+    (rows, cols), index, device = dy.shape, dy.get_device(), dy.device
+    h_ptr, ld_h, s_code = _check_matrix(h, "h", index, (rows, cols))
+    dh_ptr, ld_dh = None, 0
+    if dh is not None:
+        dh_ptr, ld_dh, _ = _check_matrix(dh, "dh", index, (rows, cols), (h.dtype,))
+    weight_ptr, w_code = _check_norm_weight(weight, index, cols)
+    if out is None:
+        out = _empty((rows, cols), out_dtype, device, stream)
+    out_ptr, ld_out, out_code = _check_matrix(out, "out", index, (rows, cols))
+    dweight_ptr, ws, ws_ptr, ws_bytes = None, None, None, 0
+    if weight is not None or dweight is not None:
+        if dweight is None:
+            dweight = _empty(cols, torch.float32, device, stream)
+        dweight_ptr = _check_dense(dweight, "dweight", index, torch.float32, (cols,))
+        ws, ws_ptr, ws_bytes = _workspace(workspace, nvfp4_rmsnorm_backward_workspace(rows, cols), device, stream)
+    st = load_library().nvfp4_rmsnorm_backward(ptr, code, ld, h_ptr, ld_h, dh_ptr, ld_dh, s_code, weight_ptr, w_code, eps,
+                                               rows, cols, out_ptr, ld_out, out_code, dweight_ptr, ws_ptr, ws_bytes,
+                                               _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, dy, h, dh, weight, out, dweight, ws)
+    if st:
+        _check(st, "nvfp4_rmsnorm_backward")
+    return out, dweight
+
+
+def _check_ends(ends, index):
+    if not isinstance(ends, torch.Tensor) or ends.dtype != torch.int32 or ends.dim() != 1 or not ends.is_cuda or \
+            ends.get_device() != index or not ends.is_contiguous():
+        raise ValueError("ends: expected a contiguous 1-D int32 tensor on the operands' device")
+    return ends.shape[0]
+
+
+def nvfp4_bf16_linear(x, w, ends=None, bias=None, activation=ACT_NONE, residual=None, with_pre=False, pre=None,
+                      out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """act(x w^T + bias) + residual (see nvfp4_bf16_linear in nvfp4.h): T x N, or
+    (that, pre) with `with_pre` or a tensor `pre`: the bf16 sums before the
+    activation, which the backward pass takes.
+
+    w: bf16 N x K, or with `ends` (int32 [E], as nvfp4_bf16_grouped_gemm) E x N x
+    K; bias: float32 or bfloat16 of w's leading dimensions; residual: T x N of
+    the output's dtype.  workspace: as for nvfp4_bf16_grouped_gemm.
+    """
+    ptr, ldx, _ = _check_matrix(x, "x", None, dtypes=(torch.bfloat16,))
+    (T, K), index, device = x.shape, x.get_device(), x.device
+    ends_ptr = None
+    if ends is None:
+        if not (isinstance(w, torch.Tensor) and w.is_cuda and w.dtype == torch.bfloat16 and w.dim() == 2):
+            raise TypeError("w: expected a 2-D bfloat16 CUDA tensor")
+        w_ptr, ldw, _ = _check_matrix(w, "w", index)
+        E, N, stride_w, lead = 1, w.shape[0], 0, w.shape[:1]
+    else:
+        E = _check_ends(ends, index)
+        _check_bf16_experts(w, "w")
+        if w.shape[0] != E:
+            raise ValueError(f"w: {w.shape[0]} experts, ends has {E}")
+        if w.get_device() != index:
+            raise ValueError(f"w: on {w.device}, expected {device}")
+        ends_ptr, w_ptr, N, lead = ends.data_ptr(), w.data_ptr(), w.shape[1], w.shape[:2]
+        ldw = w.stride(1) if N > 1 and K > 0 else _round_up(K, 8)
+        stride_w = w.stride(0) if E > 1 and N > 0 and K > 0 else N * ldw
+    if w.shape[-1] != K:
+        raise ValueError(f"w: {w.shape[-1]} columns, x has {K}")
+    if N % 8 or K % 8:
+        raise ValueError(f"N = {N} and K = {K} must be multiples of 8")
+    bias_ptr, bias_code = None, OUT_FP32
+    if bias is not None:
+        bias_code = _out_code(bias.dtype, "bias") if isinstance(bias, torch.Tensor) else OUT_FP32
+        bias_ptr = _check_dense(bias, "bias", index, torch.float32 if bias_code == OUT_FP32 else torch.bfloat16, lead)
+    if out is None:
+        out = _empty((T, N), out_dtype, device, stream)
+    out_ptr, ldc, out_code = _check_matrix(out, "out", index, (T, N))
+    r_ptr, ld_r, pre_ptr, ld_pre = None, 0, None, 0
+    if residual is not None:
+        r_ptr, ld_r, _ = _check_matrix(residual, "residual", index, (T, N), (out.dtype,))
+    if pre is None and with_pre:
+        pre = _empty((T, N), torch.bfloat16, device, stream)
+    if pre is not None:
+        pre_ptr, ld_pre, _ = _check_matrix(pre, "pre", index, (T, N), (torch.bfloat16,))
+    if workspace is not None:
+        _check_buf(workspace, "workspace", device, torch.uint8, (0,))
+    elif K >= _SPLIT_FROM:
+        need = nvfp4_bf16_grouped_gemm_workspace(FPROP, E, T, N, K)
+        if need:
+            workspace = _empty(need, torch.uint8, device, stream)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    st = load_library().nvfp4_bf16_linear(ptr, ldx, w_ptr, ldw, stride_w, ends_ptr, E, T, N, K, bias_ptr, N, bias_code,
+                                          activation, r_ptr, ld_r, pre_ptr, ld_pre, out_ptr, ldc, out_code, ws, ws_bytes,
+                                          _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, x, w, ends, bias, residual, pre, out, workspace)
+    if st:
+        _check(st, "nvfp4_bf16_linear")
+    return out if pre is None else (out, pre)
+
+
+def nvfp4_bf16_linear_backward_workspace(E, T, N):
+    """Workspace bytes of nvfp4_bf16_linear_backward with a gradient of the bias."""
+    return _asked("nvfp4_bf16_linear_backward_workspace", E, T, N)
+
+
+def nvfp4_bf16_linear_backward(dy, pre, activation=ACT_NONE, ends=None, with_bias=True, out=None, dbias=None,
+                               workspace=None, stream=None):
+    """Gradients through the epilogue of nvfp4_bf16_linear (see
+    nvfp4_bf16_linear_backward in nvfp4.h): (dpre, dbias), dpre bf16 T x N, what the
+    DGRAD and WGRAD products take, dbias float32 [N], with `ends` [E, N] (None
+    unless with_bias).  pre None with ACT_NONE: dpre is dy itself."""
+    ptr, ld, code = _check_matrix(dy, "dy", None)
+    (T, N), index, device = dy.shape, dy.get_device(), dy.device
+    pre_ptr, ld_pre, out_ptr, ld_out = None, 0, None, 0
+    if pre is not None:
+        pre_ptr, ld_pre, _ = _check_matrix(pre, "pre", index, (T, N), (torch.bfloat16,))
+        if out is None:
+            out = _empty((T, N), torch.bfloat16, device, stream)
+        out_ptr, ld_out, _ = _check_matrix(out, "out", index, (T, N), (torch.bfloat16,))
+    elif activation != ACT_NONE:
+        raise ValueError("pre: needed with an activation")
+    elif out is not None:
+        raise ValueError("out: without pre the gradient is dy itself")
+    E = 1 if ends is None else _check_ends(ends, index)
+    dbias_ptr, ws, ws_ptr, ws_bytes = None, None, None, 0
+    if with_bias or dbias is not None:
+        shape = (N,) if ends is None else (E, N)
+        if dbias is None:
+            dbias = _empty(shape, torch.float32, device, stream)
+        dbias_ptr = _check_dense(dbias, "dbias", index, torch.float32, shape)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, nvfp4_bf16_linear_backward_workspace(E, T, N), device, stream)
+    elif pre is None:
+        return dy, None
+    st = load_library().nvfp4_bf16_linear_backward(ptr, code, ld, pre_ptr, ld_pre, activation,
+                                                   None if ends is None else ends.data_ptr(), E, T, N, out_ptr, ld_out,
+                                                   dbias_ptr, ws_ptr, ws_bytes, _raw_stream(stream))
+    if stream is not None:
+        _used_on(stream, dy, pre, ends, out, dbias, ws)
+    if st:
+        _check(st, "nvfp4_bf16_linear_backward")
+    return (dy if pre is None else out), dbias
 
 
 MFMA_SUSTAIN_DECODED, MFMA_SUSTAIN_RANDOM, MFMA_SUSTAIN_FP4 = 0, 1, 2

@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_fp8blk.hip", "gemm_rows.hip", "quantize_i8.hip",
-           "adamw.hip"]
+           "adamw.hip", "api_layer.hip", "route.hip", "move_rows.hip", "norm.hip", "linear_backward.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -9,14 +9,19 @@
 #include <mutex>
 
 #include "nvfp4.h"
+#include "api_common.hpp"
 #include "internal.hpp"
 
 namespace {
 
+using nvfp4::aligned;
+using nvfp4::check_grouped;
+using nvfp4::device_cus;
 using nvfp4::GemmOperand;
+using nvfp4::holds;
+using nvfp4::kMostBigTiles;
+using nvfp4::launch_status;
 using nvfp4::QOut;
-
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
@@ -31,12 +36,6 @@ int check_layout(const nvfp4_tensor* t, bool with_t)
 }
 
 inline bool interleaved(const nvfp4_tensor* t) { return t->layout == NVFP4_LAYOUT_INTERLEAVED; }
-
-int launch_status()
-{
-    hipError_t e = hipGetLastError();
-    return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH;
-}
 
 // Checks of an output descriptor for a rows x cols NVFP4 tensor.
 int check_out(const nvfp4_tensor* o, int64_t rows, int64_t cols, int block)
@@ -398,15 +397,6 @@ int gemm_nvfp4(int32_t pass, const nvfp4_tensor* a, const nvfp4_tensor* b, void*
     return launch_status();
 }
 
-// Compute units of the current device (the tail split sizes its parts to them).
-int device_cus()
-{
-    int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
-    return n;
-}
-
 // The tail-split GEMM on a workspace of ws_bytes (or, with ws_bytes < 0, just
 // the size it needs in *need).
 int gemm_split(int32_t pass, const nvfp4_tensor* a, const nvfp4_tensor* b, void* c, int64_t ldc,
@@ -642,10 +632,6 @@ int nvfp4_mfma_sustain(int64_t blocks, int64_t iters, int32_t operands, float* o
 
 namespace {
 
-// Tiles of 256 x 256 outputs that one grid holds: 512 threads each, and a
-// grid has fewer than 2^32 threads.
-constexpr int64_t kMostBigTiles = int64_t(1) << 22;
-
 // nvfp4_adamw: one launch takes up to kAdamWTensors tensors and 2^23
 // workgroups (a tensor has at most 2^33 elements, that many workgroups).
 constexpr int64_t kMostChunks = int64_t(1) << 23;
@@ -655,27 +641,6 @@ bool adamw_vec(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight
 {
     return aligned(t.p, p_bf16 ? 8 : 16) && aligned(t.g, g_bf16 ? 8 : 16) && aligned(t.m, eight ? 4 : 16) &&
            aligned(t.v, eight ? 4 : 16) && aligned(t.copy, 8);
-}
-
-// Whether `stride` elements hold `rows` rows of `cols`, `ld` apart (ld >= cols
-// >= 0; ld * rows may pass 64 bits).
-bool holds(int64_t stride, int64_t rows, int64_t ld, int64_t cols)
-{
-    if (rows == 0) return stride >= 0;
-    return stride >= cols && (rows == 1 || (stride - cols) / (rows - 1) >= ld);
-}
-
-// Pass and sizes of a grouped product.
-int check_grouped(int32_t pass, int64_t E, int64_t T, int64_t N, int64_t K)
-{
-    if (pass != NVFP4_FPROP && pass != NVFP4_DGRAD && pass != NVFP4_WGRAD) return NVFP4_ERR_MODE;
-    if (E < 0 || T < 0 || N < 0 || K < 0 || N % 8 || K % 8) return NVFP4_ERR_SHAPE;
-    const int64_t lim = int64_t(1) << 31;
-    if (E >= lim || T >= lim || N >= lim || K >= lim) return NVFP4_ERR_SHAPE;
-    const int64_t cols = pass == NVFP4_FPROP ? N : K;
-    const int64_t row_tiles = pass == NVFP4_WGRAD ? E * ((N + 255) / 256) : T / 256 + E + 1;
-    const int64_t col_tiles = (cols + 255) / 256;  // (the product of the two may pass 64 bits)
-    return col_tiles == 0 || row_tiles <= (kMostBigTiles - 1) / col_tiles ? NVFP4_OK : NVFP4_ERR_SHAPE;
 }
 
 int check_adamw(const nvfp4_adamw_tensor& t, bool p_bf16, bool g_bf16, bool eight)

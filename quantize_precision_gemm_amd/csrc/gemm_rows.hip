@@ -26,6 +26,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "activation.hpp"
 #include "internal.hpp"
 #include "nvfp4_device.hpp"
 
@@ -115,12 +116,14 @@ __device__ __forceinline__ int wave_scan(int v, int none, const Op& op)
 
 // Rows [begin, end) of the experts e0 + lane, in order and range whatever the
 // ends hold; the rows behind the last expert count as expert E's.  prev: the
-// end before e0's rows, and then the last lane's.
+// end before e0's rows, and then the last lane's.  kDense: one expert owns all
+// rows, and there are no ends.
+template <bool kDense>
 __device__ __forceinline__ void lane_rows(const int32_t* __restrict__ ends, int64_t E, int64_t T, int64_t e0, int& prev,
                                           int& begin, int& end)
 {
     const int64_t e = e0 + (threadIdx.x & 63);
-    end = e < E ? min(max(ends[e], 0), (int)T) : (int)T;
+    end = !kDense && e < E ? min(max(ends[e], 0), (int)T) : (int)T;
     end = wave_scan(max(end, prev), 0, [](int x, int y) { return max(x, y); });
     begin = __builtin_amdgcn_update_dpp(prev, end, 0x138, 0xF, 0xF, false);  // the lane before's end
     prev = __builtin_amdgcn_readlane(end, 63);
@@ -129,7 +132,7 @@ __device__ __forceinline__ void lane_rows(const int32_t* __restrict__ ends, int6
 // One of the tiles of kRows rows of all experts, each row tile counting
 // `cols` times, expert by expert: the one that order(total, at) chooses.
 // False if it chooses none.  Each wave scans the ends, 64 at a time.
-template <int kRows, class Order>
+template <int kRows, bool kDense = false, class Order>
 __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ ends, int64_t E, int64_t T, int cols,
                                           const Order& order, Slice& s)
 {
@@ -140,7 +143,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ ends, int6
         int prev = 0, begin, end;
         uint32_t before = 0;  // tiles of the experts before this chunk
         for (int64_t e0 = 0; e0 <= E; e0 += 64) {
-            lane_rows(ends, E, T, e0, prev, begin, end);
+            lane_rows<kDense>(ends, E, T, e0, prev, begin, end);
             const int own = (end - begin + kRows - 1) / kRows * cols;
             const int upto = wave_scan(own, 0, add);
             const int all = __builtin_amdgcn_readlane(upto, 63);
@@ -820,8 +823,111 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
     }
 }
 
+// A linear layer's epilogue for the rows of one expert, 4 neighbouring columns
+// at a time: pre = v + bias, c = act(pre) + residual.  Rows of no expert get zeros.
+template <bool kF32>
+struct Finish {
+    static constexpr bool kWhole = true;
+    typedef typename std::conditional<kF32, uint4, uint2>::type Raw;  // 4 values of c's type
+    Epilogue ep;
+    int64_t e, begin;  // the expert, its first row
+    bool none;
+
+    __device__ __forceinline__ void bias_of(int64_t n, float (&b)[4]) const
+    {
+        b[0] = b[1] = b[2] = b[3] = 0.0f;
+        if (!ep.bias || none) return;
+        const int64_t at = e * ep.bias_expert + n;
+        if (ep.bias_f32) {
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(ep.bias) + at);
+            b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(ep.bias) + at);
+            b[0] = bf16_lo(v.x), b[1] = bf16_hi(v.x), b[2] = bf16_lo(v.y), b[3] = bf16_hi(v.y);
+        }
+    }
+    __device__ __forceinline__ Raw residual_at(int64_t m, int64_t n) const  // m: row of the expert
+    {
+        Raw r = {};
+        if (ep.residual && !none)
+            r = *reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(ep.residual) +
+                                              ((begin + m) * ep.ld_residual + n) * (kF32 ? 4 : 2));
+        return r;
+    }
+    __device__ __forceinline__ void store(int64_t m, int64_t n, const float (&v)[4], const float (&b)[4], const Raw& r,
+                                          void* c, int64_t ldc) const
+    {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = none ? 0.0f : v[j] + b[j];
+        if (ep.pre)
+            *reinterpret_cast<uint2*>(ep.pre + (begin + m) * ep.ld_pre + n) =
+                make_uint2(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]));
+        const int64_t at = (begin + m) * ldc + n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = activation(ep.act, y[j]);
+        if constexpr (kF32) {
+            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] += ep.residual ? __uint_as_float(w[j]) : 0.0f;
+            *reinterpret_cast<float4*>(static_cast<float*>(c) + at) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+            const float w[4] = {bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] += ep.residual ? w[j] : 0.0f;
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c) + at) =
+                make_uint2(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]));
+        }
+    }
+};
+
+// store_wave with an epilogue: the sums are staged unrounded, 32 columns at a
+// time, and finished by the lane that stores them (rows of 32 columns: 64
+// bytes of bf16).  N is a multiple of 8, so a lane's 4 columns are all there or none.
+template <bool kF32, class Value>
+__device__ __forceinline__ void store_wave_finished(uint8_t* stage, int64_t row0, const int64_t (&col)[2], int64_t mend,
+                                                    int64_t N, void* c, int64_t ldc, const Finish<kF32>& f,
+                                                    const Value& value)
+{
+    const int lane = threadIdx.x & 63, g = lane >> 5, p = lane & 7;
+    if (row0 >= mend) return;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int64_t n = col[u] + 4 * p;
+        const bool in = n < N;
+        float b[4];
+        f.bias_of(in ? n : 0, b);
+        typename Finish<kF32>::Raw r[8];
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+            const int64_t m = row0 + 8 * it + (lane >> 3);
+            r[it] = typename Finish<kF32>::Raw{};
+            if (in && m < mend) r[it] = f.residual_at(m, n);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = 32 * i + (lane & 31);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<float4*>(stage + 128 * row + (((2 * q + g) ^ (row & 7)) << 4)) =
+                    make_float4(value(i, u, 4 * q), value(i, u, 4 * q + 1), value(i, u, 4 * q + 2), value(i, u, 4 * q + 3));
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+            const int row = 8 * it + (lane >> 3);
+            const float4 v = *reinterpret_cast<const float4*>(stage + 128 * row + ((p ^ (row & 7)) << 4));
+            if (!in || row0 + row >= mend) continue;
+            const float y[4] = {v.x, v.y, v.z, v.w};
+            f.store(row0 + row, n, y, b, r[it], c, ldc);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 // Sums as they are.
 struct Plain {
+    static constexpr bool kWhole = false;  // (a converter of values, not a whole epilogue)
     __device__ __forceinline__ void row(int, int64_t) {}
     __device__ __forceinline__ void columns(int, int64_t, int) {}
     __device__ __forceinline__ float operator()(float v, int, int, int) const { return v; }
@@ -829,6 +935,7 @@ struct Plain {
 
 // Integer sums times the scales of their row and column.
 struct Scaled {
+    static constexpr bool kWhole = false;
     const float *sa, *sb;
     int64_t M, N;
     float rows[2], cols[2][16];
@@ -866,17 +973,25 @@ __device__ __forceinline__ void tile(const View& A, const View& B, int64_t m0, i
             Acc acc[2][2][2] = {};  // [half of A][half of B][32 rows]
             if (steps > 0) big_tile<Acc, kTA, kTB>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
             const int64_t col[2] = {n0 + column0<kTB>(wn, 0), n0 + column0<kTB>(wn, 1)};
+            if constexpr (Convert::kWhole) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) convert.columns(k, col[k], 4 * (lane >> 5));
+                for (int h = 0; h < 2; ++h)
+                    store_wave_finished(lds + 8192 * wave, m0 + 128 * h + 64 * wm, col, mend, B.rows, c, ldc, convert,
+                                        [&](int i, int k, int e) { return acc[h][k][i][e]; });
+                return;
+            } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t row0 = m0 + 128 * h + 64 * wm;
+                for (int k = 0; k < 2; ++k) convert.columns(k, col[k], 4 * (lane >> 5));
 #pragma unroll
-                for (int i = 0; i < 2; ++i) convert.row(i, row0 + 32 * i + (lane & 31));
-                store_wave<kF32, kStream>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc,
-                                          [&](int i, int k, int e) { return convert(acc[h][k][i][e], i, k, e); });
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t row0 = m0 + 128 * h + 64 * wm;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) convert.row(i, row0 + 32 * i + (lane & 31));
+                    store_wave<kF32, kStream>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc,
+                                              [&](int i, int k, int e) { return convert(acc[h][k][i][e], i, k, e); });
+                }
+                return;
             }
-            return;
         }
     }
     Acc acc[2][2] = {};  // [32 columns][32 rows]
@@ -885,12 +1000,17 @@ __device__ __forceinline__ void tile(const View& A, const View& B, int64_t m0, i
         else mid_tile<Acc, kTA, kTB>(A, B, m0, n0, Ka, Kb, mend, steps, lds, acc);
     }
     const int64_t row0 = m0 + 64 * wm, col[2] = {n0 + 64 * wn, n0 + 64 * wn + 32};
+    if constexpr (Convert::kWhole) {
+        store_wave_finished(lds + 8192 * wave, row0, col, mend, B.rows, c, ldc, convert,
+                            [&](int i, int k, int e) { return acc[k][i][e]; });
+    } else {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) convert.columns(k, col[k], 4 * (lane >> 5));
+        for (int k = 0; k < 2; ++k) convert.columns(k, col[k], 4 * (lane >> 5));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) convert.row(i, row0 + 32 * i + (lane & 31));
-    store_wave<kF32, kStream>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc,
-                              [&](int i, int k, int e) { return convert(acc[k][i][e], i, k, e); });
+        for (int i = 0; i < 2; ++i) convert.row(i, row0 + 32 * i + (lane & 31));
+        store_wave<kF32, kStream>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc,
+                                  [&](int i, int k, int e) { return convert(acc[k][i][e], i, k, e); });
+    }
 }
 
 // Tile `in` of a product of tm x tn tiles, walked in groups of 8 tile rows,
@@ -952,12 +1072,13 @@ constexpr int kThinN = 1, kThinU = 2;
 struct Place {
     View A, B;
     int64_t m0, n0, mend, Ka, Kb, c_at;
+    int64_t e, begin;  // its expert (E: none) and that one's first row (fprop, dgrad)
     uint32_t at;
     int steps;
 };
 
 // The hw-th tile's; false: there is none.
-template <bool kBig, int kPass>
+template <bool kBig, int kPass, bool kDense = false>
 __device__ __forceinline__ bool place_tile(const GroupedArgs& g, uint32_t hw, Place& t)
 {
     constexpr int kTile = kBig ? 256 : 128;
@@ -983,7 +1104,7 @@ __device__ __forceinline__ bool place_tile(const GroupedArgs& g, uint32_t hw, Pl
             t.at = tile;
             return true;
         };
-        if (!find_tile<kTile>(g.ends, g.E, g.T, tn, order, s)) return false;
+        if (!find_tile<kTile, kDense>(g.ends, g.E, g.T, tn, order, s)) return false;
         grouped_order((int)s.tile, (int)((s.end - s.begin + kTile - 1) / kTile), tn, im, in_);
         const bool none = s.e >= g.E;  // rows of no expert: zeros
         t.A = View{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
@@ -993,6 +1114,8 @@ __device__ __forceinline__ bool place_tile(const GroupedArgs& g, uint32_t hw, Pl
         t.Kb = kPass == 0 ? 2 * K : K;
         t.steps = (int)((K + 63) / 64);
         t.c_at = s.begin * g.ldc;
+        t.e = s.e;
+        t.begin = s.begin;
     }
     t.m0 = (int64_t)kTile * im + (half == 1 ? 128 : 0);
     t.n0 = (int64_t)kTile * in_;
@@ -1021,12 +1144,12 @@ __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_grouped(Grou
 // and 512 x 512 34.7 -> 24.0; dgrad of 300 tokens, 1280 of 5120, 42.4 -> 21.0;
 // fprop of 128 tokens, 1024 of 4096, 32.7 -> 16.9.  The partial tiles are 64 KB
 // each way for 4 steps of 32 KB or more.)
-template <int kPass>
+template <int kPass, bool kDense = false>
 __global__ __launch_bounds__(256, 1) void k_grouped_part(GroupedArgs g)
 {
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLdsBytes];
     Place t;
-    if (!place_tile<false, kPass>(g, blockIdx.x / g.split, t)) return;
+    if (!place_tile<false, kPass, kDense>(g, blockIdx.x / g.split, t)) return;
     const int part = blockIdx.x % g.split;
     const int first = (int)((int64_t)t.steps * part / g.split), last = (int)((int64_t)t.steps * (part + 1) / g.split);
     // a step is 128 bytes of a row, or 64 k rows
@@ -1059,6 +1182,37 @@ __global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs g)
         y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
     }
     store_cols<kF32>(g.c, t.c_at + m * g.ldc + n, n, t.B.rows, y);
+}
+
+// A linear layer's forward product with its epilogue, by the same loops.
+template <bool kBig, bool kF32, bool kDense>
+__global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_linear(GroupedArgs g, Epilogue ep)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLdsBytes];
+    Place t;
+    if (!place_tile<kBig, 0, kDense>(g, blockIdx.x, t)) return;
+    tile<kBig, f32x16_t, false, false, kF32, false>(t.A, t.B, t.m0, t.n0, t.Ka, t.Kb, t.mend, t.steps, lds, g.c, t.c_at,
+                                                    g.ldc, Finish<kF32>{ep, t.e, t.begin, t.e >= g.E});
+}
+
+template <bool kF32, bool kDense>
+__global__ __launch_bounds__(256) void k_linear_join(GroupedArgs g, Epilogue ep)
+{
+    Place t;
+    if (!place_tile<false, 0, kDense>(g, blockIdx.x / (128 / kJoinRows), t)) return;
+    const int r = blockIdx.x % (128 / kJoinRows) * kJoinRows + (threadIdx.x >> 5), c = 4 * (threadIdx.x & 31);
+    const int64_t m = t.m0 + r, n = t.n0 + c;
+    if (m >= t.mend || n >= t.B.rows) return;
+    const Finish<kF32> f{ep, t.e, t.begin, t.e >= g.E};
+    float b[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    f.bias_of(n, b);
+    const auto res = f.residual_at(m, n);
+    const float* part = g.ws + t.at * g.split * kPart + r * 128 + c;
+    for (int i = 0; i < g.split; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)i * kPart);
+        y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
+    }
+    f.store(m, n, y, b, res, g.c, g.ldc);
 }
 
 template <bool kBig, bool kF32>
@@ -1101,6 +1255,29 @@ __global__ __launch_bounds__(256) void k_grouped_thin(GroupedArgs g)
         [&](int64_t m, int64_t n, f32x4_t v) {
             const float y[4] = {v[0], v[1], v[2], v[3]};
             store_cols<kF32>(g.c, c_at + m * g.ldc + n, n, g.N, y);
+        });
+}
+
+template <int kM, bool kF32, bool kDense>
+__global__ __launch_bounds__(256) void k_linear_thin(GroupedArgs g, Epilogue ep)
+{
+    __shared__ f32x4_t lds[4 * kM * kThinN * 64];
+    const int64_t tn = (g.N + 16 * kThinN - 1) / (16 * kThinN);
+    Slice s;
+    const auto order = [&](uint32_t total, uint32_t& at) { return xcd_order(blockIdx.x, total, at); };
+    if (!find_tile<16 * kM, kDense>(g.ends, g.E, g.T, (int)tn, order, s)) return;
+    const bool none = s.e >= g.E;
+    const View A{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
+    const View B{reinterpret_cast<const uint8_t*>(g.b + (none ? 0 : s.e) * g.b_expert), 2 * g.ldb, g.N};
+    const Finish<kF32> f{ep, s.e, s.begin, none};
+    const int tm = (int)((s.end - s.begin + 16 * kM - 1) / (16 * kM));
+    thin_tile<f32x4_t, kM, kThinN, kThinU>(
+        A, B, none ? 0 : 2 * g.K, s.tile % tm * 16 * kM, s.tile / tm * 16 * kThinN, lds,
+        [&](int64_t m, int64_t n, f32x4_t v) {
+            const float y[4] = {v[0], v[1], v[2], v[3]};
+            float b[4];
+            f.bias_of(n, b);
+            f.store(m, n, y, b, f.residual_at(m, n), g.c, g.ldc);
         });
 }
 
@@ -1277,7 +1454,62 @@ void launch_grouped_pass(const GroupedArgs& g0, int64_t ws_bytes, bool out_fp32,
         launch_grouped_tiles<false, kPass>(g, out_fp32, s);
 }
 
+template <bool kBig, bool kDense>
+void launch_linear_tiles(const GroupedArgs& g, const Epilogue& e, bool out_fp32, hipStream_t s)
+{
+    const int64_t t = kBig ? 256 : 128;
+    const dim3 grid((uint32_t)(grouped_grid<0>(g, t, t) + (kBig ? g.cus : 0)));
+    if (out_fp32)
+        hipLaunchKernelGGL((k_linear<kBig, true, kDense>), grid, dim3(kBig ? 512 : 256), 0, s, g, e);
+    else
+        hipLaunchKernelGGL((k_linear<kBig, false, kDense>), grid, dim3(kBig ? 512 : 256), 0, s, g, e);
+}
+
+template <int kM, bool kDense>
+void launch_linear_thin(const GroupedArgs& g, const Epilogue& e, bool out_fp32, hipStream_t s)
+{
+    const dim3 grid((uint32_t)grouped_grid<0>(g, 16 * kM, 16 * kThinN));
+    if (out_fp32)
+        hipLaunchKernelGGL((k_linear_thin<kM, true, kDense>), grid, dim3(256), 0, s, g, e);
+    else
+        hipLaunchKernelGGL((k_linear_thin<kM, false, kDense>), grid, dim3(256), 0, s, g, e);
+}
+
+template <bool kDense>
+void launch_linear_rows(const GroupedArgs& g0, const Epilogue& e, int64_t ws_bytes, bool out_fp32, hipStream_t s)
+{
+    GroupedArgs g = g0;
+    const Plan p = plan_grouped<0>(g);
+    const int64_t grid = grouped_grid<0>(g, 128, 128);
+    if (p.split > 1 && g.ws && ws_bytes >= plan_bytes<0>(g)) {
+        g.split = p.split;
+        hipLaunchKernelGGL((k_grouped_part<0, kDense>), dim3((uint32_t)(grid * p.split)), dim3(256), 0, s, g);
+        const dim3 join((uint32_t)(grid * (128 / kJoinRows)));
+        if (out_fp32)
+            hipLaunchKernelGGL((k_linear_join<true, kDense>), join, dim3(256), 0, s, g, e);
+        else
+            hipLaunchKernelGGL((k_linear_join<false, kDense>), join, dim3(256), 0, s, g, e);
+        return;
+    }
+    if (p.tiles == Tiles::kThin)
+        return p.m == 1 ? launch_linear_thin<1, kDense>(g, e, out_fp32, s)
+               : p.m == 2 ? launch_linear_thin<2, kDense>(g, e, out_fp32, s) : launch_linear_thin<4, kDense>(g, e, out_fp32, s);
+    if (p.tiles == Tiles::kBig)
+        launch_linear_tiles<true, kDense>(g, e, out_fp32, s);
+    else
+        launch_linear_tiles<false, kDense>(g, e, out_fp32, s);
+}
+
 }  // namespace
+
+void launch_linear(const GroupedArgs& g, const Epilogue& e, int64_t ws_bytes, bool out_fp32, hipStream_t s)
+{
+    if (g.T == 0 || g.N == 0) return;  // (an empty contraction still writes what the epilogue makes of zeros)
+    if (g.ends)
+        launch_linear_rows<false>(g, e, ws_bytes, out_fp32, s);
+    else
+        launch_linear_rows<true>(g, e, ws_bytes, out_fp32, s);
+}
 
 int64_t grouped_workspace(int pass, const GroupedArgs& g)
 {

@@ -180,7 +180,128 @@ struct GroupedArgs {
 // The workspace with which launch_grouped may split the contraction (0: it
 // would not); without one, or with less, it does not split.
 int64_t grouped_workspace(int pass, const GroupedArgs& g);
+
+// What becomes of the sums of a linear layer's forward product:
+// pre = sum + bias, c = act(pre) + residual.  Rows are counted in the whole
+// product; rows of no expert get zeros.
+struct Epilogue {
+    const void* bias;      // N values (expert e: at e * bias_expert), or null
+    int64_t bias_expert;
+    bool bias_f32;
+    int act;
+    const void* residual;  // of c's type, or null
+    int64_t ld_residual;
+    uint16_t* pre;         // bf16, or null
+    int64_t ld_pre;
+};
+// g.ends null: one dense layer (E = 1).
+void launch_linear(const GroupedArgs& g, const Epilogue& e, int64_t ws_bytes, bool out_fp32, hipStream_t s);
+
+// Its gradients: dpre = dy act'(pre), dbias the column sums of dpre (expert by
+// expert, or with ends null of all rows).
+struct LinearBackArgs {
+    const void* dy;
+    int64_t ld_dy;
+    bool dy_f32;
+    const uint16_t* pre;  // null: act is none, and dpre is not written
+    int64_t ld_pre;
+    uint16_t* dpre;
+    int64_t ld_dpre;
+    const int32_t* ends;
+    int64_t E, T, N;
+    int act;
+    float* dbias;         // E x N, or null
+    float* parts;         // workspace of linear_backward_workspace bytes (dbias)
+    int cus;
+};
+int64_t linear_backward_workspace(int64_t E, int64_t T, int64_t N, int cus);
+void launch_linear_backward(const LinearBackArgs& a, hipStream_t s);
 void launch_grouped(int pass, const GroupedArgs& g, int64_t ws_bytes, bool out_fp32, hipStream_t s);
+
+// ---- routing to experts ----
+constexpr int kRouteChunk = 64;  // tokens whose places one workgroup counts
+constexpr int kRouteMostExperts = 1024, kRouteMostGroups = 64, kRouteMostK = 16;
+
+struct RouteArgs {
+    const void* logits;  // T rows of E, ld apart
+    int64_t T, ld;
+    const float* bias;   // or null
+    int E, k, groups, kept;
+    bool f32, vec;       // fp32 logits (else bf16); rows suit accesses of 4 values
+    bool sigmoid, renorm;
+    float scale;
+    int* experts;        // T x k
+    float* weights;
+    int* rows;
+    int* ends;           // E, or null: no places are wanted
+    float* scores;       // T x E, or null
+    int* counts;         // workspace of route_workspace bytes
+};
+
+struct RouteBackArgs {
+    RouteArgs f;  // logits, sizes, score and scale, and the chosen experts
+    const float* dweights;  // T x k
+    const float* dscores;   // T x E, or null
+    void* out;
+    int64_t ld_out;
+    bool out_f32, vec_out;
+};
+
+int64_t route_workspace(int64_t T, int64_t E);  // bytes (0: none)
+void launch_route(const RouteArgs& a, hipStream_t s);
+void launch_route_backward(const RouteBackArgs& a, hipStream_t s);
+
+// ---- rows into the experts' order and back ----
+struct MoveArgs {
+    const int* rows;  // T x k places; outside [0, R): none
+    int64_t T, R;
+    int k;
+    int64_t cols;           // a multiple of 8
+    const float* weights;   // T x k, or null
+    const void* tokens;     // dispatch: x; backward: dy; combine: the residual, or null
+    int64_t ld_tokens;
+    bool tokens_f32;
+    const void* from;       // combine, backward: the experts' rows (R rows)
+    int64_t ld_from;
+    bool from_f32;
+    void* out;              // dispatch, backward: R rows, bf16; combine: T rows
+    int64_t ld_out;
+    bool out_f32;
+    float* dweights;        // backward
+};
+constexpr int kMoveMostK = 64;
+void launch_dispatch(const MoveArgs& a, hipStream_t s);
+void launch_combine(const MoveArgs& a, hipStream_t s);
+void launch_combine_backward(const MoveArgs& a, hipStream_t s);
+
+// ---- root-mean-square norm ----
+struct NormArgs {
+    int64_t rows, cols;     // cols a multiple of 8 (int8: 16)
+    const void* x;          // backward: dy
+    int64_t ld_x;
+    const void* residual;   // or null; backward: dh, or null
+    int64_t ld_r;
+    const void* weight;     // or null
+    bool x_f32, s_f32, w_f32;  // s: residual, h (backward: h and dh)
+    float eps;
+    void* h;                // the sum, or null; backward: read
+    int64_t ld_h;
+    uint16_t* y;            // bf16, or null
+    int64_t ld_y;
+    int8_t* codes;          // int8, or null
+    int64_t ld_codes;
+    float* scales;
+    void* dx;               // backward
+    int64_t ld_dx;
+    bool dx_f32;
+    float* dweight;         // or null
+    float* parts;           // workspace of norm_backward_workspace bytes (dweight)
+    int cus;
+};
+constexpr int64_t kNormMostCols = 16384;  // backward: a row is held by 16 waves
+int64_t norm_backward_workspace(int64_t rows, int64_t cols, int cus);
+void launch_norm(const NormArgs& a, hipStream_t s);
+void launch_norm_backward(const NormArgs& a, hipStream_t s);
 
 // Register-only stream of matrix instructions: `blocks` workgroups of 512
 // threads, `iters` rounds of 64 instructions per wave; operands 0 = fp16

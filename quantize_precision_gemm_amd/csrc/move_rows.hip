@@ -1,0 +1,209 @@
+// move_rows.hip -- tokens into the experts' order and back.
+//
+//   dispatch   o[rows[t, j]] = x[t]
+//   combine    y[t] = r[t] + sum_j w[t, j] o[rows[t, j]]
+//   backward   do[rows[t, j]] = w[t, j] dy[t],  dw[t, j] = sum_c dy[t, c] o[rows[t, j], c]
+// Dispatch's backward is combine without weights.  A place outside the rows
+// there are stands for a row of zeros that nobody reads.
+//
+// All three go token by token: a token's k places are scalar loads, its own
+// row moves once, and the experts' rows are whole row pieces wherever they
+// lie.  Sums run over j in order, so no atomic and no order of workgroups
+// shows in a result.  Bound by the bytes of the experts' rows.
+#include "internal.hpp"
+#include "wave.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int64_t kMostBlocks = int64_t(1) << 22;  // of a launch; each takes more tokens beyond that
+
+__device__ __forceinline__ bool inside(int64_t place, int64_t R) { return (uint64_t)place < (uint64_t)R; }
+
+}  // namespace
+
+// A wave moves kPieces x 64 pieces of 16 bytes of one token.
+template <int kPieces>
+__global__ __launch_bounds__(256) void k_dispatch(MoveArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t c0 = 8 * ((int64_t)blockIdx.y * 64 * kPieces + lane);
+    for (int64_t t = (int64_t)blockIdx.x * 4 + wave_index(); t < a.T; t += (int64_t)gridDim.x * 4) {
+        const uint16_t* src = static_cast<const uint16_t*>(a.tokens) + t * a.ld_tokens;
+        uint4 v[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int64_t c = c0 + 512 * i;
+            v[i] = c < a.cols ? *reinterpret_cast<const uint4*>(src + c) : make_uint4(0, 0, 0, 0);
+        }
+        for (int j = 0; j < a.k; ++j) {
+            const int64_t place = a.rows[t * a.k + j];
+            if (!inside(place, a.R)) continue;
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + place * a.ld_out;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int64_t c = c0 + 512 * i;
+                if (c < a.cols) *reinterpret_cast<uint4*>(dst + c) = v[i];
+            }
+        }
+    }
+}
+
+// A wave adds up kPieces x 64 pieces of 8 columns of one token, four of its
+// rows in flight.
+template <int kPieces>
+__global__ __launch_bounds__(256) void k_combine(MoveArgs a)
+{
+    constexpr int kAhead = 4;
+    const int lane = threadIdx.x & 63;
+    const int64_t c0 = 8 * ((int64_t)blockIdx.y * 64 * kPieces + lane);
+    for (int64_t t = (int64_t)blockIdx.x * 4 + wave_index(); t < a.T; t += (int64_t)gridDim.x * 4) {
+        Piece sum[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[i].v[e] = 0.0f;
+        for (int j0 = 0; j0 < a.k; j0 += kAhead) {
+            RawPiece raw[kAhead][kPieces];
+            float w[kAhead];
+            bool there[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const bool in = j0 + u < a.k;
+                const int64_t slot = t * a.k + (in ? j0 + u : j0);
+                const int64_t place = a.rows[slot];
+                there[u] = in && inside(place, a.R);
+                w[u] = !in ? 0.0f : a.weights ? a.weights[slot] : 1.0f;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int64_t c = c0 + 512 * i;
+                    raw[u][i].a = raw[u][i].b = make_uint4(0, 0, 0, 0);
+                    if (there[u] && c < a.cols) raw[u][i] = load_raw(a.from, place * a.ld_from + c, a.from_f32);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const Piece o = widen(raw[u][i], a.from_f32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum[i].v[e] = __builtin_fmaf(w[u], o.v[e], sum[i].v[e]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int64_t c = c0 + 512 * i;
+            if (c >= a.cols) continue;
+            if (a.tokens) {
+                const Piece r = load_piece(a.tokens, t * a.ld_tokens + c, a.out_f32);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[i].v[e] += r.v[e];
+            }
+            store_piece(a.out, t * a.ld_out + c, sum[i], a.out_f32);
+        }
+    }
+}
+
+// kWaves waves a token (4: a workgroup, 1: four tokens a workgroup); dy stays
+// in registers while the token's rows pass by.
+template <int kWaves>
+__global__ __launch_bounds__(256) void k_combine_backward(MoveArgs a)
+{
+    constexpr int kHeld = 4, kLanes = 64 * kWaves;
+    __shared__ float part[kWaves == 4 ? 4 : 1][kMoveMostK];
+    const int lane = kWaves == 4 ? threadIdx.x : threadIdx.x & 63, wave = wave_index();
+    const int64_t each = 4 / kWaves;
+    for (int64_t t = (int64_t)blockIdx.x * each + (kWaves == 4 ? 0 : wave); t < a.T; t += (int64_t)gridDim.x * each) {
+        RawPiece dy[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int64_t c = 8 * (lane + (int64_t)kLanes * i);
+            if (c < a.cols) dy[i] = load_raw(a.tokens, t * a.ld_tokens + c, a.tokens_f32);
+        }
+        for (int j = 0; j < a.k; ++j) {
+            const int64_t place = a.rows[t * a.k + j];
+            float dot = 0.0f;
+            if (inside(place, a.R)) {
+                const float w = a.weights[t * a.k + j];
+                const auto piece = [&](const Piece& d, const Piece& o, int64_t c) {
+                    Piece g;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dot = __builtin_fmaf(d.v[e], o.v[e], dot);
+                        g.v[e] = w * d.v[e];
+                    }
+                    store_piece(a.out, place * a.ld_out + c, g, false);
+                };
+                RawPiece o[kHeld];
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    const int64_t c = 8 * (lane + (int64_t)kLanes * i);
+                    if (c < a.cols) o[i] = load_raw(a.from, place * a.ld_from + c, a.from_f32);
+                }
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    const int64_t c = 8 * (lane + (int64_t)kLanes * i);
+                    if (c < a.cols) piece(widen(dy[i], a.tokens_f32), widen(o[i], a.from_f32), c);
+                }
+                for (int64_t c = 8 * (lane + (int64_t)kLanes * kHeld); c < a.cols; c += 8 * kLanes)
+                    piece(load_piece(a.tokens, t * a.ld_tokens + c, a.tokens_f32),
+                          load_piece(a.from, place * a.ld_from + c, a.from_f32), c);
+            }
+            dot = wave_sum(dot);
+            if constexpr (kWaves == 4) {
+                if ((threadIdx.x & 63) == 0) part[wave][j] = dot;
+            } else {
+                if (lane == 0) a.dweights[t * a.k + j] = dot;
+            }
+        }
+        if constexpr (kWaves == 4) {
+            __syncthreads();
+            if (lane < a.k)
+                a.dweights[t * a.k + lane] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+            __syncthreads();  // part is written again for the next token
+        }
+    }
+}
+
+namespace {
+
+template <class Kernel>
+void launch_pieces(Kernel kernel, int pieces, const MoveArgs& a, hipStream_t s)
+{
+    const int64_t blocks = (a.T + 3) / 4, units = (a.cols / 8 + 64 * pieces - 1) / (64 * pieces);
+    const int64_t most = kMostBlocks / units > 0 ? kMostBlocks / units : 1;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(blocks < most ? blocks : most), (uint32_t)units), dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+void launch_dispatch(const MoveArgs& a, hipStream_t s)
+{
+    if (a.cols > 512)
+        launch_pieces(k_dispatch<2>, 2, a, s);
+    else
+        launch_pieces(k_dispatch<1>, 1, a, s);
+}
+
+void launch_combine(const MoveArgs& a, hipStream_t s)
+{
+    if (a.cols > 512)
+        launch_pieces(k_combine<2>, 2, a, s);
+    else
+        launch_pieces(k_combine<1>, 1, a, s);
+}
+
+void launch_combine_backward(const MoveArgs& a, hipStream_t s)
+{
+    if (a.cols <= 2048) {
+        const int64_t blocks = (a.T + 3) / 4;
+        hipLaunchKernelGGL(k_combine_backward<1>, dim3((uint32_t)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(256),
+                           0, s, a);
+    } else {
+        hipLaunchKernelGGL(k_combine_backward<4>, dim3((uint32_t)(a.T < kMostBlocks ? a.T : kMostBlocks)), dim3(256), 0,
+                           s, a);
+    }
+}
+
+}  // namespace nvfp4

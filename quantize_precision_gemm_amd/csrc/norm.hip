@@ -1,0 +1,304 @@
+// norm.hip -- root-mean-square norm of rows with the residual's addition.
+//
+//   h = x + r,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd w
+//   int8: scale = max|y| / 127, code = rint(127 y / max|y|), ties to even
+//   backward, u = dy w:  dx = rstd (u - h rstd^2 mean(u h)) + dh,
+//                        dw = sum over rows of dy h rstd
+// h is written rounded to its type and normalised unrounded, in fp32; an int8
+// code is rounded from the unrounded y.  A row whose largest |y| is not finite
+// keeps that as its scale, and its codes are 0.
+//
+// Bound by the bytes of x, r, h and y (backward dy, h, dh, dx): a row is read
+// once and stays in registers between its sum and its outputs.
+#include <algorithm>
+
+#include "internal.hpp"
+#include "wave.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int64_t kMostBlocks = int64_t(1) << 22;  // of a launch; each takes more rows beyond that
+constexpr int kHeld = 4;                           // pieces of 8 columns that a lane keeps
+
+__device__ __forceinline__ Piece sum_of(const NormArgs& a, int64_t row, int64_t c)
+{
+    const RawPiece x = load_raw(a.x, row * a.ld_x + c, a.x_f32);
+    Piece h = widen(x, a.x_f32);
+    if (a.residual) {
+        const Piece r = load_piece(a.residual, row * a.ld_r + c, a.s_f32);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h.v[e] += r.v[e];
+    }
+    return h;
+}
+
+// h rstd w in place; the largest |y| so far.
+__device__ __forceinline__ void scale_piece(const NormArgs& a, int64_t c, float rstd, Piece& h, float& top)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h.v[e] *= rstd;
+    if (a.weight) {
+        const Piece w = load_piece(a.weight, c, a.w_f32);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h.v[e] *= w.v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(h.v[e]) & 0x7FFFFFFFu));
+}
+
+// Codes of 8 values; the instruction takes NaN as 0.
+__device__ __forceinline__ uint2 codes_of(const Piece& y, float lift, float factor)
+{
+    uint32_t o[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        uint32_t code;
+        asm("v_cvt_i32_f32 %0, %1" : "=v"(code) : "v"(__builtin_rintf(y.v[e] * lift * factor)));
+        o[e >> 2] |= (code & 0xFFu) << (8 * (e & 3));
+    }
+    return make_uint2(o[0], o[1]);
+}
+
+}  // namespace
+
+// kWaves waves a row (4: a workgroup, 1: four rows a workgroup).
+template <int kWaves, bool kI8>
+__global__ __launch_bounds__(256) void k_norm(NormArgs a)
+{
+    constexpr int kLanes = 64 * kWaves, kRows = 4 / kWaves;
+    __shared__ float part[2][4];
+    const int lane = kWaves == 4 ? threadIdx.x : threadIdx.x & 63, wave = wave_index();
+    const float each = 1.0f / (float)a.cols;
+    for (int64_t row = (int64_t)blockIdx.x * kRows + (kWaves == 4 ? 0 : wave); row < a.rows;
+         row += (int64_t)gridDim.x * kRows) {
+        Piece h[kHeld];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int64_t c = 8 * (lane + (int64_t)kLanes * i);
+            if (c < a.cols) h[i] = sum_of(a, row, c);
+        }
+        const auto square = [&](const Piece& p) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(p.v[e], p.v[e], sum);
+        };
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int64_t c = 8 * (lane + (int64_t)kLanes * i);
+            if (c >= a.cols) continue;
+            square(h[i]);
+            if (a.h) store_piece(a.h, row * a.ld_h + c, h[i], a.s_f32);
+        }
+        const int64_t rest = 8 * (lane + (int64_t)kLanes * kHeld);  // what is not kept is read again
+        for (int64_t c = rest; c < a.cols; c += 8 * kLanes) square(sum_of(a, row, c));
+        sum = wave_sum(sum);
+        if constexpr (kWaves == 4) {
+            if ((threadIdx.x & 63) == 0) part[0][wave] = sum;
+            __syncthreads();
+            sum = (part[0][0] + part[0][1]) + (part[0][2] + part[0][3]);
+        }
+        const float rstd = 1.0f / __builtin_sqrtf(sum * each + a.eps);
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int64_t c = 8 * (lane + (int64_t)kLanes * i);
+            if (c >= a.cols) continue;
+            scale_piece(a, c, rstd, h[i], top);
+            if (a.y) store_piece(a.y, row * a.ld_y + c, h[i], false);
+        }
+        for (int64_t c = rest; c < a.cols; c += 8 * kLanes) {
+            Piece p = sum_of(a, row, c);
+            if (a.h && !kI8) store_piece(a.h, row * a.ld_h + c, p, a.s_f32);  // (h may lie where r does)
+            scale_piece(a, c, rstd, p, top);
+            if (a.y) store_piece(a.y, row * a.ld_y + c, p, false);
+        }
+        if constexpr (kI8) {
+            top = wave_top(top);
+            if constexpr (kWaves == 4) {
+                if ((threadIdx.x & 63) == 0) part[1][wave] = top;
+                __syncthreads();
+                top = __uint_as_float(max(max(__float_as_uint(part[1][0]), __float_as_uint(part[1][1])),
+                                          max(__float_as_uint(part[1][2]), __float_as_uint(part[1][3]))));
+            }
+            if (lane == 0) a.scales[row] = top / 127.0f;
+            // a power of two on both sides of the quotient keeps 127 / max finite
+            const float lift = top < 0x1p-100f ? 0x1p64f : 1.0f;
+            const float factor = top > 0.0f ? 127.0f / (top * lift) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int64_t c = 8 * (lane + (int64_t)kLanes * i);
+                if (c < a.cols) *reinterpret_cast<uint2*>(a.codes + row * a.ld_codes + c) = codes_of(h[i], lift, factor);
+            }
+            for (int64_t c = rest; c < a.cols; c += 8 * kLanes) {
+                Piece p = sum_of(a, row, c);
+                if (a.h) store_piece(a.h, row * a.ld_h + c, p, a.s_f32);
+                scale_piece(a, c, rstd, p, top);
+                *reinterpret_cast<uint2*>(a.codes + row * a.ld_codes + c) = codes_of(p, lift, factor);
+            }
+        } else if constexpr (kWaves == 4) {
+            __syncthreads();  // part[0] is written again for the next row
+        }
+    }
+}
+
+namespace {
+
+// How the backward pass holds rows of `cols` columns: pieces of 8 a lane, waves
+// a row, and the groups of waves that go through the rows.
+struct BackPlan {
+    int held, waves;
+    int64_t groups;
+    bool solo() const { return waves == 1; }
+};
+
+BackPlan back_plan(int64_t rows, int64_t cols, int cus)
+{
+    const int64_t pieces = (cols + 7) / 8;
+    const int held = pieces <= 64 ? 1 : 2;
+    const int waves = (int)((pieces + 64 * held - 1) / (64 * held));
+    const int64_t most = waves == 1 ? 16 * (int64_t)cus : std::max<int64_t>(1, 16 / waves) * cus;
+    return BackPlan{held, waves, std::min(rows, most)};
+}
+
+}  // namespace
+
+template <int kBackHeld, bool kSolo>
+__global__ __launch_bounds__(kSolo ? 256 : 1024) void k_norm_backward(NormArgs a, int groups)
+{
+    __shared__ float part[2][2][16];
+    const int lane = kSolo ? threadIdx.x & 63 : threadIdx.x, lanes = kSolo ? 64 : blockDim.x, wave = wave_index();
+    const int group = kSolo ? blockIdx.x * 4 + wave : blockIdx.x;
+    const float each = 1.0f / (float)a.cols;
+    Piece w[kBackHeld], dw[kBackHeld];
+#pragma unroll
+    for (int i = 0; i < kBackHeld; ++i) {
+        const int64_t c = 8 * (lane + (int64_t)lanes * i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[i].v[e] = 1.0f, dw[i].v[e] = 0.0f;
+        if (a.weight && c < a.cols) w[i] = load_piece(a.weight, c, a.w_f32);
+    }
+    int turn = 0;
+    if (group < groups)
+        for (int64_t row = group; row < a.rows; row += groups, turn ^= 1) {
+            RawPiece dy[kBackHeld], h[kBackHeld], dh[kBackHeld];
+#pragma unroll
+            for (int i = 0; i < kBackHeld; ++i) {
+                const int64_t c = 8 * (lane + (int64_t)lanes * i);
+                dy[i].a = dy[i].b = h[i].a = h[i].b = dh[i].a = dh[i].b = make_uint4(0, 0, 0, 0);
+                if (c < a.cols) {
+                    dy[i] = load_raw(a.x, row * a.ld_x + c, a.x_f32);
+                    h[i] = load_raw(a.h, row * a.ld_h + c, a.s_f32);
+                    if (a.residual) dh[i] = load_raw(a.residual, row * a.ld_r + c, a.s_f32);
+                }
+            }
+            float squares = 0.0f, along = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kBackHeld; ++i) {
+                const Piece d = widen(dy[i], a.x_f32), x = widen(h[i], a.s_f32);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    squares = __builtin_fmaf(x.v[e], x.v[e], squares);
+                    along = __builtin_fmaf(d.v[e] * w[i].v[e], x.v[e], along);
+                }
+            }
+            squares = wave_sum(squares);
+            along = wave_sum(along);
+            if constexpr (!kSolo) {
+                if ((threadIdx.x & 63) == 0) {
+                    part[turn][0][wave] = squares;
+                    part[turn][1][wave] = along;
+                }
+                __syncthreads();  // (the other turn's are read before the next barrier)
+                squares = along = 0.0f;
+                for (int v = 0; v < (int)blockDim.x / 64; ++v) {
+                    squares += part[turn][0][v];
+                    along += part[turn][1][v];
+                }
+            }
+            const float rstd = 1.0f / __builtin_sqrtf(squares * each + a.eps);
+            const float mean = along * each * rstd * rstd;
+#pragma unroll
+            for (int i = 0; i < kBackHeld; ++i) {
+                const int64_t c = 8 * (lane + (int64_t)lanes * i);
+                if (c >= a.cols) continue;
+                const Piece d = widen(dy[i], a.x_f32), x = widen(h[i], a.s_f32), r = widen(dh[i], a.s_f32);
+                Piece o;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dw[i].v[e] = __builtin_fmaf(d.v[e] * rstd, x.v[e], dw[i].v[e]);
+                    o.v[e] = __builtin_fmaf(rstd, __builtin_fmaf(-mean, x.v[e], d.v[e] * w[i].v[e]), r.v[e]);
+                }
+                store_piece(a.dx, row * a.ld_dx + c, o, a.dx_f32);
+            }
+        }
+    if (!a.dweight || group >= groups) return;
+#pragma unroll
+    for (int i = 0; i < kBackHeld; ++i) {
+        const int64_t c = 8 * (lane + (int64_t)lanes * i);
+        if (c < a.cols) store_piece(a.parts, group * a.cols + c, dw[i], true);
+    }
+}
+
+// Column sums of `parts` (groups x cols) in the order of the groups: 32
+// columns a workgroup, 32 runs of the groups.
+__global__ __launch_bounds__(256) void k_column_sums(const float* __restrict__ parts, int64_t groups, int64_t cols,
+                                                     float* __restrict__ out)
+{
+    __shared__ float4 part[32][8];
+    const int q = threadIdx.x & 7, s = threadIdx.x >> 3;
+    const int64_t c = 32 * (int64_t)blockIdx.x + 4 * q;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < cols)
+        for (int64_t g = groups * s / 32, to = groups * (s + 1) / 32; g < to; ++g) {
+            const float4 v = *reinterpret_cast<const float4*>(parts + g * cols + c);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+    part[s][q] = sum;
+    __syncthreads();
+    if (s != 0 || c >= cols) return;
+    for (int j = 1; j < 32; ++j) {
+        const float4 v = part[j][q];
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    *reinterpret_cast<float4*>(out + c) = sum;
+}
+
+void launch_norm(const NormArgs& a, hipStream_t s)
+{
+    if (a.rows == 0) return;
+    const bool solo = a.cols <= 512 * kHeld && (a.cols <= 256 * kHeld || a.rows > 512);
+    const int64_t blocks = solo ? (a.rows + 3) / 4 : a.rows;
+    const dim3 grid((uint32_t)(blocks < kMostBlocks ? blocks : kMostBlocks));
+    if (a.codes) {
+        if (solo) hipLaunchKernelGGL((k_norm<1, true>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((k_norm<4, true>), grid, dim3(256), 0, s, a);
+    } else {
+        if (solo) hipLaunchKernelGGL((k_norm<1, false>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((k_norm<4, false>), grid, dim3(256), 0, s, a);
+    }
+}
+
+int64_t norm_backward_workspace(int64_t rows, int64_t cols, int cus)
+{
+    return back_plan(rows, cols, cus).groups * cols * (int64_t)sizeof(float);
+}
+
+void launch_norm_backward(const NormArgs& a, hipStream_t s)
+{
+    const BackPlan p = back_plan(a.rows, a.cols, a.cus);
+    const int groups = (int)p.groups;
+    if (groups > 0) {
+        const dim3 grid((uint32_t)(p.solo() ? (groups + 3) / 4 : groups)), block((uint32_t)(p.solo() ? 256 : 64 * p.waves));
+        if (p.solo() && p.held == 1) hipLaunchKernelGGL((k_norm_backward<1, true>), grid, block, 0, s, a, groups);
+        else if (p.solo()) hipLaunchKernelGGL((k_norm_backward<2, true>), grid, block, 0, s, a, groups);
+        else hipLaunchKernelGGL((k_norm_backward<2, false>), grid, block, 0, s, a, groups);
+    }
+    if (a.dweight && a.cols > 0)
+        hipLaunchKernelGGL(k_column_sums, dim3((uint32_t)((a.cols + 31) / 32)), dim3(256), 0, s, a.parts, p.groups, a.cols,
+                           a.dweight);
+}
+
+}  // namespace nvfp4

@@ -20,7 +20,7 @@ sys.path.insert(0, ROOT)
 TESTS = ["tests/test_oracle_codecs.py", "tests/test_oracle_quant.py", "tests/test_oracle_philox.py",
          "tests/test_oracle_rht_gemm.py", "tests/test_oracle_rht_sized.py", "tests/test_oracle_mx.py",
          "tests/test_abi.py", "tests/test_binding_checks.py", "tests/test_operator_checks.py",
-         "tests/test_operator_ranges.py"]
+         "tests/test_operator_ranges.py", "tests/test_layer_checks.py"]
 
 
 def main():

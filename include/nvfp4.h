@@ -702,7 +702,7 @@ int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int
  * infinity: a padded token).  A token with a logit that is NaN or plus
  * infinity has weights NaN.
  *   logits    device fp32 or bf16 (l_dtype), T rows of E, ld apart (any ld >= E;
- *             multiples of 4 from 16-byte aligned logits (bf16: 8) are read faster).
+ *             16-byte aligned rows are read faster).
  *   bias      device float, E values, or NULL; it enters the choice alone.
  *   T         0 to 2^27; E 1 to 1024; k 1 to min(16, E / groups * groups_kept);
  *             T k below 2^31; groups 1 to 64, a divisor of E.

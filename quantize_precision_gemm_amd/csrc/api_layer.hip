@@ -56,7 +56,7 @@ nvfp4::RouteArgs route_args(const void* logits, int32_t l_dtype, int64_t ld, int
     a.k = (int)k;
     a.groups = a.kept = 1;
     a.f32 = l_dtype == NVFP4_OUT_FP32;
-    a.vec = ld % 4 == 0 && aligned(logits, a.f32 ? 16 : 8);
+    a.vec = ld % (a.f32 ? 4 : 8) == 0 && aligned(logits, 16);
     a.sigmoid = score == NVFP4_SIGMOID;
     a.renorm = renormalise != 0;
     a.scale = scale;
@@ -119,6 +119,7 @@ int nvfp4_route(const void* logits, int32_t l_dtype, int64_t ld, int64_t T, int6
     if (need > 0 && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
     nvfp4::RouteArgs a = route_args(logits, l_dtype, ld, T, E, k, score, renormalise, scale);
     a.bias = bias;
+    a.vec_bias = aligned(bias, 16);
     a.groups = (int)groups;
     a.kept = (int)groups_kept;
     a.experts = experts;
@@ -126,7 +127,7 @@ int nvfp4_route(const void* logits, int32_t l_dtype, int64_t ld, int64_t T, int6
     a.rows = rows;
     a.ends = ends;
     a.scores = scores;
-    a.counts = static_cast<int*>(workspace);
+    a.counts = static_cast<uint8_t*>(workspace);
     nvfp4::launch_route(a, static_cast<hipStream_t>(stream));
     return launch_status();
 }
@@ -152,6 +153,7 @@ int nvfp4_route_backward(const void* logits, int32_t l_dtype, int64_t ld, int64_
     a.out = dlogits;
     a.ld_out = ld_out;
     a.out_f32 = f32;
+    a.vec_scores = E % 4 == 0 && aligned(dscores, 16);
     a.vec_out = ld_out % 4 == 0 && aligned(dlogits, f32 ? 16 : 8);
     nvfp4::launch_route_backward(a, static_cast<hipStream_t>(stream));
     return launch_status();

@@ -227,7 +227,8 @@ struct RouteArgs {
     int64_t T, ld;
     const float* bias;   // or null
     int E, k, groups, kept;
-    bool f32, vec;       // fp32 logits (else bf16); rows suit accesses of 4 values
+    bool f32, vec;       // fp32 logits (else bf16); rows suit accesses of 16 bytes
+    bool vec_bias;
     bool sigmoid, renorm;
     float scale;
     int* experts;        // T x k
@@ -235,7 +236,8 @@ struct RouteArgs {
     int* rows;
     int* ends;           // E, or null: no places are wanted
     float* scores;       // T x E, or null
-    int* counts;         // workspace of route_workspace bytes
+    uint8_t* counts;     // workspace of route_workspace bytes
+    int pitch, per_group;  // (the launch sets them)
 };
 
 struct RouteBackArgs {
@@ -244,7 +246,7 @@ struct RouteBackArgs {
     const float* dscores;   // T x E, or null
     void* out;
     int64_t ld_out;
-    bool out_f32, vec_out;
+    bool out_f32, vec_out, vec_scores;
 };
 
 int64_t route_workspace(int64_t T, int64_t E);  // bytes (0: none)

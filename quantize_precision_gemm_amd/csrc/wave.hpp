@@ -34,6 +34,14 @@ __device__ __forceinline__ float lane_move(float none, float v)
     return __int_as_float(lane_move<kCtrl, kRows>(__float_as_int(none), __float_as_int(v)));
 }
 
+// v of a lane that there always is (rotations and mirrors); the move becomes
+// part of the instruction that takes its result.
+template <int kCtrl>
+__device__ __forceinline__ int lane_turn(int v)
+{
+    return __builtin_amdgcn_update_dpp(0, v, kCtrl, 0xF, 0xF, true);
+}
+
 // op over all 64 lanes, the same value in each (a scalar register): within rows
 // of 16 by 1, 2, 4, 8 lanes, then the last lane of a row into the next.
 template <class Op>

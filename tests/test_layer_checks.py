@@ -36,7 +36,7 @@ ROUTE = dict(logits=FAKE, ldt=1, ld=64, T=100, E=64, k=4, bias=FAKE, groups=8, k
     ({"logits": None}, -1), ({"experts": None}, -1), ({"weights": None}, -1), ({"rows": None}, -1), ({"ends": None}, -1),
     ({"logits": FAKE + 2}, -3), ({"logits": FAKE + 1, "ldt": 0}, -3), ({"bias": FAKE + 2}, -3), ({"experts": FAKE + 1}, -3),
     ({"weights": FAKE + 2}, -3), ({"rows": FAKE + 2}, -3), ({"ends": FAKE + 3}, -3), ({"scores": FAKE + 2}, -3), ({"ws": FAKE + 8}, -3),
-    ({"ws": None}, -7), ({"wb": 511}, -7), ({"T": 20000, "wb": (313 + 1) * 64 * 4 - 1}, -7),
+    ({"ws": None}, -7), ({"wb": 127}, -7), ({"T": 20000, "wb": 313 * 64 + 314 * 64 * 4 - 1}, -7),
 ])
 def test_route_validation(lib, change, status):
     d = dict(ROUTE, **change)
@@ -45,8 +45,8 @@ def test_route_validation(lib, change, status):
                            d["wb"], None) == status
 
 
-@pytest.mark.parametrize("T,E,want", [(0, 64, 0), (64, 64, 0), (65, 64, 2 * 64 * 4), (16384, 256, 256 * 256 * 4),
-                                      (16385, 256, 258 * 256 * 4)])
+@pytest.mark.parametrize("T,E,want", [(0, 64, 0), (64, 64, 0), (65, 64, 2 * 64), (16384, 200, 256 * 256),
+                                      (16385, 256, 257 * 256 + 258 * 256 * 4)])
 def test_route_workspace(T, E, want):
     assert q.nvfp4_route_workspace(T, E) == want
 

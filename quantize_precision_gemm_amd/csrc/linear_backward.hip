@@ -92,17 +92,16 @@ __global__ __launch_bounds__(256) void k_linear_backward(LinearBackArgs a, int64
     }
 }
 
-// dbias of one expert: its lines in order, 256 columns a workgroup of 4 waves,
-// each a quarter of the lines.
+// dbias of one expert: its lines in order, 64 columns a workgroup, 16 runs of the lines.
 __global__ __launch_bounds__(256) void k_bias_sums(LinearBackArgs a, int64_t each)
 {
-    __shared__ float4 part[4][64];
-    const int lane = threadIdx.x & 63, wave = wave_index();
-    const int64_t e = blockIdx.y, c = 256 * (int64_t)blockIdx.x + 4 * lane;
+    __shared__ float4 part[16][16];
+    const int q = threadIdx.x & 15, s = threadIdx.x >> 4;
+    const int64_t e = blockIdx.y, c = 64 * (int64_t)blockIdx.x + 4 * q;
     int64_t begin = 0, end = a.T;
     if (a.ends) {
         int b = 0;
-        for (int64_t i = lane; i < e; i += 64) b = max(b, a.ends[i]);
+        for (int64_t i = threadIdx.x & 63; i < e; i += 64) b = max(b, a.ends[i]);
         b = (int)wave_max_u32((uint32_t)b);
         begin = min((int64_t)__builtin_amdgcn_readfirstlane(b), a.T);
         end = min((int64_t)__builtin_amdgcn_readfirstlane(a.ends[e]), a.T);
@@ -110,16 +109,18 @@ __global__ __launch_bounds__(256) void k_bias_sums(LinearBackArgs a, int64_t eac
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (end > begin && c < a.N) {
         const int64_t first = begin / each, count = (end - 1) / each - first + 1;
-        for (int64_t i = first + count * wave / 4, to = first + count * (wave + 1) / 4; i < to; ++i) {
+#pragma unroll 4
+        for (int64_t i = first + count * s / 16, to = first + count * (s + 1) / 16; i < to; ++i) {
             const float4 v = *reinterpret_cast<const float4*>(a.parts + (i + e) * a.N + c);
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
     }
-    part[wave][lane] = sum;
+    part[s][q] = sum;
     __syncthreads();
-    if (wave != 0 || c >= a.N) return;
-    for (int w = 1; w < 4; ++w) {
-        const float4 v = part[w][lane];
+    if (s != 0 || c >= a.N) return;
+#pragma unroll
+    for (int j = 1; j < 16; ++j) {
+        const float4 v = part[j][q];
         sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
     }
     *reinterpret_cast<float4*>(a.dbias + e * a.N + c) = sum;
@@ -140,7 +141,7 @@ void launch_linear_backward(const LinearBackArgs& a, hipStream_t s)
         else hipLaunchKernelGGL(k_linear_backward<false>, grid, dim3(256), 0, s, a, each);
     }
     if (a.dbias && a.E > 0)
-        hipLaunchKernelGGL(k_bias_sums, dim3((uint32_t)((a.N + 255) / 256), (uint32_t)a.E), dim3(256), 0, s, a, each);
+        hipLaunchKernelGGL(k_bias_sums, dim3((uint32_t)((a.N + 63) / 64), (uint32_t)a.E), dim3(256), 0, s, a, each);
 }
 
 }  // namespace nvfp4

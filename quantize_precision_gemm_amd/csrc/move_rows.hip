@@ -10,6 +10,8 @@
 // row moves once, and the experts' rows are whole row pieces wherever they
 // lie.  Sums run over j in order, so no atomic and no order of workgroups
 // shows in a result.  Bound by the bytes of the experts' rows.
+#include <algorithm>
+
 #include "internal.hpp"
 #include "wave.hpp"
 
@@ -105,62 +107,80 @@ __global__ __launch_bounds__(256) void k_combine(MoveArgs a)
     }
 }
 
-// kWaves waves a token (4: a workgroup, 1: four tokens a workgroup); dy stays
-// in registers while the token's rows pass by.
-template <int kWaves>
-__global__ __launch_bounds__(256) void k_combine_backward(MoveArgs a)
+// A token's waves hold two pieces of dy a lane while its rows pass by, four of
+// them in flight; each wave adds its dot products up by lane moves, and the
+// waves' are added in order.  kSolo: a wave a token, four a workgroup;
+// otherwise a workgroup a token, as many waves as its columns fill.
+template <bool kDyF32, bool kOF32, bool kSolo>
+__global__ __launch_bounds__(kSolo ? 256 : 1024) void k_combine_backward(MoveArgs a)
 {
-    constexpr int kHeld = 4, kLanes = 64 * kWaves;
-    __shared__ float part[kWaves == 4 ? 4 : 1][kMoveMostK];
-    const int lane = kWaves == 4 ? threadIdx.x : threadIdx.x & 63, wave = wave_index();
-    const int64_t each = 4 / kWaves;
-    for (int64_t t = (int64_t)blockIdx.x * each + (kWaves == 4 ? 0 : wave); t < a.T; t += (int64_t)gridDim.x * each) {
-        RawPiece dy[kHeld];
+    constexpr int kHeld = 2, kAhead = 4;
+    __shared__ float part[16][kMoveMostK];
+    const int lanes = kSolo ? 64 : blockDim.x, lane = kSolo ? threadIdx.x & 63 : threadIdx.x, wave = wave_index();
+    const int64_t each = kSolo ? 4 : 1;
+    for (int64_t t = (int64_t)blockIdx.x * each + (kSolo ? wave : 0); t < a.T; t += (int64_t)gridDim.x * each) {
+        for (int64_t c0 = 0; c0 == 0 || c0 < a.cols; c0 += 8 * kHeld * lanes) {  // (one turn, but for the longest rows)
+            Piece dy[kHeld];
+            bool in[kHeld];
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int64_t c = 8 * (lane + (int64_t)kLanes * i);
-            if (c < a.cols) dy[i] = load_raw(a.tokens, t * a.ld_tokens + c, a.tokens_f32);
-        }
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t place = a.rows[t * a.k + j];
-            float dot = 0.0f;
-            if (inside(place, a.R)) {
-                const float w = a.weights[t * a.k + j];
-                const auto piece = [&](const Piece& d, const Piece& o, int64_t c) {
-                    Piece g;
+            for (int i = 0; i < kHeld; ++i) {
+                const int64_t c = c0 + 8 * (lane + (int64_t)lanes * i);
+                in[i] = c < a.cols;
+                RawPiece r = {};
+                if (in[i]) r = load_raw(a.tokens, t * a.ld_tokens + c, kDyF32);
+                dy[i] = widen(r, kDyF32);
+            }
+            for (int j0 = 0; j0 < a.k; j0 += kAhead) {
+                int64_t place[kAhead];
+                RawPiece o[kAhead][kHeld];
+                float w[kAhead], dot[kAhead];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        dot = __builtin_fmaf(d.v[e], o.v[e], dot);
-                        g.v[e] = w * d.v[e];
+                for (int u = 0; u < kAhead; ++u) {
+                    const int64_t slot = t * a.k + min(j0 + u, a.k - 1);
+                    place[u] = j0 + u < a.k ? a.rows[slot] : -1;
+                    w[u] = a.weights[slot];
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i) {
+                        o[u][i] = RawPiece{};
+                        if (in[i] && inside(place[u], a.R))
+                            o[u][i] = load_raw(a.from, place[u] * a.ld_from + c0 + 8 * (lane + (int64_t)lanes * i), kOF32);
                     }
-                    store_piece(a.out, place * a.ld_out + c, g, false);
-                };
-                RawPiece o[kHeld];
-#pragma unroll
-                for (int i = 0; i < kHeld; ++i) {
-                    const int64_t c = 8 * (lane + (int64_t)kLanes * i);
-                    if (c < a.cols) o[i] = load_raw(a.from, place * a.ld_from + c, a.from_f32);
                 }
 #pragma unroll
-                for (int i = 0; i < kHeld; ++i) {
-                    const int64_t c = 8 * (lane + (int64_t)kLanes * i);
-                    if (c < a.cols) piece(widen(dy[i], a.tokens_f32), widen(o[i], a.from_f32), c);
+                for (int u = 0; u < kAhead; ++u) {
+                    dot[u] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i) {
+                        const Piece v = widen(o[u][i], kOF32);
+                        Piece g;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            dot[u] = __builtin_fmaf(dy[i].v[e], v.v[e], dot[u]);
+                            g.v[e] = w[u] * dy[i].v[e];
+                        }
+                        if (in[i] && inside(place[u], a.R))
+                            store_piece(a.out, place[u] * a.ld_out + c0 + 8 * (lane + (int64_t)lanes * i), g, false);
+                    }
                 }
-                for (int64_t c = 8 * (lane + (int64_t)kLanes * kHeld); c < a.cols; c += 8 * kLanes)
-                    piece(load_piece(a.tokens, t * a.ld_tokens + c, a.tokens_f32),
-                          load_piece(a.from, place * a.ld_from + c, a.from_f32), c);
-            }
-            dot = wave_sum(dot);
-            if constexpr (kWaves == 4) {
-                if ((threadIdx.x & 63) == 0) part[wave][j] = dot;
-            } else {
-                if (lane == 0) a.dweights[t * a.k + j] = dot;
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    // (an empty slot's row of zeros: 0, whatever dy holds)
+                    const float sum = inside(place[u], a.R) ? wave_sum(dot[u]) : 0.0f;
+                    if ((threadIdx.x & 63) == 0 && j0 + u < a.k) part[wave][j0 + u] = c0 == 0 ? sum : part[wave][j0 + u] + sum;
+                }
             }
         }
-        if constexpr (kWaves == 4) {
+        if constexpr (kSolo) {
+            __builtin_amdgcn_wave_barrier();
+            if (lane < a.k) a.dweights[t * a.k + lane] = part[wave][lane];
+            __builtin_amdgcn_wave_barrier();
+        } else {
             __syncthreads();
-            if (lane < a.k)
-                a.dweights[t * a.k + lane] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+            if (lane < a.k) {
+                float sum = part[0][lane];
+                for (int v = 1; v < (int)blockDim.x / 64; ++v) sum += part[v][lane];
+                a.dweights[t * a.k + lane] = sum;
+            }
             __syncthreads();  // part is written again for the next token
         }
     }
@@ -194,16 +214,29 @@ void launch_combine(const MoveArgs& a, hipStream_t s)
         launch_pieces(k_combine<1>, 1, a, s);
 }
 
-void launch_combine_backward(const MoveArgs& a, hipStream_t s)
+namespace {
+
+template <bool kDyF32, bool kOF32>
+void launch_combine_backward_of(const MoveArgs& a, hipStream_t s)
 {
-    if (a.cols <= 2048) {
+    const int64_t pieces = (a.cols + 7) / 8, waves = std::max<int64_t>(1, std::min<int64_t>(16, (pieces + 127) / 128));
+    if (waves == 1) {
         const int64_t blocks = (a.T + 3) / 4;
-        hipLaunchKernelGGL(k_combine_backward<1>, dim3((uint32_t)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(256),
+        hipLaunchKernelGGL((k_combine_backward<kDyF32, kOF32, true>), dim3((uint32_t)std::min(blocks, kMostBlocks)), dim3(256),
                            0, s, a);
     } else {
-        hipLaunchKernelGGL(k_combine_backward<4>, dim3((uint32_t)(a.T < kMostBlocks ? a.T : kMostBlocks)), dim3(256), 0,
-                           s, a);
+        hipLaunchKernelGGL((k_combine_backward<kDyF32, kOF32, false>), dim3((uint32_t)std::min(a.T, kMostBlocks)),
+                           dim3((uint32_t)(64 * waves)), 0, s, a);
     }
+}
+
+}  // namespace
+
+void launch_combine_backward(const MoveArgs& a, hipStream_t s)
+{
+    const auto launch = a.tokens_f32 ? (a.from_f32 ? launch_combine_backward_of<true, true> : launch_combine_backward_of<true, false>)
+                                     : (a.from_f32 ? launch_combine_backward_of<false, true> : launch_combine_backward_of<false, false>);
+    launch(a, s);
 }
 
 }  // namespace nvfp4

@@ -20,7 +20,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int64_t kMostBlocks = int64_t(1) << 22;  // of a launch; each takes more rows beyond that
-constexpr int kHeld = 4;                           // pieces of 8 columns that a lane keeps
+constexpr int kHeld = 2;                           // pieces of 8 columns that a lane keeps
 
 __device__ __forceinline__ Piece sum_of(const NormArgs& a, int64_t row, int64_t c)
 {
@@ -64,52 +64,64 @@ __device__ __forceinline__ uint2 codes_of(const Piece& y, float lift, float fact
 
 }  // namespace
 
-// kWaves waves a row (4: a workgroup, 1: four rows a workgroup).
-template <int kWaves, bool kI8>
-__global__ __launch_bounds__(256) void k_norm(NormArgs a)
+// kSolo: a wave a row, four rows a workgroup; otherwise a workgroup a row, as
+// many waves as its columns fill (16 at most).
+template <bool kSolo, bool kI8>
+__global__ __launch_bounds__(kSolo ? 256 : 1024) void k_norm(NormArgs a)
 {
-    constexpr int kLanes = 64 * kWaves, kRows = 4 / kWaves;
-    __shared__ float part[2][4];
-    const int lane = kWaves == 4 ? threadIdx.x : threadIdx.x & 63, wave = wave_index();
+    __shared__ float part[2][16];
+    const int lanes = kSolo ? 64 : blockDim.x, lane = kSolo ? threadIdx.x & 63 : threadIdx.x, wave = wave_index();
+    const int waves = lanes / 64;
     const float each = 1.0f / (float)a.cols;
-    for (int64_t row = (int64_t)blockIdx.x * kRows + (kWaves == 4 ? 0 : wave); row < a.rows;
-         row += (int64_t)gridDim.x * kRows) {
+    for (int64_t row = kSolo ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; row < a.rows;
+         row += (int64_t)gridDim.x * (kSolo ? 4 : 1)) {
         Piece h[kHeld];
         float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int64_t c = 8 * (lane + (int64_t)kLanes * i);
-            if (c < a.cols) h[i] = sum_of(a, row, c);
-        }
         const auto square = [&](const Piece& p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(p.v[e], p.v[e], sum);
         };
+        {
+            RawPiece x[kHeld], r[kHeld];
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int64_t c = 8 * (lane + (int64_t)kLanes * i);
-            if (c >= a.cols) continue;
-            square(h[i]);
-            if (a.h) store_piece(a.h, row * a.ld_h + c, h[i], a.s_f32);
+            for (int i = 0; i < kHeld; ++i) {
+                const int64_t c = 8 * (lane + (int64_t)lanes * i);
+                x[i] = r[i] = RawPiece{};
+                if (c < a.cols) {
+                    x[i] = load_raw(a.x, row * a.ld_x + c, a.x_f32);
+                    if (a.residual) r[i] = load_raw(a.residual, row * a.ld_r + c, a.s_f32);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int64_t c = 8 * (lane + (int64_t)lanes * i);
+                h[i] = widen(x[i], a.x_f32);
+                const Piece d = widen(r[i], a.s_f32);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[i].v[e] += d.v[e];
+                square(h[i]);
+                if (a.h && c < a.cols) store_piece(a.h, row * a.ld_h + c, h[i], a.s_f32);
+            }
         }
-        const int64_t rest = 8 * (lane + (int64_t)kLanes * kHeld);  // what is not kept is read again
-        for (int64_t c = rest; c < a.cols; c += 8 * kLanes) square(sum_of(a, row, c));
+        const int64_t rest = 8 * (lane + (int64_t)lanes * kHeld);  // what is not kept is read again
+        for (int64_t c = rest; c < a.cols; c += 8 * lanes) square(sum_of(a, row, c));
         sum = wave_sum(sum);
-        if constexpr (kWaves == 4) {
+        if constexpr (!kSolo) {
             if ((threadIdx.x & 63) == 0) part[0][wave] = sum;
             __syncthreads();
-            sum = (part[0][0] + part[0][1]) + (part[0][2] + part[0][3]);
+            sum = part[0][0];
+            for (int v = 1; v < waves; ++v) sum += part[0][v];
         }
         const float rstd = 1.0f / __builtin_sqrtf(sum * each + a.eps);
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            const int64_t c = 8 * (lane + (int64_t)kLanes * i);
+            const int64_t c = 8 * (lane + (int64_t)lanes * i);
             if (c >= a.cols) continue;
             scale_piece(a, c, rstd, h[i], top);
             if (a.y) store_piece(a.y, row * a.ld_y + c, h[i], false);
         }
-        for (int64_t c = rest; c < a.cols; c += 8 * kLanes) {
+        for (int64_t c = rest; c < a.cols; c += 8 * lanes) {
             Piece p = sum_of(a, row, c);
             if (a.h && !kI8) store_piece(a.h, row * a.ld_h + c, p, a.s_f32);  // (h may lie where r does)
             scale_piece(a, c, rstd, p, top);
@@ -117,11 +129,12 @@ __global__ __launch_bounds__(256) void k_norm(NormArgs a)
         }
         if constexpr (kI8) {
             top = wave_top(top);
-            if constexpr (kWaves == 4) {
+            if constexpr (!kSolo) {
                 if ((threadIdx.x & 63) == 0) part[1][wave] = top;
                 __syncthreads();
-                top = __uint_as_float(max(max(__float_as_uint(part[1][0]), __float_as_uint(part[1][1])),
-                                          max(__float_as_uint(part[1][2]), __float_as_uint(part[1][3]))));
+                uint32_t most = 0;
+                for (int v = 0; v < waves; ++v) most = max(most, __float_as_uint(part[1][v]));
+                top = __uint_as_float(most);
             }
             if (lane == 0) a.scales[row] = top / 127.0f;
             // a power of two on both sides of the quotient keeps 127 / max finite
@@ -129,16 +142,16 @@ __global__ __launch_bounds__(256) void k_norm(NormArgs a)
             const float factor = top > 0.0f ? 127.0f / (top * lift) : 0.0f;
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
-                const int64_t c = 8 * (lane + (int64_t)kLanes * i);
+                const int64_t c = 8 * (lane + (int64_t)lanes * i);
                 if (c < a.cols) *reinterpret_cast<uint2*>(a.codes + row * a.ld_codes + c) = codes_of(h[i], lift, factor);
             }
-            for (int64_t c = rest; c < a.cols; c += 8 * kLanes) {
+            for (int64_t c = rest; c < a.cols; c += 8 * lanes) {
                 Piece p = sum_of(a, row, c);
                 if (a.h) store_piece(a.h, row * a.ld_h + c, p, a.s_f32);
                 scale_piece(a, c, rstd, p, top);
                 *reinterpret_cast<uint2*>(a.codes + row * a.ld_codes + c) = codes_of(p, lift, factor);
             }
-        } else if constexpr (kWaves == 4) {
+        } else if constexpr (!kSolo) {
             __syncthreads();  // part[0] is written again for the next row
         }
     }
@@ -252,6 +265,7 @@ __global__ __launch_bounds__(256) void k_column_sums(const float* __restrict__ p
     const int64_t c = 32 * (int64_t)blockIdx.x + 4 * q;
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c < cols)
+#pragma unroll 8
         for (int64_t g = groups * s / 32, to = groups * (s + 1) / 32; g < to; ++g) {
             const float4 v = *reinterpret_cast<const float4*>(parts + g * cols + c);
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
@@ -269,15 +283,16 @@ __global__ __launch_bounds__(256) void k_column_sums(const float* __restrict__ p
 void launch_norm(const NormArgs& a, hipStream_t s)
 {
     if (a.rows == 0) return;
-    const bool solo = a.cols <= 512 * kHeld && (a.cols <= 256 * kHeld || a.rows > 512);
+    const int64_t waves = std::max<int64_t>(1, std::min<int64_t>(16, (a.cols / 8 + 64 * kHeld - 1) / (64 * kHeld)));
+    const bool solo = waves == 1;
     const int64_t blocks = solo ? (a.rows + 3) / 4 : a.rows;
-    const dim3 grid((uint32_t)(blocks < kMostBlocks ? blocks : kMostBlocks));
+    const dim3 grid((uint32_t)std::min(blocks, kMostBlocks)), block((uint32_t)(solo ? 256 : 64 * waves));
     if (a.codes) {
-        if (solo) hipLaunchKernelGGL((k_norm<1, true>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((k_norm<4, true>), grid, dim3(256), 0, s, a);
+        if (solo) hipLaunchKernelGGL((k_norm<true, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_norm<false, true>), grid, block, 0, s, a);
     } else {
-        if (solo) hipLaunchKernelGGL((k_norm<1, false>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((k_norm<4, false>), grid, dim3(256), 0, s, a);
+        if (solo) hipLaunchKernelGGL((k_norm<true, false>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_norm<false, false>), grid, block, 0, s, a);
     }
 }
 

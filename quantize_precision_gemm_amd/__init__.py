@@ -1090,28 +1090,41 @@ def nvfp4_i8_gemm(a, b, out_dtype=torch.bfloat16, out=None, stream=None):
 
 # ---- what stands around the expert products ----
 
-def _check_matrix(t, what, index, shape=None, dtypes=(torch.bfloat16, torch.float32)):
+_ROW_DTYPES = (torch.bfloat16, torch.float32)
+
+
+def _check_matrix(t, what, index, shape=None, dtypes=_ROW_DTYPES):
     """A 2-D device tensor with a contiguous last dimension: its address, row
     pitch and dtype code (index None: any device)."""
+    if isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in dtypes:
+        at = t.get_device()  # (of a CPU tensor: -1)
+        if at == index or (index is None and at >= 0):
+            rows, cols = t.shape
+            if shape is None or shape == (rows, cols):
+                pitch, step = t.stride()
+                if rows <= 1 or cols == 0:  # the stride of a dimension of one element or none means nothing
+                    if step == 1 or cols <= 1 or rows == 0:
+                        return t.data_ptr(), (cols + 15) // 16 * 16, OUT_FP32 if t.dtype == torch.float32 else OUT_BF16
+                elif (step == 1 or cols == 1) and pitch >= cols:
+                    return t.data_ptr(), pitch, OUT_FP32 if t.dtype == torch.float32 else OUT_BF16
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
         raise TypeError(f"{what}: expected a 2-D CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if index is not None and t.get_device() != index:
         raise ValueError(f"{what}: on {t.device}, expected cuda:{index}")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{what}: shape {(rows, cols)}, expected {shape}")
-    pitch, step = t.stride()
-    if rows == 0 or cols == 0 or rows == 1:  # the stride of a dimension of one element or none means nothing
-        if step != 1 and cols > 1 and rows > 0:
-            raise ValueError(f"{what}: the last dimension must be contiguous")
-        pitch = _round_up(cols, 16)
-    elif step != 1 and cols > 1:
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    elif pitch < cols:
-        raise ValueError(f"{what}: rows overlap")
-    return t.data_ptr(), pitch, OUT_FP32 if t.dtype == torch.float32 else OUT_BF16
+    raise ValueError(f"{what}: rows overlap")
+
+
+def _rows_like(rows, cols, dtype, device, stream):
+    """A new matrix, as _empty makes it (1.2 us; torch.empty of a shape in a tuple 1.7)."""
+    if stream is None:
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+    return _empty((rows, cols), dtype, device, stream)
 
 
 def _check_dense(t, what, index, dtype, shape):
@@ -1169,9 +1182,9 @@ class Routing:
     def empty(cls, T, E, k, device, with_scores=False, stream=None):
         """Buffers for nvfp4_route(..., out=), which a layer may keep from batch to batch."""
         need = nvfp4_route_workspace(T, E)
-        return cls(_empty((T, k), torch.int32, device, stream), _empty((T, k), torch.float32, device, stream),
-                   _empty((T, k), torch.int32, device, stream), _empty(E, torch.int32, device, stream),
-                   _empty((T, E), torch.float32, device, stream) if with_scores else None,
+        return cls(_rows_like(T, k, torch.int32, device, stream), _rows_like(T, k, torch.float32, device, stream),
+                   _rows_like(T, k, torch.int32, device, stream), _empty(E, torch.int32, device, stream),
+                   _rows_like(T, E, torch.float32, device, stream) if with_scores else None,
                    _empty(need, torch.uint8, device, stream) if need else None)
 
 
@@ -1232,7 +1245,7 @@ def nvfp4_route_backward(logits, experts, dweights, score=SOFTMAX, renormalise=T
     dscores_ptr = None if dscores is None else _check_dense(dscores, "dscores", index, torch.float32, (T, E))
     if out is None:
         out_code, ld_out = _out_code(out_dtype), E
-        out = _empty((T, E), out_dtype, logits.device, stream)
+        out = _rows_like(T, E, out_dtype, logits.device, stream)
         out_ptr = out.data_ptr()
     else:
         out_ptr, ld_out, out_code = _check_matrix(out, "out", index, (T, E))
@@ -1263,7 +1276,7 @@ def nvfp4_dispatch(x, rows, out=None, stream=None):
         raise ValueError(f"rows: {rows.shape[0]} tokens, x has {T}")
     k = rows.shape[1]
     if out is None:
-        out = _empty((T * k, cols), torch.bfloat16, x.device, stream)
+        out = _rows_like(T * k, cols, torch.bfloat16, x.device, stream)
     out_ptr, ld_out, _ = _check_matrix(out, "out", index, dtypes=(torch.bfloat16,))
     if out.shape[1] != cols:
         raise ValueError(f"out: {out.shape[1]} columns, x has {cols}")
@@ -1285,7 +1298,7 @@ def nvfp4_combine(o, rows, weights=None, residual=None, out_dtype=torch.bfloat16
     T, k = rows.shape
     weights_ptr = None if weights is None else _check_dense(weights, "weights", index, torch.float32, (T, k))
     if out is None:
-        out = _empty((T, cols), out_dtype, o.device, stream)
+        out = _rows_like(T, cols, out_dtype, o.device, stream)
     out_ptr, ld_out, out_code = _check_matrix(out, "out", index, (T, cols))
     r_ptr, ld_r = None, 0
     if residual is not None:
@@ -1313,10 +1326,10 @@ def nvfp4_combine_backward(dy, o, rows, weights, out=None, dweights=None, stream
     k = rows.shape[1]
     weights_ptr = _check_dense(weights, "weights", index, torch.float32, (T, k))
     if out is None:
-        out = _empty((R, cols), torch.bfloat16, dy.device, stream)
+        out = _rows_like(R, cols, torch.bfloat16, dy.device, stream)
     out_ptr, ld_out, _ = _check_matrix(out, "out", index, (R, cols), (torch.bfloat16,))
     if dweights is None:
-        dweights = _empty((T, k), torch.float32, dy.device, stream)
+        dweights = _rows_like(T, k, torch.float32, dy.device, stream)
     dweights_ptr = _check_dense(dweights, "dweights", index, torch.float32, (T, k))
     st = load_library().nvfp4_combine_backward(ptr, code, ld, o_ptr, o_code, ld_o, R, rows_ptr, weights_ptr, T, k, cols,
                                                out_ptr, ld_out, dweights_ptr, _raw_stream(stream))
@@ -1343,7 +1356,7 @@ def _rmsnorm(x, weight, eps, residual, h, y, codes, scales, stream, what):
     if residual is not None:
         r_ptr, ld_r, s_code = _check_matrix(residual, "residual", index, (rows, cols))
         if h is None:
-            h = _empty((rows, cols), residual.dtype, x.device, stream)
+            h = _rows_like(rows, cols, residual.dtype, x.device, stream)
     if h is not None:
         h_ptr, ld_h, h_code = _check_matrix(h, "h", index, (rows, cols))
         if residual is not None and h_code != s_code:
@@ -1369,7 +1382,7 @@ def nvfp4_rmsnorm(x, weight=None, eps=1e-6, residual=None, h=None, out=None, str
     (bf16 rows, h).  h is the sum, of the residual's dtype: a new tensor, or the
     one given (which may be residual); None without a residual (unless given)."""
     if out is None and isinstance(x, torch.Tensor) and x.is_cuda:
-        out = _empty(x.shape, torch.bfloat16, x.device, stream)
+        out = _rows_like(*x.shape, torch.bfloat16, x.device, stream) if x.dim() == 2 else None
     h = _rmsnorm(x, weight, eps, residual, h, out, None, None, stream, "nvfp4_rmsnorm")
     return out, h
 
@@ -1378,7 +1391,7 @@ def nvfp4_rmsnorm_i8(x, weight=None, eps=1e-6, residual=None, h=None, out=None, 
     """nvfp4_rmsnorm with the normalised rows as int8 and one scale per row: (an
     I8Tensor, which nvfp4_i8_gemm takes, h)."""
     if out is None and isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2:
-        out = I8Tensor(_empty(x.shape, torch.int8, x.device, stream), _empty(x.shape[0], torch.float32, x.device, stream))
+        out = I8Tensor(_rows_like(*x.shape, torch.int8, x.device, stream), _empty(x.shape[0], torch.float32, x.device, stream))
     if not isinstance(out, I8Tensor):
         raise TypeError("out: expected an I8Tensor" if out is not None else "x: expected a 2-D CUDA tensor")
     h = _rmsnorm(x, weight, eps, residual, h, None, out.codes, out.scales, stream, "nvfp4_rmsnorm")
@@ -1404,7 +1417,7 @@ def nvfp4_rmsnorm_backward(dy, h, weight=None, eps=1e-6, dh=None, out_dtype=torc
         dh_ptr, ld_dh, _ = _check_matrix(dh, "dh", index, (rows, cols), (h.dtype,))
     weight_ptr, w_code = _check_norm_weight(weight, index, cols)
     if out is None:
-        out = _empty((rows, cols), out_dtype, device, stream)
+        out = _rows_like(rows, cols, out_dtype, device, stream)
     out_ptr, ld_out, out_code = _check_matrix(out, "out", index, (rows, cols))
     dweight_ptr, ws, ws_ptr, ws_bytes = None, None, None, 0
     if weight is not None or dweight is not None:
@@ -1466,13 +1479,13 @@ def nvfp4_bf16_linear(x, w, ends=None, bias=None, activation=ACT_NONE, residual=
         bias_code = _out_code(bias.dtype, "bias") if isinstance(bias, torch.Tensor) else OUT_FP32
         bias_ptr = _check_dense(bias, "bias", index, torch.float32 if bias_code == OUT_FP32 else torch.bfloat16, lead)
     if out is None:
-        out = _empty((T, N), out_dtype, device, stream)
+        out = _rows_like(T, N, out_dtype, device, stream)
     out_ptr, ldc, out_code = _check_matrix(out, "out", index, (T, N))
     r_ptr, ld_r, pre_ptr, ld_pre = None, 0, None, 0
     if residual is not None:
         r_ptr, ld_r, _ = _check_matrix(residual, "residual", index, (T, N), (out.dtype,))
     if pre is None and with_pre:
-        pre = _empty((T, N), torch.bfloat16, device, stream)
+        pre = _rows_like(T, N, torch.bfloat16, device, stream)
     if pre is not None:
         pre_ptr, ld_pre, _ = _check_matrix(pre, "pre", index, (T, N), (torch.bfloat16,))
     if workspace is not None:
@@ -1509,7 +1522,7 @@ def nvfp4_bf16_linear_backward(dy, pre, activation=ACT_NONE, ends=None, with_bia
     if pre is not None:
         pre_ptr, ld_pre, _ = _check_matrix(pre, "pre", index, (T, N), (torch.bfloat16,))
         if out is None:
-            out = _empty((T, N), torch.bfloat16, device, stream)
+            out = _rows_like(T, N, torch.bfloat16, device, stream)
         out_ptr, ld_out, _ = _check_matrix(out, "out", index, (T, N), (torch.bfloat16,))
     elif activation != ACT_NONE:
         raise ValueError("pre: needed with an activation")

@@ -346,35 +346,66 @@ __device__ __forceinline__ uint32_t whole_of(float v)
     return r;
 }
 
-// The k largest of a row's keys, (value << kBits) + (2^kBits - 1 - index), a
-// value of 0: never.  Lane j of the row gets the j-th one's index (-1: there is none left).
-// Returns whether values no further apart than `near` decided, other than those of
-// equal logits (the row's, in LDS) and biases.
+// The largest key of a row below `last` (0: the largest of all).
+template <int L, int P>
+__device__ __forceinline__ uint32_t key_below(const uint32_t (&key)[P], uint32_t last)
+{
+    uint32_t top = key[0] - last;
+#pragma unroll
+    for (int i = 1; i < P; ++i) top = max(top, key[i] - last);
+    return (uint32_t)over_lanes<L>((int)top, MaxUnsigned()) + last;
+}
+
+// The k + 1 largest of a row's keys, (value << kBits) + (2^kBits - 1 - index),
+// a value of 0: never.  Lane j of the row gets the j-th one's index (-1: there
+// is none left), `last` the last one's key.  Returns whether values no further
+// apart than `near` decided, other than those of equal logits (the row's, in
+// LDS) and biases.
 template <int L, int P>
 __device__ __forceinline__ bool pick(const RouteArgs& a, const float* logits, const uint32_t (&key)[P], uint32_t near,
-                                     int& mine)
+                                     int& mine, uint32_t& last)
 {
     constexpr int kBits = __builtin_ctz(L * P);
     constexpr uint32_t kMask = (1u << kBits) - 1;
     const int sub = threadIdx.x & (L - 1);
     mine = -1;
-    uint32_t last = 0;
+    last = 0;
     bool close = false;
-    for (int r = 0; r <= a.k; ++r) {  // (the first that is left out is compared, too)
-        uint32_t top = key[0] - last;
-#pragma unroll
-        for (int i = 1; i < P; ++i) top = max(top, key[i] - last);
-        const uint32_t best = (uint32_t)over_lanes<L>((int)top, MaxUnsigned()) + last;
+    for (int r = 0; r <= a.k; ++r) {
+        const uint32_t best = key_below<L, P>(key, last);
         const bool some = best > kMask;
         const int e = (int)(kMask - (best & kMask));
         if (r > 0 && some && (last >> kBits) - (best >> kBits) <= near) {
             const int was = (int)(kMask - (last & kMask));  // equal logits and biases make equal values
             close |= logits[was] != logits[e] || (a.bias && a.bias[was] != a.bias[e]);
         }
-        if (sub == r && r < a.k) mine = some ? e : -1;
+        if (sub == r) mine = some ? e : -1;
         last = best;
     }
     return close;
+}
+
+__device__ __forceinline__ double sigmoid64(float l)
+{
+    const double e = exp(-__builtin_fabs((double)l));
+    return (l < 0 ? e : 1.0) / (1.0 + e);
+}
+
+// The k + 1 candidates of each row (lane j: the j-th, -1: none) in the order of
+// their sigmoid scores and biases in 64 bits, one exponential a lane, by their ranks.
+__device__ __forceinline__ int sort_exactly(const RouteArgs& a, const float* logits, int mine)
+{
+    const int sub = threadIdx.x & 15;
+    const bool there = sub <= a.k && mine >= 0;
+    const double c = there ? sigmoid64(logits[mine]) + (double)a.bias[mine] : -INFINITY;
+    int rank = 0;
+    for (int i = 0; i <= a.k; ++i) {
+        const double other = __shfl(c, i, 16);
+        const int e = __shfl(mine, i, 16);
+        rank += other > c || (other == c && (e < mine || (e == mine && i < sub)));
+    }
+    if (sub > a.k) rank = sub;
+    return __builtin_amdgcn_ds_permute(((threadIdx.x & 48) + rank) << 2, mine);
 }
 
 // Bound on the error of c as fp32 computes it.  Softmax, relative to the
@@ -426,6 +457,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& a, int64_t row, d
         __builtin_amdgcn_wave_barrier();
         if (lane < G) {
             double one = -INFINITY, two = -INFINITY;
+#pragma unroll 8
             for (int i = 0; i < per; ++i) take(buf[lane * per + i], one, two);
             value[lane] = pair_sum(one, two);
         }
@@ -434,6 +466,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs& a, int64_t row, d
         if (lane < G) {
             const double v = value[lane];
             int before = 0;
+#pragma unroll 8
             for (int i = 0; i < G; ++i) before += value[i] > v || (value[i] == v && i < lane);
             keep = before < a.kept && v > -INFINITY;
         }
@@ -621,7 +654,21 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a)
         for (int i = 0; i < P; ++i) own[e0 + i] = l[i];
         __builtin_amdgcn_wave_barrier();
         int mine;
-        close |= pick<L, P>(a, own, key, near, mine);
+        uint32_t last;
+        bool swapped = pick<L, P>(a, own, key, near, mine, last);
+        if constexpr (L == 16 && kMode != 0) {
+            // Values of neighbours in the order alone: the candidates are put in order in 64 bits
+            // (unless the last of them and what comes next lie close, too).
+            if (a.sigmoid && a.bias && a.k < 16 && __ballot(swapped)) {
+                const uint32_t next = key_below<L, P>(key, last);
+                const bool more = next >> kBits && (last >> kBits) - (next >> kBits) <= near;
+                const int sorted = sort_exactly(a, own, mine);
+                mine = swapped ? sorted : mine;
+                swapped = swapped && more;
+            }
+        }
+        close |= swapped;
+        if (sub >= a.k) mine = -1;
         float chosen = mine >= 0 ? own[mine] : -INFINITY;
         uint64_t again = __ballot(close && live);
         while (again) {
@@ -772,74 +819,93 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBackArgs a)
     for (int64_t t0 = (int64_t)blockIdx.x * (256 / L); t0 < a.f.T; t0 += step) {
         const bool live = t0 + tid / L < a.f.T;
         const int64_t t = live ? t0 + tid / L : a.f.T - 1, row = t * a.f.ld;
-        float s[P], top = 0.0f, inverse = 1.0f;
+        const int e = sub < a.f.k ? a.f.experts[t * a.f.k + sub] : -1;
+        const bool there = e >= 0 && e < a.f.E;
+        const float g = there ? a.f.scale * a.dweights[t * a.f.k + sub] : 0.0f;
+        // all scores, where the form needs them: softmax s, sigmoid s (1 - s)
+        float s[P], mine = 0.0f;
         bool bad = false;
         if (whole) {
             load_logits<P>(a.f, row, e0, s);
             bad = own_bits<L>(__ballot(drop_not_finite(s))) != 0;
             if (softmax) {
-                top = top_of<L, P>(s);
-                const float sum = sum_of<L, P>(s, top);
-                inverse = sum > 0.0f ? 1.0f / sum : 0.0f;
+                const float top = top_of<L, P>(s);
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    s[i] = exp_neg(s[i] - top);
+                    sum += s[i];
+                }
+                sum = over_lanes<L>(sum, Add());
+                const float inverse = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+                for (int i = 0; i < P; ++i) s[i] *= inverse;
+                if (!a.f.renorm) {
+                    __builtin_amdgcn_wave_barrier();  // (the last row's reads)
+#pragma unroll
+                    for (int i = 0; i < P; ++i) part[e0 + i] = s[i];
+                    __builtin_amdgcn_wave_barrier();
+                    mine = there ? part[e] : 0.0f;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const float p = exp_neg(-__builtin_fabsf(s[i])), h = 1.0f / (1.0f + p);
+                    s[i] = p * h * h;
+                }
             }
         }
-        // the chosen
-        const int e = sub < a.f.k ? a.f.experts[t * a.f.k + sub] : -1;
-        const bool there = e >= 0 && e < a.f.E;
-        const float l = there ? logit_at(a.f, row + e) : -INFINITY;
-        const float g = there ? a.f.scale * a.dweights[t * a.f.k + sub] : 0.0f;
-        const float neg = l < 0.0f ? l : 0.0f, half = 1.0f / (1.0f + exp_neg(-__builtin_fabsf(l)));
-        const float rest = exp_neg(l > 0.0f ? -l : 0.0f) * half;  // 1 - 1 / (1 + e^-l)
+        // the chosen: d their gradient, or (softmax, not renormalised) what it has beside s times the mean
         float d, dot = 0.0f;
-        if (a.f.renorm) {
-            const float x = a.f.sigmoid ? neg : l;
-            float m = over_lanes<L>(there ? x : -INFINITY, Max());
-            m = m > -INFINITY ? m : 0.0f;
-            const float q = there ? exp_neg(x - m) * (a.f.sigmoid ? half : 1.0f) : 0.0f;
-            const float all = over_lanes<L>(q, Add());
-            const float p = all > 0.0f ? q / all : 0.0f;
-            const float mean = over_lanes<L>(there ? g * p : 0.0f, Add());
-            d = p * (g - mean) * (a.f.sigmoid ? rest : 1.0f);
-        } else if (a.f.sigmoid) {
-            d = g * (exp_neg(neg) * half) * rest;
+        if (softmax && !a.f.renorm) {
+            d = g * mine;
+            dot = over_lanes<L>(d, Add());
         } else {
-            d = g * (exp_neg(l - top) * inverse);
-            dot = over_lanes<L>(there ? d : 0.0f, Add());
+            const float l = there ? logit_at(a.f, row + e) : -INFINITY;
+            const float neg = l < 0.0f ? l : 0.0f, half = 1.0f / (1.0f + exp_neg(-__builtin_fabsf(l)));
+            const float rest = exp_neg(l > 0.0f ? -l : 0.0f) * half;  // 1 - 1 / (1 + e^-l)
+            if (a.f.renorm) {
+                const float x = a.f.sigmoid ? neg : l;
+                float m = over_lanes<L>(there ? x : -INFINITY, Max());
+                m = m > -INFINITY ? m : 0.0f;
+                const float q = there ? exp_neg(x - m) * (a.f.sigmoid ? half : 1.0f) : 0.0f;
+                const float all = over_lanes<L>(q, Add());
+                const float p = all > 0.0f ? q / all : 0.0f;
+                const float mean = over_lanes<L>(there ? g * p : 0.0f, Add());
+                d = p * (g - mean) * (a.f.sigmoid ? rest : 1.0f);
+            } else {
+                d = g * (exp_neg(neg) * half) * rest;
+            }
         }
-        if (!there) d = 0.0f;
-        __builtin_amdgcn_wave_barrier();  // (the last row's reads)
+        float o[P];
 #pragma unroll
-        for (int i = 0; i < P; ++i) part[e0 + i] = 0.0f;
+        for (int i = 0; i < P; ++i) o[i] = 0.0f;
+        if (whole) {
+            float ds[P], along = 0.0f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) ds[i] = 0.0f;
+            if (a.dscores) {
+                load_values<P>(a.dscores, true, a.vec_scores, t * a.f.E, e0, a.f.E, 0.0f, ds);
+                if (softmax) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) along = __builtin_fmaf(ds[i], s[i], along);
+                    along = over_lanes<L>(along, Add());
+                }
+            }
+            along += dot;
+#pragma unroll
+            for (int i = 0; i < P; ++i) o[i] = bad ? NAN : s[i] * (ds[i] - along);
+        }
+        __builtin_amdgcn_wave_barrier();  // (reads of the last row's, or of the scores)
+#pragma unroll
+        for (int i = 0; i < P; ++i) part[e0 + i] = o[i];
         __builtin_amdgcn_wave_barrier();
         for (int j = 0; j < a.f.k; ++j) {
             if (sub == j && there) part[e] += d;
             __builtin_amdgcn_wave_barrier();
         }
-        float o[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) o[i] = part[e0 + i];
-        if (whole) {
-            float ds[P], along = 0.0f;
-#pragma unroll
-            for (int i = 0; i < P; ++i) ds[i] = 0.0f;
-            if (a.dscores) load_values<P>(a.dscores, true, a.vec_scores, t * a.f.E, e0, a.f.E, 0.0f, ds);
-            if (softmax) {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    s[i] = exp_neg(s[i] - top) * inverse;
-                    along = __builtin_fmaf(ds[i], s[i], along);
-                }
-                along = (a.dscores ? over_lanes<L>(along, Add()) : 0.0f) + dot;
-            } else {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const float e = exp_neg(-__builtin_fabsf(s[i])), h = 1.0f / (1.0f + e);
-                    s[i] = e * h * h;  // s (1 - s)
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < P; ++i) o[i] = bad ? NAN : __builtin_fmaf(s[i], ds[i] - along, o[i]);
-        }
         if (!live) continue;  // (no lane moves follow in this round of the loop)
         const int64_t at = t * a.ld_out + e0;
         const bool wide = P >= 4 && a.vec_out && e0 + P <= a.f.E;

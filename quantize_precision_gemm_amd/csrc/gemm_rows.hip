@@ -823,8 +823,11 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
     }
 }
 
-// A linear layer's epilogue for the rows of one expert, 4 neighbouring columns
-// at a time: pre = v + bias, c = act(pre) + residual.  Rows of no expert get zeros.
+// A linear layer's epilogue for the rows of one expert: pre = v + bias, c =
+// act(pre) + residual.  Rows of no expert get zeros (their sums are 0, they get
+// no bias, and every activation of 0 is 0).  Without a residual a tile's sums go through
+// it in the accumulators' layout and are stored as other products are; a
+// residual is added by the lane that stores, 4 neighbouring columns at a time.
 template <bool kF32>
 struct Finish {
     static constexpr bool kWhole = true;
@@ -832,6 +835,41 @@ struct Finish {
     Epilogue ep;
     int64_t e, begin;  // the expert, its first row
     bool none;
+
+    __device__ __forceinline__ Finish(const Epilogue& ep_, int64_t e_, int64_t begin_, bool none_)
+        : ep(ep_), e(e_), begin(begin_), none(none_)
+    {
+    }
+    // bias of accumulators of 32 columns from n on (row tiles t): columns n + first + 8 (j / 4) + j % 4;
+    // N is a multiple of 8
+    template <class Acc, int kTiles>
+    __device__ __forceinline__ void add_bias(int64_t n, int first, int64_t N, Acc (&acc)[kTiles]) const
+    {
+        if (!ep.bias || none) return;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int64_t at = n + first + 8 * q;
+            float b[4];
+            bias_of(at < N ? at : 0, b);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[t][4 * q + j] += b[j];
+        }
+    }
+    template <class Acc, int kTiles>
+    __device__ __forceinline__ void act(Acc (&acc)[kTiles]) const
+    {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            float z[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] = acc[t][j];
+            activate<kF32>(ep.act, z);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[t][j] = z[j];
+        }
+    }
 
     __device__ __forceinline__ void bias_of(int64_t n, float (&b)[4]) const
     {
@@ -859,13 +897,16 @@ struct Finish {
     {
         float y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = none ? 0.0f : v[j] + b[j];
+        for (int j = 0; j < 4; ++j) y[j] = v[j] + b[j];
         if (ep.pre)
             *reinterpret_cast<uint2*>(ep.pre + (begin + m) * ep.ld_pre + n) =
                 make_uint2(bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]));
+        activate<kF32>(ep.act, y);
+        store_sum(m, n, y, r, c, ldc);
+    }
+    __device__ __forceinline__ void store_sum(int64_t m, int64_t n, float (&y)[4], const Raw& r, void* c, int64_t ldc) const
+    {
         const int64_t at = (begin + m) * ldc + n;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = activation(ep.act, y[j]);
         if constexpr (kF32) {
             const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -881,11 +922,11 @@ struct Finish {
     }
 };
 
-// store_wave with an epilogue: the sums are staged unrounded, 32 columns at a
-// time, and finished by the lane that stores them (rows of 32 columns: 64
-// bytes of bf16).  N is a multiple of 8, so a lane's 4 columns are all there or none.
+// store_wave with a residual: the values are staged unrounded, 32 columns at a
+// time, and the lane that stores 4 of them adds its residual (rows of 32
+// columns: 64 bytes of bf16).  N is a multiple of 8, so those 4 are all there or none.
 template <bool kF32, class Value>
-__device__ __forceinline__ void store_wave_finished(uint8_t* stage, int64_t row0, const int64_t (&col)[2], int64_t mend,
+__device__ __forceinline__ void store_wave_residual(uint8_t* stage, int64_t row0, const int64_t (&col)[2], int64_t mend,
                                                     int64_t N, void* c, int64_t ldc, const Finish<kF32>& f,
                                                     const Value& value)
 {
@@ -895,8 +936,6 @@ __device__ __forceinline__ void store_wave_finished(uint8_t* stage, int64_t row0
     for (int u = 0; u < 2; ++u) {
         const int64_t n = col[u] + 4 * p;
         const bool in = n < N;
-        float b[4];
-        f.bias_of(in ? n : 0, b);
         typename Finish<kF32>::Raw r[8];
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
@@ -918,8 +957,8 @@ __device__ __forceinline__ void store_wave_finished(uint8_t* stage, int64_t row0
             const int row = 8 * it + (lane >> 3);
             const float4 v = *reinterpret_cast<const float4*>(stage + 128 * row + ((p ^ (row & 7)) << 4));
             if (!in || row0 + row >= mend) continue;
-            const float y[4] = {v.x, v.y, v.z, v.w};
-            f.store(row0 + row, n, y, b, r[it], c, ldc);
+            float y[4] = {v.x, v.y, v.z, v.w};
+            f.store_sum(row0 + row, n, y, r[it], c, ldc);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -975,9 +1014,21 @@ __device__ __forceinline__ void tile(const View& A, const View& B, int64_t m0, i
             const int64_t col[2] = {n0 + column0<kTB>(wn, 0), n0 + column0<kTB>(wn, 1)};
             if constexpr (Convert::kWhole) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    store_wave_finished(lds + 8192 * wave, m0 + 128 * h + 64 * wm, col, mend, B.rows, c, ldc, convert,
-                                        [&](int i, int k, int e) { return acc[h][k][i][e]; });
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t row0 = m0 + 128 * h + 64 * wm;
+                    const auto sums = [&](int i, int k, int e) { return acc[h][k][i][e]; };
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) convert.add_bias(col[k], 4 * (lane >> 5), B.rows, acc[h][k]);
+                    if (convert.ep.pre)
+                        store_wave<false, false>(lds + 8192 * wave, row0, col, mend, B.rows, convert.ep.pre,
+                                                 convert.begin * convert.ep.ld_pre, convert.ep.ld_pre, sums);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) convert.act(acc[h][k]);
+                    if (convert.ep.residual)
+                        store_wave_residual(lds + 8192 * wave, row0, col, mend, B.rows, c, ldc, convert, sums);
+                    else
+                        store_wave<kF32, false>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc, sums);
+                }
                 return;
             } else {
 #pragma unroll
@@ -1001,8 +1052,18 @@ __device__ __forceinline__ void tile(const View& A, const View& B, int64_t m0, i
     }
     const int64_t row0 = m0 + 64 * wm, col[2] = {n0 + 64 * wn, n0 + 64 * wn + 32};
     if constexpr (Convert::kWhole) {
-        store_wave_finished(lds + 8192 * wave, row0, col, mend, B.rows, c, ldc, convert,
-                            [&](int i, int k, int e) { return acc[k][i][e]; });
+        const auto sums = [&](int i, int k, int e) { return acc[k][i][e]; };
+#pragma unroll
+        for (int k = 0; k < 2; ++k) convert.add_bias(col[k], 4 * (lane >> 5), B.rows, acc[k]);
+        if (convert.ep.pre)
+            store_wave<false, false>(lds + 8192 * wave, row0, col, mend, B.rows, convert.ep.pre,
+                                     convert.begin * convert.ep.ld_pre, convert.ep.ld_pre, sums);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) convert.act(acc[k]);
+        if (convert.ep.residual)
+            store_wave_residual(lds + 8192 * wave, row0, col, mend, B.rows, c, ldc, convert, sums);
+        else
+            store_wave<kF32, false>(lds + 8192 * wave, row0, col, mend, B.rows, c, c_at, ldc, sums);
     } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k) convert.columns(k, col[k], 4 * (lane >> 5));
@@ -1192,7 +1253,7 @@ __global__ __launch_bounds__(kBig ? 512 : 256, kBig ? 2 : 1) void k_linear(Group
     Place t;
     if (!place_tile<kBig, 0, kDense>(g, blockIdx.x, t)) return;
     tile<kBig, f32x16_t, false, false, kF32, false>(t.A, t.B, t.m0, t.n0, t.Ka, t.Kb, t.mend, t.steps, lds, g.c, t.c_at,
-                                                    g.ldc, Finish<kF32>{ep, t.e, t.begin, t.e >= g.E});
+                                                    g.ldc, Finish<kF32>(ep, t.e, t.begin, t.e >= g.E));
 }
 
 template <bool kF32, bool kDense>
@@ -1203,7 +1264,7 @@ __global__ __launch_bounds__(256) void k_linear_join(GroupedArgs g, Epilogue ep)
     const int r = blockIdx.x % (128 / kJoinRows) * kJoinRows + (threadIdx.x >> 5), c = 4 * (threadIdx.x & 31);
     const int64_t m = t.m0 + r, n = t.n0 + c;
     if (m >= t.mend || n >= t.B.rows) return;
-    const Finish<kF32> f{ep, t.e, t.begin, t.e >= g.E};
+    const Finish<kF32> f(ep, t.e, t.begin, t.e >= g.E);
     float b[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     f.bias_of(n, b);
     const auto res = f.residual_at(m, n);
@@ -1269,7 +1330,7 @@ __global__ __launch_bounds__(256) void k_linear_thin(GroupedArgs g, Epilogue ep)
     const bool none = s.e >= g.E;
     const View A{reinterpret_cast<const uint8_t*>(g.a + s.begin * g.lda), 2 * g.lda, s.end - s.begin};
     const View B{reinterpret_cast<const uint8_t*>(g.b + (none ? 0 : s.e) * g.b_expert), 2 * g.ldb, g.N};
-    const Finish<kF32> f{ep, s.e, s.begin, none};
+    const Finish<kF32> f(ep, s.e, s.begin, none);
     const int tm = (int)((s.end - s.begin + 16 * kM - 1) / (16 * kM));
     thin_tile<f32x4_t, kM, kThinN, kThinU>(
         A, B, none ? 0 : 2 * g.K, s.tile % tm * 16 * kM, s.tile / tm * 16 * kThinN, lds,

@@ -13,7 +13,9 @@ quantised first, by role (2.A, 2.B.2-2.B.4):
          SR for dY, RNE for X, one sign vector for both   (wgrad)
 
 A layer kept in BF16 (2.B.1) runs the same three GEMMs on the bf16 tensors;
-a layer of experts kept in BF16 runs them grouped by expert.
+a layer of experts kept in BF16 runs them grouped by expert, and a block of
+experts all of what stands around them, too: norm, router, dispatch, the two
+products with an activation between them, combine.
 
 Every operation is a library call; this module only allocates buffers (once,
 in the constructors) and orders the launches.  Nothing here computes.
@@ -299,6 +301,125 @@ class BF16Experts:
 
     def wgrad_ops(self):
         return [("experts_wgrad", lambda: self._product(self.q.WGRAD, self.dy, self.x, self.dw))]
+
+
+class BF16ExpertBlock:
+    """One block of experts kept in bf16, from a layer's output to the next
+    one's input:
+
+      h = x + residual,  n = norm(h) * norm_weight
+      logits = n router^T,  k of E experts each, their weights (nvfp4_route)
+      a = act(n w1[e]^T + b1[e]),  o = a w2[e]^T   for each token and expert of it
+      y = h + sum of the experts' o times their weights
+
+    x, residual, dy (T x H, bf16; dy: y's gradient); norm_weight (H, fp32);
+    router (E x H, bf16); w1 (E x F x H, bf16), b1 (E x F, fp32), w2 (E x H x F,
+    bf16).  H, F and E multiples of 8.  choice_bias (E, fp32, or None) balances
+    the choice; groups, groups_kept, score, renormalise and scale as for
+    nvfp4_route.
+    Outputs: y, h, routing (a Routing: experts, weights, rows, ends), dx (T x H,
+    bf16: the gradient of x and of residual), dnorm (H), drouter (E x H), dw1,
+    db1, dw2 (fp32).  x, residual and dy may be refilled from step to step.
+    """
+
+    def __init__(self, q, torch, x, residual, dy, norm_weight, router, w1, b1, w2, k, activation=None, score=None,
+                 choice_bias=None, groups=1, groups_kept=None, renormalise=True, scale=1.0, eps=1e-6):
+        self.q, self.torch = q, torch
+        self.x, self.residual, self.dy, self.norm_weight, self.router = x, residual, dy, norm_weight, router
+        self.w1, self.b1, self.w2, self.k, self.eps = w1, b1, w2, k, eps
+        self.activation = q.ACT_RELU2 if activation is None else activation
+        self.route_args = dict(score=q.SOFTMAX if score is None else score, renormalise=renormalise, scale=scale)
+        self.choice_args = dict(bias=choice_bias, groups=groups, groups_kept=groups_kept)
+        T, H = x.shape
+        E, F = w1.shape[:2]
+        assert w1.shape == (E, F, H) and w2.shape == (E, H, F) and b1.shape == (E, F) and router.shape == (E, H)
+        assert residual.shape == (T, H) and dy.shape == (T, H) and norm_weight.shape == (H,)
+        self.T, self.H, self.E, self.F, self.R = T, H, E, F, T * k
+        dev, bf16, f32 = x.device, torch.bfloat16, torch.float32
+
+        def new(*shape, dtype=bf16):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        def bytes_of(n):
+            return torch.empty(n, dtype=torch.uint8, device=dev)
+        self.h, self.n, self.y, self.dx = new(T, H), new(T, H), new(T, H), new(T, H)
+        self.logits, self.dlogits, self.dn_router = new(T, E, dtype=f32), new(T, E), new(T, H, dtype=f32)
+        self.dn = new(T, H, dtype=f32)
+        self.routing = q.Routing.empty(T, E, k, dev)
+        self.dweights = new(T, k, dtype=f32)
+        # rows by expert; those behind the last expert's (of padded tokens) are nobody's
+        self.rows, self.pre, self.act, self.o = new(self.R, H), new(self.R, F), new(self.R, F), new(self.R, H)
+        self.do, self.dact, self.dpre, self.drows = new(self.R, H), new(self.R, F), new(self.R, F), new(self.R, H)
+        self.dnorm, self.drouter = new(H, dtype=f32), new(1, E, H, dtype=f32)
+        self.dw1, self.db1, self.dw2 = new(E, F, H, dtype=f32), new(E, F, dtype=f32), new(E, H, F, dtype=f32)
+        self.all = torch.full((1,), T, dtype=torch.int32, device=dev)  # the router is a layer of one expert with all tokens
+        space = q.nvfp4_bf16_grouped_gemm_workspace
+        self.ws = {name: bytes_of(space(*args)) for name, args in {
+            "router": (q.FPROP, 1, T, E, H), "router_dgrad": (q.DGRAD, 1, T, E, H), "router_wgrad": (q.WGRAD, 1, T, E, H),
+            "up": (q.FPROP, E, self.R, F, H), "up_dgrad": (q.DGRAD, E, self.R, F, H), "up_wgrad": (q.WGRAD, E, self.R, F, H),
+            "down": (q.FPROP, E, self.R, H, F), "down_dgrad": (q.DGRAD, E, self.R, H, F),
+            "down_wgrad": (q.WGRAD, E, self.R, H, F)}.items()}
+        self.ws["norm"] = bytes_of(q.nvfp4_rmsnorm_backward_workspace(T, H))
+        self.ws["bias"] = bytes_of(q.nvfp4_bf16_linear_backward_workspace(E, self.R, F))
+
+    def flops(self):
+        return 3 * 2.0 * (2 * self.R * self.H * self.F + self.T * self.E * self.H)
+
+    def weight_ops(self):
+        return []
+
+    def _product(self, pass_, name, a, b, out, ends=None):
+        self.q.nvfp4_bf16_grouped_gemm(pass_, a, b, self.routing.ends if ends is None else ends, out=out,
+                                       workspace=self.ws[name])
+
+    def forward_ops(self):
+        q, r = self.q, self.routing
+        return [
+            ("block_norm", lambda: q.nvfp4_rmsnorm(self.x, self.norm_weight, self.eps, residual=self.residual, h=self.h,
+                                                   out=self.n)),
+            ("block_router", lambda: q.nvfp4_bf16_linear(self.n, self.router, out=self.logits, workspace=self.ws["router"])),
+            ("block_route", lambda: q.nvfp4_route(self.logits, self.k, out=r, **self.route_args, **self.choice_args)),
+            ("block_dispatch", lambda: q.nvfp4_dispatch(self.n, r.rows, out=self.rows)),
+            ("block_up", lambda: q.nvfp4_bf16_linear(self.rows, self.w1, ends=r.ends, bias=self.b1, activation=self.activation,
+                                                     pre=self.pre, out=self.act, workspace=self.ws["up"])),
+            ("block_down", lambda: self._product(q.FPROP, "down", self.act, self.w2, self.o)),
+            ("block_combine", lambda: q.nvfp4_combine(self.o, r.rows, r.weights, residual=self.h, out=self.y)),
+        ]
+
+    def backward_shared_ops(self):
+        """What dgrad and wgrad wait for: gradients of the experts' rows, of their sums and of the logits."""
+        q, r = self.q, self.routing
+        return [
+            ("block_combine_backward", lambda: q.nvfp4_combine_backward(self.dy, self.o, r.rows, r.weights, out=self.do,
+                                                                        dweights=self.dweights)),
+            ("block_down_dgrad", lambda: self._product(q.DGRAD, "down_dgrad", self.do, self.w2, self.dact)),
+            ("block_act_backward", lambda: q.nvfp4_bf16_linear_backward(self.dact, self.pre, self.activation, ends=r.ends,
+                                                                        out=self.dpre, dbias=self.db1, workspace=self.ws["bias"])),
+            ("block_route_backward", lambda: q.nvfp4_route_backward(self.logits, r.experts, self.dweights, out=self.dlogits,
+                                                                    **self.route_args)),
+        ]
+
+    def backward_quant_ops(self):
+        return []
+
+    def dgrad_ops(self):
+        q, r = self.q, self.routing
+        return [
+            ("block_up_dgrad", lambda: self._product(q.DGRAD, "up_dgrad", self.dpre, self.w1, self.drows)),
+            ("block_router_dgrad", lambda: self._product(q.DGRAD, "router_dgrad", self.dlogits, self.router[None],
+                                                         self.dn_router, self.all)),
+            ("block_dispatch_backward", lambda: q.nvfp4_combine(self.drows, r.rows, residual=self.dn_router, out=self.dn)),
+            ("block_norm_backward", lambda: q.nvfp4_rmsnorm_backward(self.dn, self.h, self.norm_weight, self.eps, dh=self.dy,
+                                                                     out=self.dx, dweight=self.dnorm, workspace=self.ws["norm"])),
+        ]
+
+    def wgrad_ops(self):
+        q = self.q
+        return [
+            ("block_router_wgrad", lambda: self._product(q.WGRAD, "router_wgrad", self.dlogits, self.n, self.drouter, self.all)),
+            ("block_down_wgrad", lambda: self._product(q.WGRAD, "down_wgrad", self.do, self.act, self.dw2)),
+            ("block_up_wgrad", lambda: self._product(q.WGRAD, "up_wgrad", self.dpre, self.rows, self.dw1)),
+        ]
 
 
 class TrainingStep:

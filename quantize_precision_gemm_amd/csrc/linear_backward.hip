@@ -20,8 +20,10 @@ namespace {
 
 // Rows of a run: 4096 waves where there are as many rows, no run shorter than
 // 8 rows (its sums are 4 bytes a column, a row moves 6) nor more than 4096 runs.
+// 16 rows are one run: without experts its sums are dbias (a second launch costs 4 us).
 int64_t run_rows(int64_t T, int64_t N)
 {
+    if (T <= 16) return 16;
     const int64_t units = (N + 511) / 512, runs = std::max<int64_t>(1, std::min<int64_t>(4096, 4096 / std::max<int64_t>(units, 1)));
     return std::max<int64_t>(8, (T + runs - 1) / runs);
 }
@@ -131,16 +133,21 @@ int64_t linear_backward_workspace(int64_t E, int64_t T, int64_t N, int cus)
     return T == 0 || N == 0 || E == 0 ? 0 : (run_count(T, N) + E) * N * (int64_t)sizeof(float);
 }
 
-void launch_linear_backward(const LinearBackArgs& a, hipStream_t s)
+bool linear_backward_one_run(const int32_t* ends, int64_t T, int64_t N) { return !ends && T > 0 && run_count(T, N) == 1; }
+
+void launch_linear_backward(const LinearBackArgs& args, hipStream_t s)
 {
+    LinearBackArgs a = args;
     if (a.N == 0) return;
+    const bool whole = linear_backward_one_run(a.ends, a.T, a.N);
+    if (whole) a.parts = a.dbias;
     const int64_t each = run_rows(a.T, a.N), runs = run_count(a.T, a.N);
     if (a.T > 0 && a.E > 0) {
         const dim3 grid((uint32_t)((runs + 3) / 4), (uint32_t)((a.N + 511) / 512));
         if (a.dbias) hipLaunchKernelGGL(k_linear_backward<true>, grid, dim3(256), 0, s, a, each);
         else hipLaunchKernelGGL(k_linear_backward<false>, grid, dim3(256), 0, s, a, each);
     }
-    if (a.dbias && a.E > 0)
+    if (a.dbias && a.E > 0 && !whole)
         hipLaunchKernelGGL(k_bias_sums, dim3((uint32_t)((a.N + 63) / 64), (uint32_t)a.E), dim3(256), 0, s, a, each);
 }
 

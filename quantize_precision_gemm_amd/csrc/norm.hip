@@ -171,7 +171,9 @@ BackPlan back_plan(int64_t rows, int64_t cols, int cus)
     const int64_t pieces = (cols + 7) / 8;
     const int held = pieces <= 64 ? 1 : 2;
     const int waves = (int)std::max<int64_t>(1, (pieces + 64 * held - 1) / (64 * held)), teams = 16 / waves;
-    return BackPlan{held, waves, teams, std::min((rows + teams - 1) / teams, (held == 1 ? 2 : 1) * (int64_t)cus)};
+    // two rows a team: one workgroup, whose sums are dweight (a second launch costs 4 us)
+    const int64_t turns = (rows + teams - 1) / teams;
+    return BackPlan{held, waves, teams, turns <= 2 ? std::min<int64_t>(turns, 1) : std::min(turns, (held == 1 ? 2 : 1) * (int64_t)cus)};
 }
 
 }  // namespace
@@ -317,7 +319,8 @@ void launch_norm(const NormArgs& a, hipStream_t s)
 
 int64_t norm_backward_workspace(int64_t rows, int64_t cols, int cus)
 {
-    return back_plan(rows, cols, cus).blocks * cols * (int64_t)sizeof(float);
+    const int64_t blocks = back_plan(rows, cols, cus).blocks;
+    return blocks > 1 ? blocks * cols * (int64_t)sizeof(float) : 0;
 }
 
 namespace {
@@ -332,9 +335,11 @@ void launch_norm_backward_of(const BackPlan& p, const NormArgs& a, hipStream_t s
 
 }  // namespace
 
-void launch_norm_backward(const NormArgs& a, hipStream_t s)
+void launch_norm_backward(const NormArgs& args, hipStream_t s)
 {
+    NormArgs a = args;
     const BackPlan p = back_plan(a.rows, a.cols, a.cus);
+    if (p.blocks == 1) a.parts = a.dweight;
     if (p.blocks > 0) {
         if (a.x_f32) {
             if (a.s_f32) launch_norm_backward_of<true, true>(p, a, s);
@@ -344,7 +349,7 @@ void launch_norm_backward(const NormArgs& a, hipStream_t s)
             else launch_norm_backward_of<false, false>(p, a, s);
         }
     }
-    if (a.dweight && a.cols > 0)
+    if (a.dweight && a.cols > 0 && p.blocks != 1)  // (no rows: zeros)
         hipLaunchKernelGGL(k_column_sums, dim3((uint32_t)((a.cols + 31) / 32)), dim3(256), 0, s, a.parts, p.blocks, a.cols,
                            a.dweight);
 }

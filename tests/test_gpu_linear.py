@@ -251,7 +251,7 @@ def test_far_values(act):
 def test_refusals():
     x, w = randn(1, 4, 64).bfloat16(), randn(2, 32, 64).bfloat16()
     ends = torch.tensor([2, 4], dtype=torch.int32, device=DEV)
-    w3 = torch.stack([w, w])
+    w3, x40 = torch.stack([w, w]), randn(3, 40, 64).bfloat16()
     for call, error in (
             (lambda: q.nvfp4_bf16_linear(x.float(), w), TypeError), (lambda: q.nvfp4_bf16_linear(x, w3), TypeError),
             (lambda: q.nvfp4_bf16_linear(x, w, ends=ends), TypeError), (lambda: q.nvfp4_bf16_linear(x, w3[:1], ends=ends), ValueError),
@@ -266,6 +266,6 @@ def test_refusals():
             (lambda: q.nvfp4_bf16_linear(x, w, activation=9), RuntimeError),
             (lambda: q.nvfp4_bf16_linear(x, w3, ends=ends.long()), ValueError),
             (lambda: q.nvfp4_bf16_linear_backward(x, x[:, :32], q.ACT_SILU), ValueError),
-            (lambda: q.nvfp4_bf16_linear_backward(x, x, q.ACT_SILU, workspace=torch.empty(16, dtype=torch.uint8, device=DEV)), ValueError)):
+            (lambda: q.nvfp4_bf16_linear_backward(x40, x40, q.ACT_SILU, workspace=torch.empty(16, dtype=torch.uint8, device=DEV)), ValueError)):
         with pytest.raises(error):
             call()

@@ -358,9 +358,9 @@ __device__ __forceinline__ uint32_t key_below(const uint32_t (&key)[P], uint32_t
 
 // The k + 1 largest of a row's keys, (value << kBits) + (2^kBits - 1 - index),
 // a value of 0: never.  Lane j of the row gets the j-th one's index (-1: there
-// is none left), `last` the last one's key.  Returns whether values no further
-// apart than `near` decided, other than those of equal logits (the row's, in
-// LDS) and biases.
+// is none left), `last` the last one's key.  Returns (in every lane of the
+// row) whether values no further apart than `near` decided, other than those of equal
+// logits (the row's, in LDS) and biases.
 template <int L, int P>
 __device__ __forceinline__ bool pick(const RouteArgs& a, const float* logits, const uint32_t (&key)[P], uint32_t near,
                                      int& mine, uint32_t& last)
@@ -368,21 +368,21 @@ __device__ __forceinline__ bool pick(const RouteArgs& a, const float* logits, co
     constexpr int kBits = __builtin_ctz(L * P);
     constexpr uint32_t kMask = (1u << kBits) - 1;
     const int sub = threadIdx.x & (L - 1);
-    mine = -1;
+    uint32_t own = 0;
     last = 0;
-    bool close = false;
     for (int r = 0; r <= a.k; ++r) {
-        const uint32_t best = key_below<L, P>(key, last);
-        const bool some = best > kMask;
-        const int e = (int)(kMask - (best & kMask));
-        if (r > 0 && some && (last >> kBits) - (best >> kBits) <= near) {
-            const int was = (int)(kMask - (last & kMask));  // equal logits and biases make equal values
-            close |= logits[was] != logits[e] || (a.bias && a.bias[was] != a.bias[e]);
-        }
-        if (sub == r) mine = some ? e : -1;
-        last = best;
+        last = key_below<L, P>(key, last);
+        own = sub == r ? last : own;
     }
-    return close;
+    // each with the next one (lane j + 1's; a 17th has no lane)
+    uint32_t next = (uint32_t)lane_move<0x101>((int)last, (int)own);
+    if (sub == a.k - 1) next = last;
+    const int e = (int)(kMask - (own & kMask)), after = (int)(kMask - (next & kMask));
+    bool close = false;
+    if (sub < a.k && next > kMask && (own >> kBits) - (next >> kBits) <= near)  // equal logits and biases make equal values
+        close = logits[e] != logits[after] || (a.bias && a.bias[e] != a.bias[after]);
+    mine = own > kMask ? e : -1;
+    return own_bits<L>(__ballot(close)) != 0;
 }
 
 __device__ __forceinline__ double sigmoid64(float l)
@@ -648,7 +648,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a)
         }
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            key[i] = (whole_of(__builtin_fmaf(c[i], unit, offset)) << kBits) + ((1u << kBits) - 1 - (e0 + i));
+            key[i] = (whole_of(__builtin_fmaf(c[i], unit, offset)) << kBits | ((1u << kBits) - P - e0)) | (P - 1 - i);
         // the row's logits, for the comparisons of equals and the weights
 #pragma unroll
         for (int i = 0; i < P; ++i) own[e0 + i] = l[i];
@@ -710,6 +710,18 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a)
     }
 }
 
+// v of this lane and of the one kLanes (16 or 32) away, by the instruction that
+// exchanges the two registers' rows or halves.
+template <int kLanes>
+__device__ __forceinline__ uint32_t sum_of_halves(uint32_t v)
+{
+    typedef uint32_t Pair __attribute__((ext_vector_type(2)));
+    Pair p;
+    if constexpr (kLanes == 16) p = __builtin_bit_cast(Pair, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+    else p = __builtin_bit_cast(Pair, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+    return p.x + p.y;
+}
+
 // The places of a chunk's slots.  Each workgroup adds up all chunks' counts
 // (256 chunks of 256 experts are 64 KB, in the L2), those before its own and
 // all of them, 16 experts a lane in pairs of 16 bits (256 chunks of 64 tokens fit); or
@@ -746,9 +758,18 @@ __global__ __launch_bounds__(kThreads) void k_route_place(RouteArgs a, int chunk
                 n[2 * j + 1] += w[j] >> 8 & earlier;
             }
         }
-        for (int d = lanes; d < 64; d <<= 1)
+        for (int d = lanes; d < 8; d <<= 1)  // (up to 64 experts)
 #pragma unroll
             for (int j = 0; j < 16; ++j) n[j] += (uint32_t)__shfl_xor((int)n[j], d, 64);
+        if (lanes <= 8)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) n[j] += (uint32_t)lane_turn<0x128>((int)n[j]);
+        if (lanes <= 16)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) n[j] = sum_of_halves<16>(n[j]);
+        if (lanes <= 32)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) n[j] = sum_of_halves<32>(n[j]);
         if ((tid & 63) < lanes) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) part[wave_index()][at][j] = n[j];

@@ -741,7 +741,7 @@ int nvfp4_route_backward(const void* logits, int32_t l_dtype, int64_t ld, int64_
 
 /*
  * nvfp4_dispatch -- tokens into the experts' order: out[rows[t, j]] = x[t].
- *   x, out    bf16, T and R rows of cols, a multiple of 8, 16-byte aligned,
+ *   x, out    bf16, T and R rows of cols, a multiple of 8 (up to 2^24), 16-byte aligned,
  *             pitches multiples of 8.  rows: T x k int32 (k 1 to 64), as nvfp4_route writes them; a place
  *             outside [0, R) is skipped, and rows that no slot names are left
  *             as they are.  A place named twice gets either token.
@@ -765,7 +765,8 @@ int nvfp4_combine(const void* o, int32_t o_dtype, int64_t ld_o, int64_t R, const
 /*
  * nvfp4_combine_backward -- do[rows[t, j]] = weights[t, j] dy[t] (bf16) and
  * dweights[t, j] = sum_c dy[t, c] o[rows[t, j], c] (fp32; 0 for a place outside [0, R)).
- * Rows of do that no slot names are left as they are.  (residual's gradient is dy.)
+ * Rows of do that no slot names are left as they are; do may be o itself (bf16,
+ * same pitch, no place named twice).  (residual's gradient is dy.)
  */
 int nvfp4_combine_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const void* o, int32_t o_dtype,
                            int64_t ld_o, int64_t R, const int32_t* rows, const float* weights, int64_t T, int64_t k,
@@ -832,7 +833,8 @@ int nvfp4_bf16_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
  *   dy        T x N fp32 or bf16; pre, dpre bf16 (dpre may be pre, or a bf16 dy itself);
  *             pre NULL with NVFP4_ACT_NONE: dpre is dy, and only dbias is computed.
  *             Rows of no expert are left as they are.
- *   dbias     or NULL (then pre is needed).  N a multiple of 8, E below 65536.
+ *   dbias     or NULL (then pre is needed).  N a multiple of 8 up to 2^24, E below
+ *             65536, E N below 2^30.
  *   workspace with dbias: nvfp4_bf16_linear_backward_workspace bytes, 16-byte
  *             aligned (none for up to 16 rows without ends); calls that share it must not overlap.
  *   Bases 16-byte aligned; pitches multiples of 8 (bf16) or 4 (fp32).

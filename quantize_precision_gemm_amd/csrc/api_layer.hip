@@ -20,7 +20,7 @@ using nvfp4::holds;
 using nvfp4::launch_status;
 
 constexpr int64_t kRowLimit = int64_t(1) << 31;
-constexpr int64_t kColLimit = int64_t(1) << 25;  // columns of a row kernel: its grid counts units of 512 in 16 bits
+constexpr int64_t kColLimit = int64_t(1) << 24;  // columns of a row kernel: its grid counts units of 512 in 16 bits
 
 bool known(int32_t dtype) { return dtype == NVFP4_OUT_BF16 || dtype == NVFP4_OUT_FP32; }
 
@@ -81,6 +81,14 @@ int check_norm(int64_t rows, int64_t cols, int32_t x_dtype, int32_t s_dtype, int
         return NVFP4_ERR_MODE;
     if (rows < 0 || rows >= kRowLimit || cols < 0 || cols >= kRowLimit || cols % 8) return NVFP4_ERR_SHAPE;
     return aligned(weight, 16) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
+// Sizes of a linear layer's gradients: the sums of the biases take a workgroup
+// of 256 threads for 64 columns of an expert, in one grid.
+bool fits_linear_backward(int64_t E, int64_t T, int64_t N)
+{
+    return E >= 0 && E <= 65535 && T >= 0 && T < kRowLimit && N >= 0 && N % 8 == 0 && N <= kColLimit &&
+           E * ((N + 63) / 64) < (int64_t(1) << 24);
 }
 
 float norm_eps(double eps)
@@ -369,7 +377,7 @@ int nvfp4_bf16_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
 int nvfp4_bf16_linear_backward_workspace(int64_t E, int64_t T, int64_t N, int64_t* bytes)
 {
     if (!bytes) return NVFP4_ERR_NULL;
-    if (E < 0 || E > 65535 || T < 0 || T >= kRowLimit || N < 0 || N % 8 || N > kColLimit) return NVFP4_ERR_SHAPE;
+    if (!fits_linear_backward(E, T, N)) return NVFP4_ERR_SHAPE;
     *bytes = nvfp4::linear_backward_workspace(E, T, N, std::max(device_cus(), 1));
     return NVFP4_OK;
 }
@@ -380,8 +388,7 @@ int nvfp4_bf16_linear_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, 
 {
     if (!known(dy_dtype) || act < NVFP4_ACT_NONE || act > NVFP4_ACT_GELU) return NVFP4_ERR_MODE;
     if (!pre && act != NVFP4_ACT_NONE && T > 0 && N > 0) return NVFP4_ERR_NULL;
-    if (E < 0 || E > 65535 || T < 0 || T >= kRowLimit || N < 0 || N % 8 || N > kColLimit || workspace_bytes < 0)
-        return NVFP4_ERR_SHAPE;
+    if (!fits_linear_backward(E, T, N) || workspace_bytes < 0) return NVFP4_ERR_SHAPE;
     if (!ends && E > 1) return NVFP4_ERR_NULL;
     if (T > 0 && N > 0 && E > 0 && (!dy || (pre && !dpre) || (!pre && !dbias))) return NVFP4_ERR_NULL;
     int st = check_rows(dy, ld_dy, N, dy_dtype);

@@ -19,7 +19,7 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int64_t kMostBlocks = int64_t(1) << 22;  // of a launch; each takes more tokens beyond that
+constexpr int64_t kMostBlocks = int64_t(1) << 21;  // of a launch (a grid has fewer than 2^32 threads); each takes more tokens beyond that
 
 __device__ __forceinline__ bool inside(int64_t place, int64_t R) { return (uint64_t)place < (uint64_t)R; }
 

@@ -19,7 +19,7 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int64_t kMostBlocks = int64_t(1) << 22;  // of a launch; each takes more rows beyond that
+constexpr int64_t kMostBlocks = int64_t(1) << 21;  // of a launch (a grid has fewer than 2^32 threads); each takes more rows beyond that
 constexpr int kHeld = 2;                           // pieces of 8 columns that a lane keeps
 
 __device__ __forceinline__ Piece sum_of(const NormArgs& a, int64_t row, int64_t c)

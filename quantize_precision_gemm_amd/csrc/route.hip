@@ -635,16 +635,16 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a)
         } else {
             float least = INFINITY;
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                least = min_of(l[i] > -INFINITY ? l[i] : INFINITY, least);
-                c[i] = (kMode == 0 ? l[i] : c[i] > -INFINITY ? l[i] : -INFINITY) - top;
-            }
+            for (int i = 0; i < P; ++i) least = min_of(l[i] > -INFINITY ? l[i] : INFINITY, least);
             least = over_lanes<L>(least, Min());
             const float range = min_of(max_of(top - least, 1e-30f), 16.0f);
             unit = kMost / range;
             offset = kMost + kLeast;
 #pragma unroll
-            for (int i = 0; i < P; ++i) c[i] = c[i] > -INFINITY ? max_of(c[i], -range) : c[i];
+            for (int i = 0; i < P; ++i) {  // (a difference that overflows is far down, not nothing)
+                const bool may = (kMode == 0 ? l[i] : c[i]) > -INFINITY;
+                c[i] = may ? max_of(l[i] - top, -range) : -INFINITY;
+            }
         }
 #pragma unroll
         for (int i = 0; i < P; ++i)

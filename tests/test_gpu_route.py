@@ -212,6 +212,24 @@ def test_masked_and_not_finite(groups, kept, score, biased):
     check(torch.full((70, E), -torch.inf, device=DEV), k, score, bias, groups, kept)
 
 
+@pytest.mark.parametrize("E,k", [(8, 8), (20, 5), (256, 4)])
+@pytest.mark.parametrize("score", [q.SOFTMAX, q.SIGMOID])
+def test_values_far_apart(E, k, score):
+    """Finite logits whose differences overflow, or pass what the fast comparison spans; biases of any size."""
+    big = torch.finfo(torch.float32).max
+    logits = randn(1, 12, E)
+    logits[0, :3] = torch.tensor([big, -big, -big], device=DEV)
+    logits[1] = -big
+    logits[1, 2] = big
+    logits[2] = torch.linspace(-big, big, E, device=DEV)
+    logits[3] = 1e-38 * logits[3]
+    logits[4, 1:] -= 40.0
+    logits[5, k - 1:] -= 1e6
+    check(logits, k, score)
+    for size in (1e-30, 5.0, 1e8, 1e38, 3e38):
+        check(logits, k, score, size * randn(2, E, scale=0.5).clamp(-1, 1))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("E,pitch,offset", [(64, 68, 0), (64, 67, 0), (64, 72, 3), (33, 33, 0), (256, 261, 1), (300, 512, 0)])
 def test_strides_and_alignment(E, pitch, offset, dtype):

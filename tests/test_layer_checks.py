@@ -76,7 +76,7 @@ def test_route_backward_validation(lib, change, status):
 MOVE = dict(x=FAKE, xd=0, ldx=64, o=FAKE, od=0, ldo=64, R=40, rows=FAKE, w=FAKE, T=10, k=4, cols=64, r=FAKE, ldr=64, y=FAKE, ldy=64,
             yd=0, dw=FAKE)
 SIZES = [({"T": -1}, -2), ({"T": BIG}, -2), ({"k": 0}, -2), ({"k": 65}, -2), ({"cols": 60}, -2), ({"cols": -8}, -2), ({"R": -1}, -2),
-         ({"R": BIG}, -2), ({"cols": (1 << 25) + 8, "ldx": 1 << 26, "ldo": 1 << 26, "ldy": 1 << 26, "ldr": 1 << 26}, -2),
+         ({"R": BIG}, -2), ({"cols": (1 << 24) + 8, "ldx": 1 << 26, "ldo": 1 << 26, "ldy": 1 << 26, "ldr": 1 << 26}, -2),
          ({"rows": None}, -1), ({"rows": FAKE + 2}, -3), ({"y": FAKE + 8}, -3), ({"ldy": 56}, -2), ({"ldy": 68}, -3), ({"y": None}, -1)]
 
 
@@ -167,6 +167,7 @@ LINB = dict(dy=FAKE, dd=0, ldd=32, pre=FAKE, ldp=32, act=1, ends=FAKE, E=4, T=10
 
 @pytest.mark.parametrize("change,status", [
     ({"dd": 2}, -4), ({"act": 4}, -4), ({"E": -1}, -2), ({"E": 65536}, -2), ({"T": -1}, -2), ({"T": BIG}, -2), ({"N": 36}, -2),
+    ({"N": (1 << 24) + 8, "ldd": 1 << 25, "ldp": 1 << 25, "ldo": 1 << 25}, -2), ({"E": 65535, "N": 16392, "ldd": 16392, "ldp": 16392, "ldo": 16392}, -2),
     ({"wb": -1}, -2), ({"pre": None}, -1), ({"ends": None}, -1), ({"dy": None}, -1), ({"out": None}, -1),
     ({"pre": None, "act": 0, "db": None}, -1), ({"dy": FAKE + 8}, -3), ({"pre": FAKE + 8}, -3), ({"out": FAKE + 8}, -3),
     ({"db": FAKE + 4}, -3), ({"ws": FAKE + 4}, -3), ({"ends": FAKE + 1}, -3), ({"ldd": 24}, -2), ({"ldp": 24}, -2), ({"ldo": 24}, -2),

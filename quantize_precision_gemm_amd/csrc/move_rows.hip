@@ -25,13 +25,29 @@ __device__ __forceinline__ bool inside(int64_t place, int64_t R) { return (uint6
 
 }  // namespace
 
-// A wave moves kPieces x 64 pieces of 16 bytes of one token.
-template <int kPieces>
+// A workgroup takes one unit of columns of four tokens, a wave each; workgroups
+// that follow each other take the units of the same tokens, so that whole rows
+// are in flight together.  (8192 tokens, 8 rows of 2048: combine 67 us, with all
+// tokens' first unit before the second 85; dispatch 54 and 61.)
+struct Turn {
+    int64_t unit, token, step;
+    __device__ __forceinline__ Turn(const MoveArgs& a, int width)
+    {
+        const uint32_t units = (uint32_t)((a.cols + width - 1) / width), first = blockIdx.x / units;
+        unit = blockIdx.x - first * units;
+        token = 4 * (int64_t)first + wave_index();
+        step = 4 * (int64_t)(gridDim.x / units);
+    }
+};
+
+// A wave moves two pieces of 16 bytes a lane.  (8192 tokens of 5120 columns to 4
+// rows: 82 us, one piece 86, four 87.)
 __global__ __launch_bounds__(256) void k_dispatch(MoveArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t c0 = 8 * ((int64_t)blockIdx.y * 64 * kPieces + lane);
-    for (int64_t t = (int64_t)blockIdx.x * 4 + wave_index(); t < a.T; t += (int64_t)gridDim.x * 4) {
+    constexpr int kPieces = 2;
+    const Turn turn(a, 512 * kPieces);
+    const int64_t c0 = 512 * kPieces * turn.unit + 8 * (threadIdx.x & 63);
+    for (int64_t t = turn.token; t < a.T; t += turn.step) {
         const uint16_t* src = static_cast<const uint16_t*>(a.tokens) + t * a.ld_tokens;
         uint4 v[kPieces];
 #pragma unroll
@@ -52,58 +68,44 @@ __global__ __launch_bounds__(256) void k_dispatch(MoveArgs a)
     }
 }
 
-// A wave adds up kPieces x 64 pieces of 8 columns of one token, four of its
-// rows in flight.
-template <int kPieces>
+// A wave adds up 512 columns of one token, four of its rows in flight.  (1024
+// columns, or eight rows, hold more registers than they hide latency: 8192
+// tokens of 4 rows of 5120 103 us, 105, 122.)
 __global__ __launch_bounds__(256) void k_combine(MoveArgs a)
 {
     constexpr int kAhead = 4;
-    const int lane = threadIdx.x & 63;
-    const int64_t c0 = 8 * ((int64_t)blockIdx.y * 64 * kPieces + lane);
-    for (int64_t t = (int64_t)blockIdx.x * 4 + wave_index(); t < a.T; t += (int64_t)gridDim.x * 4) {
-        Piece sum[kPieces];
+    const Turn turn(a, 512);
+    const int64_t c = 512 * turn.unit + 8 * (threadIdx.x & 63);
+    for (int64_t t = turn.token; t < a.T; t += turn.step) {
+        Piece sum;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[i].v[e] = 0.0f;
+        for (int e = 0; e < 8; ++e) sum.v[e] = 0.0f;
         for (int j0 = 0; j0 < a.k; j0 += kAhead) {
-            RawPiece raw[kAhead][kPieces];
+            RawPiece raw[kAhead];
             float w[kAhead];
-            bool there[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const bool in = j0 + u < a.k;
                 const int64_t slot = t * a.k + (in ? j0 + u : j0);
                 const int64_t place = a.rows[slot];
-                there[u] = in && inside(place, a.R);
                 w[u] = !in ? 0.0f : a.weights ? a.weights[slot] : 1.0f;
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int64_t c = c0 + 512 * i;
-                    raw[u][i].a = raw[u][i].b = make_uint4(0, 0, 0, 0);
-                    if (there[u] && c < a.cols) raw[u][i] = load_raw(a.from, place * a.ld_from + c, a.from_f32);
-                }
+                raw[u] = RawPiece{};
+                if (in && inside(place, a.R) && c < a.cols) raw[u] = load_raw(a.from, place * a.ld_from + c, a.from_f32);
             }
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
+            for (int u = 0; u < kAhead; ++u) {
+                const Piece o = widen(raw[u], a.from_f32);
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const Piece o = widen(raw[u][i], a.from_f32);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sum[i].v[e] = __builtin_fmaf(w[u], o.v[e], sum[i].v[e]);
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int64_t c = c0 + 512 * i;
-            if (c >= a.cols) continue;
-            if (a.tokens) {
-                const Piece r = load_piece(a.tokens, t * a.ld_tokens + c, a.out_f32);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[i].v[e] += r.v[e];
+                for (int e = 0; e < 8; ++e) sum.v[e] = __builtin_fmaf(w[u], o.v[e], sum.v[e]);
             }
-            store_piece(a.out, t * a.ld_out + c, sum[i], a.out_f32);
         }
+        if (c >= a.cols) continue;
+        if (a.tokens) {
+            const Piece r = load_piece(a.tokens, t * a.ld_tokens + c, a.out_f32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum.v[e] += r.v[e];
+        }
+        store_piece(a.out, t * a.ld_out + c, sum, a.out_f32);
     }
 }
 
@@ -188,31 +190,17 @@ __global__ __launch_bounds__(kSolo ? 256 : 1024) void k_combine_backward(MoveArg
 
 namespace {
 
-template <class Kernel>
-void launch_pieces(Kernel kernel, int pieces, const MoveArgs& a, hipStream_t s)
+void launch_turns(void (*kernel)(MoveArgs), int width, const MoveArgs& a, hipStream_t s)
 {
-    const int64_t blocks = (a.T + 3) / 4, units = (a.cols / 8 + 64 * pieces - 1) / (64 * pieces);
-    const int64_t most = kMostBlocks / units > 0 ? kMostBlocks / units : 1;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)(blocks < most ? blocks : most), (uint32_t)units), dim3(256), 0, s, a);
+    const int64_t units = (a.cols + width - 1) / width, blocks = std::min((a.T + 3) / 4, std::max<int64_t>(1, kMostBlocks / units));
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(blocks * units)), dim3(256), 0, s, a);
 }
 
 }  // namespace
 
-void launch_dispatch(const MoveArgs& a, hipStream_t s)
-{
-    if (a.cols > 512)
-        launch_pieces(k_dispatch<2>, 2, a, s);
-    else
-        launch_pieces(k_dispatch<1>, 1, a, s);
-}
+void launch_dispatch(const MoveArgs& a, hipStream_t s) { launch_turns(k_dispatch, 1024, a, s); }
 
-void launch_combine(const MoveArgs& a, hipStream_t s)
-{
-    if (a.cols > 512)
-        launch_pieces(k_combine<2>, 2, a, s);
-    else
-        launch_pieces(k_combine<1>, 1, a, s);
-}
+void launch_combine(const MoveArgs& a, hipStream_t s) { launch_turns(k_combine, 512, a, s); }
 
 namespace {
 

@@ -64,17 +64,24 @@ __device__ __forceinline__ uint2 codes_of(const Piece& y, float lift, float fact
 
 }  // namespace
 
-// kSolo: a wave a row, four rows a workgroup; otherwise a workgroup a row, as
-// many waves as its columns fill (16 at most).
-template <bool kSolo, bool kI8>
-__global__ __launch_bounds__(kSolo ? 256 : 1024) void k_norm(NormArgs a)
+// kLanes 16, 32 or 64: so many lanes a row (of up to 128, 256, 1024 columns), 256 /
+// kLanes rows a workgroup.  0: a workgroup a row, as many waves as its columns fill (16 at most).
+// (65536 x 128, a head's norm: 16 lanes a row 13 us, a wave 30.)
+template <int kLanes, bool kI8>
+__global__ __launch_bounds__(kLanes ? 256 : 1024) void k_norm(NormArgs a)
 {
+    constexpr bool kSolo = kLanes > 0;
+    constexpr int kHeld = kLanes == 16 || kLanes == 32 ? 1 : nvfp4::kHeld, kRows = kSolo ? 256 / kLanes : 1;
     __shared__ float part[2][16];
-    const int lanes = kSolo ? 64 : blockDim.x, lane = kSolo ? threadIdx.x & 63 : threadIdx.x, wave = wave_index();
-    const int waves = lanes / 64;
+    const int lanes = kSolo ? kLanes : blockDim.x, lane = kSolo ? threadIdx.x & (kLanes - 1) : threadIdx.x;
+    const int wave = wave_index(), waves = lanes / 64;
     const float each = 1.0f / (float)a.cols;
-    for (int64_t row = kSolo ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x; row < a.rows;
-         row += (int64_t)gridDim.x * (kSolo ? 4 : 1)) {
+    // (all lanes go through the lane moves: rows beyond the last one are its copies, not written)
+    const int64_t rows = kSolo ? (a.rows + kRows - 1) / kRows * kRows : a.rows;
+    for (int64_t at = kSolo ? (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes : blockIdx.x; at < rows;
+         at += (int64_t)gridDim.x * kRows) {
+        const bool live = at < a.rows;
+        const int64_t row = live ? at : a.rows - 1;
         Piece h[kHeld];
         float sum = 0.0f;
         const auto square = [&](const Piece& p) {
@@ -100,12 +107,12 @@ __global__ __launch_bounds__(kSolo ? 256 : 1024) void k_norm(NormArgs a)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[i].v[e] += d.v[e];
                 square(h[i]);
-                if (a.h && c < a.cols) store_piece(a.h, row * a.ld_h + c, h[i], a.s_f32);
+                if (a.h && c < a.cols && live) store_piece(a.h, row * a.ld_h + c, h[i], a.s_f32);
             }
         }
         const int64_t rest = 8 * (lane + (int64_t)lanes * kHeld);  // what is not kept is read again
         for (int64_t c = rest; c < a.cols; c += 8 * lanes) square(sum_of(a, row, c));
-        sum = wave_sum(sum);
+        sum = group_sum<kSolo ? kLanes : 64>(sum);
         if constexpr (!kSolo) {
             if ((threadIdx.x & 63) == 0) part[0][wave] = sum;
             __syncthreads();
@@ -119,7 +126,7 @@ __global__ __launch_bounds__(kSolo ? 256 : 1024) void k_norm(NormArgs a)
             const int64_t c = 8 * (lane + (int64_t)lanes * i);
             if (c >= a.cols) continue;
             scale_piece(a, c, rstd, h[i], top);
-            if (a.y) store_piece(a.y, row * a.ld_y + c, h[i], false);
+            if (a.y && live) store_piece(a.y, row * a.ld_y + c, h[i], false);
         }
         for (int64_t c = rest; c < a.cols; c += 8 * lanes) {
             Piece p = sum_of(a, row, c);
@@ -128,7 +135,7 @@ __global__ __launch_bounds__(kSolo ? 256 : 1024) void k_norm(NormArgs a)
             if (a.y) store_piece(a.y, row * a.ld_y + c, p, false);
         }
         if constexpr (kI8) {
-            top = wave_top(top);
+            top = group_top<kSolo ? kLanes : 64>(top);
             if constexpr (!kSolo) {
                 if ((threadIdx.x & 63) == 0) part[1][wave] = top;
                 __syncthreads();
@@ -136,14 +143,14 @@ __global__ __launch_bounds__(kSolo ? 256 : 1024) void k_norm(NormArgs a)
                 for (int v = 0; v < waves; ++v) most = max(most, __float_as_uint(part[1][v]));
                 top = __uint_as_float(most);
             }
-            if (lane == 0) a.scales[row] = top / 127.0f;
+            if (lane == 0 && live) a.scales[row] = top / 127.0f;
             // a power of two on both sides of the quotient keeps 127 / max finite
             const float lift = top < 0x1p-100f ? 0x1p64f : 1.0f;
             const float factor = top > 0.0f ? 127.0f / (top * lift) : 0.0f;
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
                 const int64_t c = 8 * (lane + (int64_t)lanes * i);
-                if (c < a.cols) *reinterpret_cast<uint2*>(a.codes + row * a.ld_codes + c) = codes_of(h[i], lift, factor);
+                if (c < a.cols && live) *reinterpret_cast<uint2*>(a.codes + row * a.ld_codes + c) = codes_of(h[i], lift, factor);
             }
             for (int64_t c = rest; c < a.cols; c += 8 * lanes) {
                 Piece p = sum_of(a, row, c);
@@ -162,6 +169,7 @@ namespace {
 // How the backward pass goes through rows of `cols` columns: pieces of 8 a
 // lane, waves a row, rows that a workgroup takes at a time (teams), and workgroups.
 struct BackPlan {
+    int lanes;  // 16 or 32: so many a row; 64: its waves'
     int held, waves, teams;
     int64_t blocks;
 };
@@ -169,11 +177,11 @@ struct BackPlan {
 BackPlan back_plan(int64_t rows, int64_t cols, int cus)
 {
     const int64_t pieces = (cols + 7) / 8;
-    const int held = pieces <= 64 ? 1 : 2;
-    const int waves = (int)std::max<int64_t>(1, (pieces + 64 * held - 1) / (64 * held)), teams = 16 / waves;
+    const int held = pieces <= 64 ? 1 : 2, lanes = pieces <= 16 ? 16 : pieces <= 32 ? 32 : 64;
+    const int waves = (int)std::max<int64_t>(1, (pieces + 64 * held - 1) / (64 * held)), teams = 16 / waves * (64 / lanes);
     // two rows a team: one workgroup, whose sums are dweight (a second launch costs 4 us)
     const int64_t turns = (rows + teams - 1) / teams;
-    return BackPlan{held, waves, teams, turns <= 2 ? std::min<int64_t>(turns, 1) : std::min(turns, (held == 1 ? 2 : 1) * (int64_t)cus)};
+    return BackPlan{lanes, held, waves, teams, turns <= 2 ? std::min<int64_t>(turns, 1) : std::min(turns, (held == 1 ? 2 : 1) * (int64_t)cus)};
 }
 
 }  // namespace
@@ -185,12 +193,14 @@ BackPlan back_plan(int64_t rows, int64_t cols, int cus)
 // for one workgroup of 16 waves on a compute unit, those of one piece for two.
 // 8192 x 5120, us: 3 rows at a time 70.2 (with the sums' kernel), one 79, one with the next's
 // loads in flight 80 to 85.
-template <int kBackHeld, bool kDyF32, bool kSF32>
+// kLanes 16 or 32: so many lanes a row.
+template <int kBackHeld, int kLanes, bool kDyF32, bool kSF32>
 __global__ __launch_bounds__(1024) void k_norm_backward(NormArgs a, int waves, int teams)
 {
     __shared__ float part[2][2][16];
     __shared__ __attribute__((aligned(16))) float sums[kNormMostCols];
-    const int wave = wave_index(), team = wave / waves, lanes = 64 * waves, lane = (int)threadIdx.x - team * lanes;
+    const int wave = wave_index(), team = kLanes < 64 ? threadIdx.x / kLanes : wave / waves;
+    const int lanes = kLanes < 64 ? kLanes : 64 * waves, lane = (int)threadIdx.x - team * lanes;
     const float each = 1.0f / (float)a.cols;
     Piece w[kBackHeld], dw[kBackHeld];
     bool in[kBackHeld];
@@ -227,8 +237,8 @@ __global__ __launch_bounds__(1024) void k_norm_backward(NormArgs a, int waves, i
                 along = __builtin_fmaf(d.v[e] * w[i].v[e], x.v[e], along);
             }
         }
-        squares = wave_sum(squares);
-        along = wave_sum(along);
+        squares = group_sum<kLanes>(squares);
+        along = group_sum<kLanes>(along);
         if (waves > 1) {
             if ((threadIdx.x & 63) == 0) {
                 part[turn][0][wave] = squares;
@@ -258,9 +268,19 @@ __global__ __launch_bounds__(1024) void k_norm_backward(NormArgs a, int waves, i
         }
     }
     if (!a.dweight) return;
-    for (int k = 0; k < teams; ++k) {
+    if constexpr (kLanes < 64) {  // the rows of a wave: the first one's lanes get their sums
+#pragma unroll
+        for (int i = 0; i < kBackHeld; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if constexpr (kLanes == 16) dw[i].v[e] = sum_of_halves<16>(dw[i].v[e]);
+                dw[i].v[e] = sum_of_halves<32>(dw[i].v[e]);
+            }
+    }
+    const int parts = kLanes < 64 ? 16 : teams, own = kLanes < 64 ? wave : team;
+    for (int k = 0; k < parts; ++k) {
         __syncthreads();
-        if (team != k) continue;
+        if (own != k || (kLanes < 64 && (threadIdx.x & 63) >= kLanes)) continue;
 #pragma unroll
         for (int i = 0; i < kBackHeld; ++i) {
             const int64_t c = 8 * (lane + (int64_t)lanes * i);
@@ -270,7 +290,7 @@ __global__ __launch_bounds__(1024) void k_norm_backward(NormArgs a, int waves, i
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dw[i].v[e] += before.v[e];
             }
-            if (k + 1 < teams) store_piece(sums, c, dw[i], true);
+            if (k + 1 < parts) store_piece(sums, c, dw[i], true);
             else store_piece(a.parts, (int64_t)blockIdx.x * a.cols + c, dw[i], true);
         }
     }
@@ -301,20 +321,27 @@ __global__ __launch_bounds__(256) void k_column_sums(const float* __restrict__ p
     *reinterpret_cast<float4*>(out + c) = sum;
 }
 
+namespace {
+
+template <int kLanes>
+void launch_norm_of(const NormArgs& a, hipStream_t s)
+{
+    const int64_t waves = std::min<int64_t>(16, (a.cols / 8 + 64 * kHeld - 1) / (64 * kHeld));
+    const int64_t blocks = kLanes ? (a.rows + 256 / (kLanes ? kLanes : 1) - 1) / (256 / (kLanes ? kLanes : 1)) : a.rows;
+    const dim3 grid((uint32_t)std::min(blocks, kMostBlocks)), block((uint32_t)(kLanes ? 256 : 64 * waves));
+    if (a.codes) hipLaunchKernelGGL((k_norm<kLanes, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_norm<kLanes, false>), grid, block, 0, s, a);
+}
+
+}  // namespace
+
 void launch_norm(const NormArgs& a, hipStream_t s)
 {
     if (a.rows == 0) return;
-    const int64_t waves = std::max<int64_t>(1, std::min<int64_t>(16, (a.cols / 8 + 64 * kHeld - 1) / (64 * kHeld)));
-    const bool solo = waves == 1;
-    const int64_t blocks = solo ? (a.rows + 3) / 4 : a.rows;
-    const dim3 grid((uint32_t)std::min(blocks, kMostBlocks)), block((uint32_t)(solo ? 256 : 64 * waves));
-    if (a.codes) {
-        if (solo) hipLaunchKernelGGL((k_norm<true, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_norm<false, true>), grid, block, 0, s, a);
-    } else {
-        if (solo) hipLaunchKernelGGL((k_norm<true, false>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((k_norm<false, false>), grid, block, 0, s, a);
-    }
+    if (a.cols <= 128) launch_norm_of<16>(a, s);
+    else if (a.cols <= 256) launch_norm_of<32>(a, s);
+    else if (a.cols <= 512 * kHeld) launch_norm_of<64>(a, s);
+    else launch_norm_of<0>(a, s);
 }
 
 int64_t norm_backward_workspace(int64_t rows, int64_t cols, int cus)
@@ -328,9 +355,11 @@ namespace {
 template <bool kDyF32, bool kSF32>
 void launch_norm_backward_of(const BackPlan& p, const NormArgs& a, hipStream_t s)
 {
-    const dim3 grid((uint32_t)p.blocks), block((uint32_t)(64 * p.waves * p.teams));
-    if (p.held == 1) hipLaunchKernelGGL((k_norm_backward<1, kDyF32, kSF32>), grid, block, 0, s, a, p.waves, p.teams);
-    else hipLaunchKernelGGL((k_norm_backward<2, kDyF32, kSF32>), grid, block, 0, s, a, p.waves, p.teams);
+    const dim3 grid((uint32_t)p.blocks), block((uint32_t)(p.lanes * p.waves * p.teams));
+    if (p.lanes == 16) hipLaunchKernelGGL((k_norm_backward<1, 16, kDyF32, kSF32>), grid, block, 0, s, a, p.waves, p.teams);
+    else if (p.lanes == 32) hipLaunchKernelGGL((k_norm_backward<1, 32, kDyF32, kSF32>), grid, block, 0, s, a, p.waves, p.teams);
+    else if (p.held == 1) hipLaunchKernelGGL((k_norm_backward<1, 64, kDyF32, kSF32>), grid, block, 0, s, a, p.waves, p.teams);
+    else hipLaunchKernelGGL((k_norm_backward<2, 64, kDyF32, kSF32>), grid, block, 0, s, a, p.waves, p.teams);
 }
 
 }  // namespace

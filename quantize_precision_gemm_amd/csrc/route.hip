@@ -710,18 +710,6 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a)
     }
 }
 
-// v of this lane and of the one kLanes (16 or 32) away, by the instruction that
-// exchanges the two registers' rows or halves.
-template <int kLanes>
-__device__ __forceinline__ uint32_t sum_of_halves(uint32_t v)
-{
-    typedef uint32_t Pair __attribute__((ext_vector_type(2)));
-    Pair p;
-    if constexpr (kLanes == 16) p = __builtin_bit_cast(Pair, __builtin_amdgcn_permlane16_swap(v, v, false, false));
-    else p = __builtin_bit_cast(Pair, __builtin_amdgcn_permlane32_swap(v, v, false, false));
-    return p.x + p.y;
-}
-
 // The places of a chunk's slots.  Each workgroup adds up all chunks' counts
 // (256 chunks of 256 experts are 64 KB, in the L2), those before its own and
 // all of them, 16 experts a lane in pairs of 16 bits (256 chunks of 64 tokens fit); or
@@ -766,10 +754,16 @@ __global__ __launch_bounds__(kThreads) void k_route_place(RouteArgs a, int chunk
             for (int j = 0; j < 16; ++j) n[j] += (uint32_t)lane_turn<0x128>((int)n[j]);
         if (lanes <= 16)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) n[j] = sum_of_halves<16>(n[j]);
+            for (int j = 0; j < 16; ++j) {
+                const uint2 both = both_of<16>(n[j]);
+                n[j] = both.x + both.y;
+            }
         if (lanes <= 32)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) n[j] = sum_of_halves<32>(n[j]);
+            for (int j = 0; j < 16; ++j) {
+                const uint2 both = both_of<32>(n[j]);
+                n[j] = both.x + both.y;
+            }
         if ((tid & 63) < lanes) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) part[wave_index()][at][j] = n[j];

@@ -69,6 +69,54 @@ __device__ __forceinline__ float wave_top(float v)
     });
 }
 
+// The register pair that exchanging v's rows of 16 lanes (kLanes 16) or its halves
+// (32) with itself gives: v of this lane and v of the one kLanes away.
+template <int kLanes>
+__device__ __forceinline__ uint2 both_of(uint32_t v)
+{
+    typedef uint32_t Pair __attribute__((ext_vector_type(2)));
+    Pair p;
+    if constexpr (kLanes == 16) p = __builtin_bit_cast(Pair, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+    else p = __builtin_bit_cast(Pair, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+    return make_uint2(p.x, p.y);
+}
+
+template <int kLanes>
+__device__ __forceinline__ float sum_of_halves(float v)
+{
+    const uint2 p = both_of<kLanes>(__float_as_uint(v));
+    return __uint_as_float(p.x) + __uint_as_float(p.y);
+}
+
+// Sums (and the largest of non-negative values, NaN the largest) over groups of
+// kLanes neighbours (16, 32 or 64), the same in each lane of a group.
+template <int kLanes>
+__device__ __forceinline__ float group_sum(float v)
+{
+    if constexpr (kLanes == 64) return wave_sum(v);
+    v += __int_as_float(lane_turn<0x128>(__float_as_int(v)));
+    v += __int_as_float(lane_turn<0x124>(__float_as_int(v)));
+    v += __int_as_float(lane_turn<0x122>(__float_as_int(v)));
+    v += __int_as_float(lane_turn<0x121>(__float_as_int(v)));
+    return kLanes == 32 ? sum_of_halves<16>(v) : v;
+}
+
+template <int kLanes>
+__device__ __forceinline__ float group_top(float v)
+{
+    if constexpr (kLanes == 64) return wave_top(v);
+    uint32_t t = __float_as_uint(v);
+    t = max(t, (uint32_t)lane_turn<0x128>((int)t));
+    t = max(t, (uint32_t)lane_turn<0x124>((int)t));
+    t = max(t, (uint32_t)lane_turn<0x122>((int)t));
+    t = max(t, (uint32_t)lane_turn<0x121>((int)t));
+    if constexpr (kLanes == 32) {
+        const uint2 p = both_of<16>(t);
+        t = max(p.x, p.y);
+    }
+    return __uint_as_float(t);
+}
+
 // 8 neighbouring elements as fp32.
 struct Piece {
     float v[8];

@@ -40,7 +40,7 @@ def units(cols):
     return (cols / 64 + 16) / 2 + 6
 
 
-CASES = [(1, 16), (3, 64), (5, 80), (600, 512), (9, 528), (2, 1024), (700, 2048), (4, 2048), (33, 2064), (1, 5120), (65, 5120), (3, 8192),
+CASES = [(1, 16), (3, 64), (5, 80), (1000, 128), (37, 112), (9, 144), (301, 256), (17, 272), (600, 512), (9, 528), (2, 1024), (700, 2048), (4, 2048), (33, 2064), (1, 5120), (65, 5120), (3, 8192),
          (5, 8208), (2, 16384), (2, 20000)]
 TYPES = [(BF, BF, BF, True), (F32, BF, F32, True), (BF, F32, F32, True), (F32, F32, BF, True), (BF, BF, F32, False), (F32, BF, None, False)]
 
@@ -126,7 +126,7 @@ def test_rows_of_zeros_tiny_and_not_finite(cols):
     assert (q.nvfp4_rmsnorm(x[:1], None, 1e-300)[0] == 0).all()  # (an eps below fp32's range is not 0)
 
 
-BACK = [(1, 16), (3, 64), (5, 72), (600, 512), (9, 520), (700, 1024), (4, 1032), (300, 2048), (1, 5120), (65, 5120), (700, 2568), (3, 8200),
+BACK = [(1, 16), (3, 64), (5, 72), (1000, 128), (130, 120), (9, 136), (301, 256), (2100, 192), (17, 264), (600, 512), (9, 520), (700, 1024), (4, 1032), (300, 2048), (1, 5120), (65, 5120), (700, 2568), (3, 8200),
         (520, 128), (2, 16384), (5000, 256)]
 
 

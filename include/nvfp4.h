@@ -744,7 +744,7 @@ int nvfp4_route_backward(const void* logits, int32_t l_dtype, int64_t ld, int64_
  *   x, out    bf16, T and R rows of cols, a multiple of 8 (up to 2^24), 16-byte aligned,
  *             pitches multiples of 8.  rows: T x k int32 (k 1 to 64), as nvfp4_route writes them; a place
  *             outside [0, R) is skipped, and rows that no slot names are left
- *             as they are.  A place named twice gets either token.
+ *             as they are.  A place named twice gets either token's columns, column by column.
  * Its gradient is nvfp4_combine without weights.
  */
 int nvfp4_dispatch(const void* x, int64_t ld_x, const int32_t* rows, int64_t T, int64_t k, int64_t cols, int64_t R,
@@ -782,6 +782,8 @@ int nvfp4_combine_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, cons
  *             may be NULL, and may be residual or x itself (same type and pitch); residual may be NULL.
  *   weight    fp32 or bf16, cols values, or NULL: 1.
  *   cols      a multiple of 8 (with codes: 16); eps finite, >= 0 (with 0 a row of zeros gives NaN).
+ *             The squares are summed in fp32: a row with values beyond 2^56, where they
+ *             may overflow, or with eps 0 below 2^-60, where they vanish, is not normalised.
  *   Bases 16-byte aligned; pitches multiples of 8 (bf16), 4 (fp32), 16 (codes).
  */
 int nvfp4_rmsnorm(const void* x, int32_t x_dtype, int64_t ld_x, const void* residual, int64_t ld_r, int32_t s_dtype,

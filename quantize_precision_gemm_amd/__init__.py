@@ -1095,10 +1095,10 @@ _ROW_DTYPES = (torch.bfloat16, torch.float32)
 
 def _check_matrix(t, what, index, shape=None, dtypes=_ROW_DTYPES):
     """A 2-D device tensor with a contiguous last dimension: its address, row
-    pitch and dtype code (index None: any device)."""
+    pitch and dtype code (index None: on the current device, where the work is launched)."""
     if isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in dtypes:
         at = t.get_device()  # (of a CPU tensor: -1)
-        if at == index or (index is None and at >= 0):
+        if at == index or (index is None and at >= 0 and at == torch._C._cuda_getDevice()):
             rows, cols = t.shape
             if shape is None or shape == (rows, cols):
                 pitch, step = t.stride()
@@ -1111,7 +1111,9 @@ def _check_matrix(t, what, index, shape=None, dtypes=_ROW_DTYPES):
         raise TypeError(f"{what}: expected a 2-D CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if index is not None and t.get_device() != index:
+    if index is None:
+        index = torch.cuda.current_device()
+    if t.get_device() != index:
         raise ValueError(f"{what}: on {t.device}, expected cuda:{index}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")

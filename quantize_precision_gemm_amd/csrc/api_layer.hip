@@ -261,15 +261,16 @@ int nvfp4_rmsnorm(const void* x, int32_t x_dtype, int64_t ld_x, const void* resi
 {
     int st = check_norm(rows, cols, x_dtype, s_dtype, w_dtype, eps, weight);
     if (st != NVFP4_OK) return st;
-    if (codes && cols % 16) return NVFP4_ERR_SHAPE;
-    if (!codes != !scales || (rows > 0 && cols > 0 && (!x || (!y && !codes)))) return NVFP4_ERR_NULL;
+    const bool some = rows > 0 && cols > 0, int8 = scales != nullptr;  // (rows of no columns have scales of 0)
+    if (int8 && cols % 16) return NVFP4_ERR_SHAPE;
+    if ((codes && !int8) || (some && (!x || (int8 ? !codes : !y)))) return NVFP4_ERR_NULL;
     st = check_rows(x, ld_x, cols, x_dtype);
     if (st == NVFP4_OK && residual) st = check_rows(residual, ld_r, cols, s_dtype);
     if (st == NVFP4_OK && h) st = check_rows(h, ld_h, cols, s_dtype);
     if (st == NVFP4_OK && y) st = check_rows(y, ld_y, cols, NVFP4_OUT_BF16);
     if (st != NVFP4_OK) return st;
-    if (codes && ld_codes < cols) return NVFP4_ERR_SHAPE;
-    if (codes && (!aligned(codes, 16) || ld_codes % 16 || !aligned(scales, 4))) return NVFP4_ERR_ALIGN;
+    if (int8 && ld_codes < cols) return NVFP4_ERR_SHAPE;
+    if (int8 && (!aligned(codes, 16) || ld_codes % 16 || !aligned(scales, 4))) return NVFP4_ERR_ALIGN;
     nvfp4::NormArgs a{};
     a.rows = rows;
     a.cols = cols;

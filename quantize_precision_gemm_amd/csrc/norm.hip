@@ -329,7 +329,7 @@ void launch_norm_of(const NormArgs& a, hipStream_t s)
     const int64_t waves = std::min<int64_t>(16, (a.cols / 8 + 64 * kHeld - 1) / (64 * kHeld));
     const int64_t blocks = kLanes ? (a.rows + 256 / (kLanes ? kLanes : 1) - 1) / (256 / (kLanes ? kLanes : 1)) : a.rows;
     const dim3 grid((uint32_t)std::min(blocks, kMostBlocks)), block((uint32_t)(kLanes ? 256 : 64 * waves));
-    if (a.codes) hipLaunchKernelGGL((k_norm<kLanes, true>), grid, block, 0, s, a);
+    if (a.scales) hipLaunchKernelGGL((k_norm<kLanes, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_norm<kLanes, false>), grid, block, 0, s, a);
 }
 

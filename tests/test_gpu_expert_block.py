@@ -280,3 +280,17 @@ def test_the_example_runs():
     ref = reference(block)
     for name in OUTPUTS:
         assert distance(getattr(block, name), ref[name]) <= FAR, name
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Work is launched on the current device: tensors that live elsewhere are refused before."""
+    x, rows = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(4, 2, dtype=torch.int32, device=DEV)
+    w, ones = torch.zeros(64, 64, dtype=torch.bfloat16, device=DEV), torch.ones(4, 2, device=DEV)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: q.nvfp4_route(x, 2), lambda: q.nvfp4_route_backward(x, rows, ones), lambda: q.nvfp4_dispatch(x, rows),
+                 lambda: q.nvfp4_combine(x, rows), lambda: q.nvfp4_combine_backward(x, x, rows, ones), lambda: q.nvfp4_rmsnorm(x),
+                 lambda: q.nvfp4_rmsnorm_i8(x), lambda: q.nvfp4_rmsnorm_backward(x, x), lambda: q.nvfp4_bf16_linear(x, w),
+                 lambda: q.nvfp4_bf16_linear_backward(x, x, q.ACT_SILU)):
+        with pytest.raises(ValueError, match="expected cuda:1"):
+            call()

@@ -189,6 +189,9 @@ def test_empty_and_refusals():
     assert q.nvfp4_rmsnorm(none, w)[0].shape == (0, 64) and q.nvfp4_rmsnorm_i8(none, w)[0].codes.shape == (0, 64)
     dx, dw = q.nvfp4_rmsnorm_backward(none, none, w)
     assert dx.shape == (0, 64) and (dw == 0).all() and dw.shape == (64,)
+    thin = torch.empty(3, 0, dtype=BF, device=DEV)
+    answer = q.nvfp4_rmsnorm_i8(thin)[0]
+    assert q.nvfp4_rmsnorm(thin)[0].shape == (3, 0) and answer.codes.shape == (3, 0) and (answer.scales == 0).all()
     x = randn(1, 4, 64).bfloat16()
     with pytest.raises(TypeError):
         q.nvfp4_rmsnorm(x.half())

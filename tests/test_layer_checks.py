@@ -131,7 +131,7 @@ NORMB = dict(dy=FAKE, dd=0, ldd=64, h=FAKE, ldh=64, dh=FAKE, ldg=64, sd=0, w=FAK
     ({"cols": 16392, "ldd": 1 << 15, "ldh": 1 << 15, "ldg": 1 << 15, "ldx": 1 << 15}, -2), ({"wb": -1}, -2),
     ({"dy": None}, -1), ({"h": None}, -1), ({"dx": None}, -1), ({"dy": FAKE + 8}, -3), ({"h": FAKE + 8}, -3), ({"dh": FAKE + 8}, -3),
     ({"dx": FAKE + 8}, -3), ({"dw": FAKE + 4}, -3), ({"ws": FAKE + 8}, -3), ({"ldd": 56}, -2), ({"ldh": 56}, -2), ({"ldg": 56}, -2),
-    ({"ldx": 56}, -2), ({"ldx": 60, "cols": 56}, -3), ({"rows": 100, "ws": None}, -7), ({"rows": 100, "wb": 64}, -7),
+    ({"ldx": 56}, -2), ({"ldx": 60, "cols": 56}, -3), ({"rows": 1000, "ws": None}, -7), ({"rows": 1000, "wb": 64}, -7),
 ])
 def test_rmsnorm_backward_validation(lib, change, status):
     d = dict(NORMB, **change)
@@ -180,7 +180,7 @@ def test_linear_backward_validation(lib, change, status):
 
 
 @pytest.mark.parametrize("query,good,bad", [
-    ("nvfp4_rmsnorm_backward_workspace", (100, 64), [(-1, 64), (5, 60), (5, 16392), (BIG, 64)]),
+    ("nvfp4_rmsnorm_backward_workspace", (1000, 64), [(-1, 64), (5, 60), (5, 16392), (BIG, 64)]),
     ("nvfp4_bf16_linear_backward_workspace", (4, 10, 32), [(-1, 10, 32), (65536, 10, 32), (4, -1, 32), (4, 10, 36)]),
 ])
 def test_workspace_queries(lib, query, good, bad):

@@ -838,7 +838,7 @@ int nvfp4_bf16_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
  *   dbias     or NULL (then pre is needed).  N a multiple of 8 up to 2^24, E below
  *             65536, E N below 2^30.
  *   workspace with dbias: nvfp4_bf16_linear_backward_workspace bytes, 16-byte
- *             aligned (none for up to 16 rows without ends); calls that share it must not overlap.
+ *             aligned (none for up to 4 rows without ends); calls that share it must not overlap.
  *   Bases 16-byte aligned; pitches multiples of 8 (bf16) or 4 (fp32).
  * (residual's gradient is dy.)
  */

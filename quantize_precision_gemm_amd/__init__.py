@@ -1578,7 +1578,7 @@ def nvfp4_bf16_linear_backward(dy, pre, activation=ACT_NONE, ends=None, with_bia
             dbias_ptr = dbias.data_ptr()
         else:
             dbias_ptr = _check_dense(dbias, "dbias", index, torch.float32, shape)
-        if ends is not None or T > 16:  # (16 dense rows need none)
+        if ends is not None or T > 4:  # (4 dense rows need none)
             ws, ws_ptr, ws_bytes = _workspace(workspace, nvfp4_bf16_linear_backward_workspace(E, T, N), device, stream)
     elif pre is None:
         return dy, None

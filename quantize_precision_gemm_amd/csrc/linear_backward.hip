@@ -18,14 +18,14 @@ namespace nvfp4 {
 
 namespace {
 
-// Rows of a run: 4096 waves where there are as many rows, no run shorter than
-// 8 rows (its sums are 4 bytes a column, a row moves 6) nor more than 4096 runs.
-// 16 rows are one run: without experts its sums are dbias (a second launch costs 4 us).
+// Rows of a run: 4096 waves where there are as many rows (of 8192 rows of 5120: 52 us,
+// 2048 waves 59, 8192 53), and no run shorter than the 4 rows that a wave has in
+// flight (64 rows of 5120: 9 us, 8 a run 14, 16 a run 23; each run costs 4 bytes a
+// column, its rows 24).  4 rows are one run: without experts its sums are dbias.
 int64_t run_rows(int64_t T, int64_t N)
 {
-    if (T <= 16) return 16;
-    const int64_t units = (N + 511) / 512, runs = std::max<int64_t>(1, std::min<int64_t>(4096, 4096 / std::max<int64_t>(units, 1)));
-    return std::max<int64_t>(8, (T + runs - 1) / runs);
+    const int64_t units = std::max<int64_t>(1, (N + 511) / 512), runs = std::max<int64_t>(1, 4096 / units);
+    return std::max<int64_t>(4, (T + runs - 1) / runs);
 }
 
 int64_t run_count(int64_t T, int64_t N) { return (T + run_rows(T, N) - 1) / run_rows(T, N); }
@@ -94,10 +94,11 @@ __global__ __launch_bounds__(256) void k_linear_backward(LinearBackArgs a, int64
     }
 }
 
-// dbias of one expert: its lines in order, 64 columns a workgroup, 16 runs of the lines.
-__global__ __launch_bounds__(256) void k_bias_sums(LinearBackArgs a, int64_t each)
+// dbias of one expert: its lines in order, 64 columns a workgroup, 64 runs of the
+// lines.  (65536 rows of 512, 4096 lines for 8 workgroups: 54 us in all, with 16 runs 61.)
+__global__ __launch_bounds__(1024) void k_bias_sums(LinearBackArgs a, int64_t each)
 {
-    __shared__ float4 part[16][16];
+    __shared__ float4 part[64][16];
     const int q = threadIdx.x & 15, s = threadIdx.x >> 4;
     const int64_t e = blockIdx.y, c = 64 * (int64_t)blockIdx.x + 4 * q;
     int64_t begin = 0, end = a.T;
@@ -112,20 +113,26 @@ __global__ __launch_bounds__(256) void k_bias_sums(LinearBackArgs a, int64_t eac
     if (end > begin && c < a.N) {
         const int64_t first = begin / each, count = (end - 1) / each - first + 1;
 #pragma unroll 4
-        for (int64_t i = first + count * s / 16, to = first + count * (s + 1) / 16; i < to; ++i) {
+        for (int64_t i = first + count * s / 64, to = first + count * (s + 1) / 64; i < to; ++i) {
             const float4 v = *reinterpret_cast<const float4*>(a.parts + (i + e) * a.N + c);
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
     }
     part[s][q] = sum;
-    __syncthreads();
-    if (s != 0 || c >= a.N) return;
+    // the runs' sums: 8 at a time, and those
+    const auto join = [&](int step) {
+        __syncthreads();
+        if (s % (8 * step)) return;
 #pragma unroll
-    for (int j = 1; j < 16; ++j) {
-        const float4 v = part[j][q];
-        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-    }
-    *reinterpret_cast<float4*>(a.dbias + e * a.N + c) = sum;
+        for (int j = 1; j < 8; ++j) {
+            const float4 v = part[s + j * step][q];
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+    };
+    join(1);
+    if (s % 8 == 0) part[s][q] = sum;
+    join(8);
+    if (s == 0 && c < a.N) *reinterpret_cast<float4*>(a.dbias + e * a.N + c) = sum;
 }
 
 int64_t linear_backward_workspace(int64_t E, int64_t T, int64_t N, int cus)
@@ -148,7 +155,7 @@ void launch_linear_backward(const LinearBackArgs& args, hipStream_t s)
         else hipLaunchKernelGGL(k_linear_backward<false>, grid, dim3(256), 0, s, a, each);
     }
     if (a.dbias && a.E > 0 && !whole)
-        hipLaunchKernelGGL(k_bias_sums, dim3((uint32_t)((a.N + 63) / 64), (uint32_t)a.E), dim3(256), 0, s, a, each);
+        hipLaunchKernelGGL(k_bias_sums, dim3((uint32_t)((a.N + 63) / 64), (uint32_t)a.E), dim3(1024), 0, s, a, each);
 }
 
 }  // namespace nvfp4

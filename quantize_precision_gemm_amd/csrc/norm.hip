@@ -64,14 +64,15 @@ __device__ __forceinline__ uint2 codes_of(const Piece& y, float lift, float fact
 
 }  // namespace
 
-// kLanes 16, 32 or 64: so many lanes a row (of up to 128, 256, 1024 columns), 256 /
-// kLanes rows a workgroup.  0: a workgroup a row, as many waves as its columns fill (16 at most).
-// (65536 x 128, a head's norm: 16 lanes a row 13 us, a wave 30.)
+// kLanes 16 or 32: so many lanes a row (of up to 128 or 256 columns), 256 / kLanes
+// rows a workgroup.  0: a workgroup a row, as many waves as its columns fill (16 at most).
+// (65536 x 128, a head's norm: 16 lanes a row 13 us, 32 14.6, a wave 28; 32768 x 256:
+// 32 lanes 13, a wave 16; 16384 x 512: a wave a workgroup 12.5, four in one 12.7.)
 template <int kLanes, bool kI8>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void k_norm(NormArgs a)
 {
     constexpr bool kSolo = kLanes > 0;
-    constexpr int kHeld = kLanes == 16 || kLanes == 32 ? 1 : nvfp4::kHeld, kRows = kSolo ? 256 / kLanes : 1;
+    constexpr int kHeld = kSolo ? 1 : nvfp4::kHeld, kRows = kSolo ? 256 / kLanes : 1;
     __shared__ float part[2][16];
     const int lanes = kSolo ? kLanes : blockDim.x, lane = kSolo ? threadIdx.x & (kLanes - 1) : threadIdx.x;
     const int wave = wave_index(), waves = lanes / 64;
@@ -179,21 +180,23 @@ BackPlan back_plan(int64_t rows, int64_t cols, int cus)
     const int64_t pieces = (cols + 7) / 8;
     const int held = pieces <= 64 ? 1 : 2, lanes = pieces <= 16 ? 16 : pieces <= 32 ? 32 : 64;
     const int waves = (int)std::max<int64_t>(1, (pieces + 64 * held - 1) / (64 * held)), teams = 16 / waves * (64 / lanes);
-    // two rows a team: one workgroup, whose sums are dweight (a second launch costs 4 us)
+    // up to two rows a team: one workgroup, whose sums are dweight (6 x 5120: 7.2 us, with a
+    // second launch 7.9; 9 x 5120, three rows a team: 9.0 and 8.0)
+    // (two or more otherwise: on a host without a device the answer is one for two units)
     const int64_t turns = (rows + teams - 1) / teams;
-    return BackPlan{lanes, held, waves, teams, turns <= 2 ? std::min<int64_t>(turns, 1) : std::min(turns, (held == 1 ? 2 : 1) * (int64_t)cus)};
+    return BackPlan{lanes, held, waves, teams, turns <= 2 ? std::min<int64_t>(turns, 1) : std::min<int64_t>(turns, std::max(cus, 2))};
 }
 
 }  // namespace
 
-// A workgroup takes `teams` rows at a time, each by `waves` waves, and keeps
-// its columns' sums of dy h rstd in registers; the teams' sums are added in LDS,
-// in order, and the workgroups' by k_column_sums.  Many rows at a time keep loads in
-// flight while others are added up; the registers of two pieces a lane leave room
-// for one workgroup of 16 waves on a compute unit, those of one piece for two.
-// 8192 x 5120, us: 3 rows at a time 70.2 (with the sums' kernel), one 79, one with the next's
-// loads in flight 80 to 85.
-// kLanes 16 or 32: so many lanes a row.
+// A workgroup takes `teams` rows at a time, each by `waves` waves (kLanes 16 or
+// 32: by so many lanes, 64 or 32 rows), and keeps its columns' sums of dy h rstd in
+// registers; the teams' sums are added in LDS, in order, and the workgroups' by
+// k_column_sums.  Many rows at a time keep loads in flight while others are added
+// up; more than one workgroup of 16 waves on a compute unit adds more sums than it
+// hides (16384 x 512: one 16.7 us, two 20.5).  8192 x 5120, us: 3 rows at a time 67
+// (with the sums' kernel), one 79, one with the next's loads in flight 80 to 85.
+// One piece a lane up to 512 columns (1000 x 512: 8.5, two a lane and half the teams 8.9).
 template <int kBackHeld, int kLanes, bool kDyF32, bool kSF32>
 __global__ __launch_bounds__(1024) void k_norm_backward(NormArgs a, int waves, int teams)
 {
@@ -327,7 +330,7 @@ template <int kLanes>
 void launch_norm_of(const NormArgs& a, hipStream_t s)
 {
     const int64_t waves = std::min<int64_t>(16, (a.cols / 8 + 64 * kHeld - 1) / (64 * kHeld));
-    const int64_t blocks = kLanes ? (a.rows + 256 / (kLanes ? kLanes : 1) - 1) / (256 / (kLanes ? kLanes : 1)) : a.rows;
+    const int64_t each = kLanes ? 256 / std::max(kLanes, 1) : 1, blocks = (a.rows + each - 1) / each;
     const dim3 grid((uint32_t)std::min(blocks, kMostBlocks)), block((uint32_t)(kLanes ? 256 : 64 * waves));
     if (a.scales) hipLaunchKernelGGL((k_norm<kLanes, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_norm<kLanes, false>), grid, block, 0, s, a);
@@ -340,7 +343,6 @@ void launch_norm(const NormArgs& a, hipStream_t s)
     if (a.rows == 0) return;
     if (a.cols <= 128) launch_norm_of<16>(a, s);
     else if (a.cols <= 256) launch_norm_of<32>(a, s);
-    else if (a.cols <= 512 * kHeld) launch_norm_of<64>(a, s);
     else launch_norm_of<0>(a, s);
 }
 

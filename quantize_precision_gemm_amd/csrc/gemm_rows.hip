@@ -828,6 +828,9 @@ __device__ __forceinline__ void store_wave(uint8_t* stage, int64_t row0, const i
 // no bias, and every activation of 0 is 0).  Without a residual a tile's sums go through
 // it in the accumulators' layout and are stored as other products are; a
 // residual is added by the lane that stores, 4 neighbouring columns at a time.
+// 8192 rows of 8 experts, 2560 -> 5120 (the product alone 201 to 204 us): bias and squared
+// ReLU 200 to 206, SiLU 203 to 211, with the sums before it, 84 MB more, 214 to 224,
+// GELU, sums and residual 246.
 template <bool kF32>
 struct Finish {
     static constexpr bool kWhole = true;

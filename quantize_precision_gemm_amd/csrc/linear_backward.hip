@@ -2,7 +2,8 @@
 // forward product: dpre = dy act'(pre), dbias = sum of dpre over the rows (of
 // each expert).
 //
-// Bound by the bytes of dy, pre and dpre.  A wave takes 512 columns of a run of
+// Bound by the bytes of dy, pre and dpre (8192 x 5120, 252 MB: 47 to 48 us, squared ReLU;
+// SiLU and GELU, 20 to 30 instructions an element, 52 and 56 with the sums).  A wave takes 512 columns of a run of
 // rows and keeps their sums in registers; where the run passes from one expert
 // to the next it writes them down.  Run c's sums for expert e go to line c + e
 // of the workspace: going along the rows, c or e grows from one to the next,

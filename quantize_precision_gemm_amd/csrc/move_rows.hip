@@ -9,7 +9,9 @@
 // All three go token by token: a token's k places are scalar loads, its own
 // row moves once, and the experts' rows are whole row pieces wherever they
 // lie.  Sums run over j in order, so no atomic and no order of workgroups
-// shows in a result.  Bound by the bytes of the experts' rows.
+// shows in a result.  Bound by the bytes of the experts' rows: 8192 tokens of 5120
+// columns, 4 rows each, take 82 us to dispatch (420 MB, 5.1 TB/s), 98 to combine
+// with a residual (503 MB), 155 backward (755 MB, 4.9 TB/s); a copy reaches 5.1 TB/s.
 #include <algorithm>
 
 #include "internal.hpp"
@@ -111,8 +113,10 @@ __global__ __launch_bounds__(256) void k_combine(MoveArgs a)
 
 // A token's waves hold two pieces of dy a lane while its rows pass by, four of
 // them in flight; each wave adds its dot products up by lane moves, and the
-// waves' are added in order.  kSolo: a wave a token, four a workgroup;
-// otherwise a workgroup a token, as many waves as its columns fill.
+// waves' are added in order.  kSolo: up to 1024 columns, a wave a token, four a
+// workgroup; otherwise a workgroup a token, as many waves as its columns fill.  (16384
+// tokens of 2 rows of 1024: 27.1 us, a wave a workgroup 27.4; 16384 of 4 of 768: 35.2, 36.0.
+// 4001 of 6 of 2568: 58.7; one piece 65, eight rows in flight 61.)
 template <bool kDyF32, bool kOF32, bool kSolo>
 __global__ __launch_bounds__(kSolo ? 256 : 1024) void k_combine_backward(MoveArgs a)
 {

@@ -9,7 +9,9 @@
 // keeps that as its scale, and its codes are 0.
 //
 // Bound by the bytes of x, r, h and y (backward dy, h, dh, dx): a row is read
-// once and stays in registers between its sum and its outputs.
+// once and stays in registers between its sum and its outputs.  8192 x 5120 in bf16
+// (336 MB): forward 59 to 62 us, int8 58 to 60, backward 65 and 4 for dw's second
+// launch; a copy of as many bytes 65.6.
 #include <algorithm>
 
 #include "internal.hpp"
@@ -300,7 +302,7 @@ __global__ __launch_bounds__(1024) void k_norm_backward(NormArgs a, int waves, i
 }
 
 // Column sums of `parts` (groups x cols) in the order of the groups: 32
-// columns a workgroup, 32 runs of the groups.
+// columns a workgroup, 32 runs of the groups.  (256 x 5120: 4.8 us, the launch.)
 __global__ __launch_bounds__(256) void k_column_sums(const float* __restrict__ parts, int64_t groups, int64_t cols,
                                                      float* __restrict__ out)
 {

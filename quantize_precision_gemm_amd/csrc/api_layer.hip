@@ -379,7 +379,7 @@ int nvfp4_bf16_linear_backward_workspace(int64_t E, int64_t T, int64_t N, int64_
 {
     if (!bytes) return NVFP4_ERR_NULL;
     if (!fits_linear_backward(E, T, N)) return NVFP4_ERR_SHAPE;
-    *bytes = nvfp4::linear_backward_workspace(E, T, N, std::max(device_cus(), 1));
+    *bytes = nvfp4::linear_backward_workspace(E, T, N);
     return NVFP4_OK;
 }
 
@@ -397,13 +397,12 @@ int nvfp4_bf16_linear_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, 
     if (st == NVFP4_OK && pre) st = check_rows(dpre, ld_dpre, N, NVFP4_OUT_BF16);
     if (st != NVFP4_OK) return st;
     if (!aligned(ends, 4) || !aligned(dbias, 16) || !aligned(workspace, 16)) return NVFP4_ERR_ALIGN;
-    const int cus = std::max(device_cus(), 1);
     const int64_t need =
-        dbias && !nvfp4::linear_backward_one_run(ends, T, N) ? nvfp4::linear_backward_workspace(E, T, N, cus) : 0;
+        dbias && !nvfp4::linear_backward_one_run(ends, T, N) ? nvfp4::linear_backward_workspace(E, T, N) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
     const nvfp4::LinearBackArgs a{dy, ld_dy, dy_dtype == NVFP4_OUT_FP32, static_cast<const uint16_t*>(pre), ld_pre,
                                   static_cast<uint16_t*>(dpre), ld_dpre, ends, E, T, N, act, dbias,
-                                  static_cast<float*>(workspace), cus};
+                                  static_cast<float*>(workspace)};
     nvfp4::launch_linear_backward(a, static_cast<hipStream_t>(stream));
     return launch_status();
 }

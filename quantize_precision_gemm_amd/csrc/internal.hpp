@@ -212,9 +212,8 @@ struct LinearBackArgs {
     int act;
     float* dbias;         // E x N, or null
     float* parts;         // workspace of linear_backward_workspace bytes (dbias)
-    int cus;
 };
-int64_t linear_backward_workspace(int64_t E, int64_t T, int64_t N, int cus);
+int64_t linear_backward_workspace(int64_t E, int64_t T, int64_t N);
 bool linear_backward_one_run(const int32_t* ends, int64_t T, int64_t N);  // (it needs no workspace)
 void launch_linear_backward(const LinearBackArgs& a, hipStream_t s);
 void launch_grouped(int pass, const GroupedArgs& g, int64_t ws_bytes, bool out_fp32, hipStream_t s);

@@ -95,11 +95,14 @@ __global__ __launch_bounds__(256) void k_linear_backward(LinearBackArgs a, int64
     }
 }
 
-// dbias of one expert: its lines in order, 64 columns a workgroup, 64 runs of the
-// lines.  (65536 rows of 512, 4096 lines for 8 workgroups: 54 us in all, with 16 runs 61.)
-__global__ __launch_bounds__(1024) void k_bias_sums(LinearBackArgs a, int64_t each)
+// dbias of one expert: its lines in order, 64 columns a workgroup, kRuns runs of
+// the lines: 64 from 256 lines an expert on, else 16.  (65536 rows of 512, 4096 lines for 8
+// workgroups: 54 us in all, with 16 runs 61; 777 of 5120, 195 lines: 12.9 and 12.5; 8192
+// of 5120 for 8 experts, 51 lines: 62.9 and 60.7.)
+template <int kRuns>
+__global__ __launch_bounds__(16 * kRuns) void k_bias_sums(LinearBackArgs a, int64_t each)
 {
-    __shared__ float4 part[64][16];
+    __shared__ float4 part[kRuns][16];
     const int q = threadIdx.x & 15, s = threadIdx.x >> 4;
     const int64_t e = blockIdx.y, c = 64 * (int64_t)blockIdx.x + 4 * q;
     int64_t begin = 0, end = a.T;
@@ -114,29 +117,30 @@ __global__ __launch_bounds__(1024) void k_bias_sums(LinearBackArgs a, int64_t ea
     if (end > begin && c < a.N) {
         const int64_t first = begin / each, count = (end - 1) / each - first + 1;
 #pragma unroll 4
-        for (int64_t i = first + count * s / 64, to = first + count * (s + 1) / 64; i < to; ++i) {
+        for (int64_t i = first + count * s / kRuns, to = first + count * (s + 1) / kRuns; i < to; ++i) {
             const float4 v = *reinterpret_cast<const float4*>(a.parts + (i + e) * a.N + c);
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
     }
     part[s][q] = sum;
-    // the runs' sums: 8 at a time, and those
+    // the runs' sums: kJoin at a time, and those
+    constexpr int kJoin = kRuns == 64 ? 8 : 4;
     const auto join = [&](int step) {
         __syncthreads();
-        if (s % (8 * step)) return;
+        if (s % (kJoin * step)) return;
 #pragma unroll
-        for (int j = 1; j < 8; ++j) {
+        for (int j = 1; j < kJoin; ++j) {
             const float4 v = part[s + j * step][q];
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
     };
     join(1);
-    if (s % 8 == 0) part[s][q] = sum;
-    join(8);
+    if (s % kJoin == 0) part[s][q] = sum;
+    join(kJoin);
     if (s == 0 && c < a.N) *reinterpret_cast<float4*>(a.dbias + e * a.N + c) = sum;
 }
 
-int64_t linear_backward_workspace(int64_t E, int64_t T, int64_t N, int cus)
+int64_t linear_backward_workspace(int64_t E, int64_t T, int64_t N)
 {
     return T == 0 || N == 0 || E == 0 ? 0 : (run_count(T, N) + E) * N * (int64_t)sizeof(float);
 }
@@ -155,8 +159,11 @@ void launch_linear_backward(const LinearBackArgs& args, hipStream_t s)
         if (a.dbias) hipLaunchKernelGGL(k_linear_backward<true>, grid, dim3(256), 0, s, a, each);
         else hipLaunchKernelGGL(k_linear_backward<false>, grid, dim3(256), 0, s, a, each);
     }
-    if (a.dbias && a.E > 0 && !whole)
-        hipLaunchKernelGGL(k_bias_sums, dim3((uint32_t)((a.N + 63) / 64), (uint32_t)a.E), dim3(1024), 0, s, a, each);
+    if (a.dbias && a.E > 0 && !whole) {
+        const dim3 grid((uint32_t)((a.N + 63) / 64), (uint32_t)a.E);
+        if (runs >= 256 * a.E) hipLaunchKernelGGL(k_bias_sums<64>, grid, dim3(1024), 0, s, a, each);
+        else hipLaunchKernelGGL(k_bias_sums<16>, grid, dim3(256), 0, s, a, each);
+    }
 }
 
 }  // namespace nvfp4

@@ -205,13 +205,13 @@ __device__ __forceinline__ void store_cols(void* c, int64_t at, int64_t n, int64
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: bound by the weights' bytes.  A workgroup of 4 waves computes
-// 16 kM rows x 16 kN columns (rows x K operands only), each wave a quarter of
+// Few rows: bound by the weights' bytes.  A workgroup of kW waves computes
+// 16 kM rows x 16 kN columns (rows x K operands only), each wave a part of
 // the contraction, 128-byte steps dealt in turn, straight from memory to
 // registers with kU steps in flight; the parts are added in wave order in LDS.
 // One token through 5120 -> 20480 in int8: 18.1 us, 5.8 TB/s of the weight.
 // ---------------------------------------------------------------------------
-template <class Acc, int kM, int kN, int kU, class Out>
+template <class Acc, int kM, int kN, int kU, int kW = 4, class Out>
 __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t kend, int64_t m0, int64_t n0,
                                           f32x4_t* lds, const Out& out)
 {
@@ -233,7 +233,7 @@ __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t 
         for (int u = 0; u < kSteps; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t k = k0 + 512 * u + 64 * h;
+                const int64_t k = k0 + 128 * kW * u + 64 * h;
 #pragma unroll
                 for (int j = 0; j < kN; ++j) b[u][j][h] = piece(pb[j], k);
 #pragma unroll
@@ -250,19 +250,19 @@ __device__ __forceinline__ void thin_tile(const View& A, const View& B, int64_t 
                     for (int j = 0; j < kN; ++j) acc[i][j] = mma(b[u][j][h], a[u][i][h], acc[i][j]);
     };
     int64_t k0 = 128 * wave;
-    for (; k0 + 512 * (kU - 1) + 128 <= kend; k0 += 512 * kU)
+    for (; k0 + 128 * kW * (kU - 1) + 128 <= kend; k0 += 128 * kW * kU)
         steps(k0, std::integral_constant<int, kU>(), std::true_type());
-    for (; k0 < kend; k0 += 512) steps(k0, std::integral_constant<int, 1>(), std::false_type());
+    for (; k0 < kend; k0 += 128 * kW) steps(k0, std::integral_constant<int, 1>(), std::false_type());
     Acc* part = reinterpret_cast<Acc*>(lds);
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll
         for (int j = 0; j < kN; ++j) part[(wave * kM * kN + i * kN + j) * 64 + lane] = acc[i][j];
     __syncthreads();
-    for (int t = wave; t < kM * kN; t += 4) {
+    for (int t = wave; t < kM * kN; t += kW) {
         Acc sum = part[t * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) sum += part[(w * kM * kN + t) * 64 + lane];
+        for (int w = 1; w < kW; ++w) sum += part[(w * kM * kN + t) * 64 + lane];
         const int64_t m = m0 + 16 * (t / kN) + r, n = n0 + 16 * (t % kN) + 4 * g;
         if (m < A.rows && n < B.rows) out(m, n, sum);
     }
@@ -1322,11 +1322,13 @@ __global__ __launch_bounds__(256) void k_grouped_thin(GroupedArgs g)
         });
 }
 
-template <int kM, bool kF32, bool kDense>
-__global__ __launch_bounds__(256) void k_linear_thin(GroupedArgs g, Epilogue ep)
+// kWide: 32 columns and 8 waves a workgroup, which halves what x's rows cost (see wide_pays).
+template <int kM, bool kF32, bool kDense, bool kWide>
+__global__ __launch_bounds__(kWide ? 512 : 256) void k_linear_thin(GroupedArgs g, Epilogue ep)
 {
-    __shared__ f32x4_t lds[4 * kM * kThinN * 64];
-    const int64_t tn = (g.N + 16 * kThinN - 1) / (16 * kThinN);
+    constexpr int kN = kWide ? 2 : kThinN, kW = kWide ? 8 : 4;
+    __shared__ f32x4_t lds[kW * kM * kN * 64];
+    const int64_t tn = (g.N + 16 * kN - 1) / (16 * kN);
     Slice s;
     const auto order = [&](uint32_t total, uint32_t& at) { return xcd_order(blockIdx.x, total, at); };
     if (!find_tile<16 * kM, kDense>(g.ends, g.E, g.T, (int)tn, order, s)) return;
@@ -1335,8 +1337,8 @@ __global__ __launch_bounds__(256) void k_linear_thin(GroupedArgs g, Epilogue ep)
     const View B{reinterpret_cast<const uint8_t*>(g.b + (none ? 0 : s.e) * g.b_expert), 2 * g.ldb, g.N};
     const Finish<kF32> f(ep, s.e, s.begin, none);
     const int tm = (int)((s.end - s.begin + 16 * kM - 1) / (16 * kM));
-    thin_tile<f32x4_t, kM, kThinN, kThinU>(
-        A, B, none ? 0 : 2 * g.K, s.tile % tm * 16 * kM, s.tile / tm * 16 * kThinN, lds,
+    thin_tile<f32x4_t, kM, kN, kThinU, kW>(
+        A, B, none ? 0 : 2 * g.K, s.tile % tm * 16 * kM, s.tile / tm * 16 * kN, lds,
         [&](int64_t m, int64_t n, f32x4_t v) {
             const float y[4] = {v[0], v[1], v[2], v[3]};
             float b[4];
@@ -1457,6 +1459,7 @@ void launch_i8_thin(const int8_t* a, int64_t lda, const float* sa, const int8_t*
 struct Plan {
     Tiles tiles;
     int m, split;
+    double time;  // us, as estimated
 };
 
 template <int kPass>
@@ -1482,8 +1485,9 @@ Plan plan_grouped(const GroupedArgs& g)
                            &time);
     // parts of 4 steps at least, a compute unit for each; 7 us to join them
     const int split = (int)std::min(std::min(32.0, std::floor((double)g.cus / grid)), std::floor(steps / 4));
-    if (split > 1 && 1.5 + 4.0 + 0.47 * std::ceil(steps / split) + 7.0 < time) return Plan{Tiles::kMid, m, split};
-    return Plan{t, m, 1};
+    const double parts = 1.5 + 4.0 + 0.47 * std::ceil(steps / split) + 7.0;
+    if (split > 1 && parts < time) return Plan{Tiles::kMid, m, split, parts};
+    return Plan{t, m, 1, time};
 }
 
 template <int kPass>
@@ -1529,14 +1533,39 @@ void launch_linear_tiles(const GroupedArgs& g, const Epilogue& e, bool out_fp32,
         hipLaunchKernelGGL((k_linear<kBig, false, kDense>), grid, dim3(kBig ? 512 : 256), 0, s, g, e);
 }
 
-template <int kM, bool kDense>
+template <int kM, bool kDense, bool kWide>
 void launch_linear_thin(const GroupedArgs& g, const Epilogue& e, bool out_fp32, hipStream_t s)
 {
-    const dim3 grid((uint32_t)grouped_grid<0>(g, 16 * kM, 16 * kThinN));
+    const dim3 grid((uint32_t)grouped_grid<0>(g, 16 * kM, kWide ? 32 : 16 * kThinN)), block(kWide ? 512 : 256);
     if (out_fp32)
-        hipLaunchKernelGGL((k_linear_thin<kM, true, kDense>), grid, dim3(256), 0, s, g, e);
+        hipLaunchKernelGGL((k_linear_thin<kM, true, kDense, kWide>), grid, block, 0, s, g, e);
     else
-        hipLaunchKernelGGL((k_linear_thin<kM, false, kDense>), grid, dim3(256), 0, s, g, e);
+        hipLaunchKernelGGL((k_linear_thin<kM, false, kDense, kWide>), grid, block, 0, s, g, e);
+}
+
+template <bool kDense, bool kWide>
+void launch_linear_thin_rows(const GroupedArgs& g, const Epilogue& e, int m, bool out_fp32, hipStream_t s)
+{
+    if (m == 1) launch_linear_thin<1, kDense, kWide>(g, e, out_fp32, s);
+    else if (m == 2) launch_linear_thin<2, kDense, kWide>(g, e, out_fp32, s);
+    else launch_linear_thin<4, kDense, kWide>(g, e, out_fp32, s);
+}
+
+// Dense rows, 9 to 64: whether wide thin tiles take less time than `p`.  Each workgroup reads all
+// of x, which then costs as much as w; below half a workgroup a compute unit there are
+// too few loads in flight.  Their time, us, w coming from memory: 3.5, its bytes at 5
+// TB/s and those of x at 5.5; parts of the contraction take 5 more than `p` counts, whose
+// weights are in a cache.  (SiLU and bias; what `p` takes, thin tiles, wide ones:
+// 5120 x 5120, 16 rows 22.2, 22.1, 19.3; 32 23.8, 31, 24.5; 64 26.2, 49, 33;
+// 10240 x 2560, 16 rows 26.6, 18.2, 19.8; 32 27.8, 24.8, 24.5; 64 30.8, 39, 37;
+// 5120 x 2048, 16 rows 10.3, 10.2, 8.6; 32 13.9, 13.9, 10.7; 64 16.9, 20.9, 14.5;
+// 2048 x 8192, 64 workgroups, 16 rows 17.7, 17.7, 25; one row of 10240 x 2560 14.1, 14.1, 16.5.)
+bool wide_pays(const GroupedArgs& g, const Plan& p)
+{
+    const int64_t columns = ceil_div(g.N, (int64_t)32);
+    if (g.T <= 8 || g.T > 64 || 2 * columns < g.cus) return false;
+    const double w = 2.0 * g.N * g.K, x = 2.0 * columns * g.T * g.K;
+    return p.tiles == Tiles::kThin || 3.5 + w / 5.0e6 + x / 5.5e6 < p.time + (p.split > 1 ? 5.0 : 0.0);
 }
 
 template <bool kDense>
@@ -1544,6 +1573,8 @@ void launch_linear_rows(const GroupedArgs& g0, const Epilogue& e, int64_t ws_byt
 {
     GroupedArgs g = g0;
     const Plan p = plan_grouped<0>(g);
+    if constexpr (kDense)
+        if (wide_pays(g, p)) return launch_linear_thin_rows<kDense, true>(g, e, p.m, out_fp32, s);
     const int64_t grid = grouped_grid<0>(g, 128, 128);
     if (p.split > 1 && g.ws && ws_bytes >= plan_bytes<0>(g)) {
         g.split = p.split;
@@ -1555,9 +1586,7 @@ void launch_linear_rows(const GroupedArgs& g0, const Epilogue& e, int64_t ws_byt
             hipLaunchKernelGGL((k_linear_join<false, kDense>), join, dim3(256), 0, s, g, e);
         return;
     }
-    if (p.tiles == Tiles::kThin)
-        return p.m == 1 ? launch_linear_thin<1, kDense>(g, e, out_fp32, s)
-               : p.m == 2 ? launch_linear_thin<2, kDense>(g, e, out_fp32, s) : launch_linear_thin<4, kDense>(g, e, out_fp32, s);
+    if (p.tiles == Tiles::kThin) return launch_linear_thin_rows<kDense, false>(g, e, p.m, out_fp32, s);
     if (p.tiles == Tiles::kBig)
         launch_linear_tiles<true, kDense>(g, e, out_fp32, s);
     else

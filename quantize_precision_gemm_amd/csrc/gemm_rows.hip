@@ -1322,11 +1322,11 @@ __global__ __launch_bounds__(256) void k_grouped_thin(GroupedArgs g)
         });
 }
 
-// kWide: 32 columns and 8 waves a workgroup, which halves what x's rows cost (see wide_pays).
-template <int kM, bool kF32, bool kDense, bool kWide>
-__global__ __launch_bounds__(kWide ? 512 : 256) void k_linear_thin(GroupedArgs g, Epilogue ep)
+// kN > 1: 16 kN columns and 8 waves a workgroup, which read x 1 / kN as often (see wide_columns).
+template <int kM, bool kF32, bool kDense, int kN>
+__global__ __launch_bounds__(kN > 1 ? 512 : 256) void k_linear_thin(GroupedArgs g, Epilogue ep)
 {
-    constexpr int kN = kWide ? 2 : kThinN, kW = kWide ? 8 : 4;
+    constexpr int kW = kN > 1 ? 8 : 4;
     __shared__ f32x4_t lds[kW * kM * kN * 64];
     const int64_t tn = (g.N + 16 * kN - 1) / (16 * kN);
     Slice s;
@@ -1533,39 +1533,41 @@ void launch_linear_tiles(const GroupedArgs& g, const Epilogue& e, bool out_fp32,
         hipLaunchKernelGGL((k_linear<kBig, false, kDense>), grid, dim3(kBig ? 512 : 256), 0, s, g, e);
 }
 
-template <int kM, bool kDense, bool kWide>
+template <int kM, bool kDense, int kN>
 void launch_linear_thin(const GroupedArgs& g, const Epilogue& e, bool out_fp32, hipStream_t s)
 {
-    const dim3 grid((uint32_t)grouped_grid<0>(g, 16 * kM, kWide ? 32 : 16 * kThinN)), block(kWide ? 512 : 256);
+    const dim3 grid((uint32_t)grouped_grid<0>(g, 16 * kM, 16 * kN)), block(kN > 1 ? 512 : 256);
     if (out_fp32)
-        hipLaunchKernelGGL((k_linear_thin<kM, true, kDense, kWide>), grid, block, 0, s, g, e);
+        hipLaunchKernelGGL((k_linear_thin<kM, true, kDense, kN>), grid, block, 0, s, g, e);
     else
-        hipLaunchKernelGGL((k_linear_thin<kM, false, kDense, kWide>), grid, block, 0, s, g, e);
+        hipLaunchKernelGGL((k_linear_thin<kM, false, kDense, kN>), grid, block, 0, s, g, e);
 }
 
-template <bool kDense, bool kWide>
+template <bool kDense, int kN>
 void launch_linear_thin_rows(const GroupedArgs& g, const Epilogue& e, int m, bool out_fp32, hipStream_t s)
 {
-    if (m == 1) launch_linear_thin<1, kDense, kWide>(g, e, out_fp32, s);
-    else if (m == 2) launch_linear_thin<2, kDense, kWide>(g, e, out_fp32, s);
-    else launch_linear_thin<4, kDense, kWide>(g, e, out_fp32, s);
+    if (m == 1) launch_linear_thin<1, kDense, kN>(g, e, out_fp32, s);
+    else if (m == 2) launch_linear_thin<2, kDense, kN>(g, e, out_fp32, s);
+    else launch_linear_thin<4, kDense, kN>(g, e, out_fp32, s);
 }
 
-// Dense rows, 9 to 64: whether wide thin tiles take less time than `p`.  Each workgroup reads all
-// of x, which then costs as much as w; below half a workgroup a compute unit there are
-// too few loads in flight.  Their time, us, w coming from memory: 3.5, its bytes at 5
-// TB/s and those of x at 5.5; parts of the contraction take 5 more than `p` counts, whose
-// weights are in a cache.  (SiLU and bias; what `p` takes, thin tiles, wide ones:
-// 5120 x 5120, 16 rows 22.2, 22.1, 19.3; 32 23.8, 31, 24.5; 64 26.2, 49, 33;
-// 10240 x 2560, 16 rows 26.6, 18.2, 19.8; 32 27.8, 24.8, 24.5; 64 30.8, 39, 37;
-// 5120 x 2048, 16 rows 10.3, 10.2, 8.6; 32 13.9, 13.9, 10.7; 64 16.9, 20.9, 14.5;
-// 2048 x 8192, 64 workgroups, 16 rows 17.7, 17.7, 25; one row of 10240 x 2560 14.1, 14.1, 16.5.)
-bool wide_pays(const GroupedArgs& g, const Plan& p)
+// Dense rows, 9 to 64: columns / 16 of a workgroup's tile, 2 or 4, where such tiles take less
+// time than `p`, else 1.  Each workgroup reads all of x, which costs as much as w in tiles
+// of 16 columns; below half a workgroup a compute unit there are too few loads in
+// flight.  Their time, us, w coming from memory: 3.5, its bytes at 5 TB/s and those of x at 5.5;
+// parts of the contraction take 5 more than `p` counts, whose weights are in a
+// cache.  (SiLU and bias; what `p` takes, tiles of 16 columns, 32, 64:
+// 5120 x 5120, 16 rows 22.2, 22.1, 19.3, 30; 32 23.8, 31, 24.5, 35; 64 26.2, 49, 33, 44;
+// 10240 x 2560, 16 rows 26.6, 18.2, 19.8, 19.0; 32 27.8, 24.8, 24.5, 21.4; 64 30.8, 39, 37, 26.9;
+// 5120 x 2048, 16 rows 10.3, 10.2, 8.6, 12.4; 32 13.9, 13.9, 10.7, 14.6; 64 16.9, 20.9, 14.5, 18.8;
+// 2048 x 8192, 16 rows 17.7, 17.7, 25, 41; one row of 10240 x 2560 14.1, 14.1, 16.5, 17.6.)
+int wide_columns(const GroupedArgs& g, const Plan& p)
 {
-    const int64_t columns = ceil_div(g.N, (int64_t)32);
-    if (g.T <= 8 || g.T > 64 || 2 * columns < g.cus) return false;
-    const double w = 2.0 * g.N * g.K, x = 2.0 * columns * g.T * g.K;
-    return p.tiles == Tiles::kThin || 3.5 + w / 5.0e6 + x / 5.5e6 < p.time + (p.split > 1 ? 5.0 : 0.0);
+    if (g.T <= 8 || g.T > 64 || 2 * ceil_div(g.N, (int64_t)32) < g.cus) return 1;
+    const int n = 2 * ceil_div(g.N, (int64_t)64) < g.cus ? 2 : 4;
+    const double w = 2.0 * g.N * g.K, x = 2.0 * ceil_div(g.N, (int64_t)(16 * n)) * g.T * g.K;
+    const bool pays = p.tiles == Tiles::kThin || 3.5 + w / 5.0e6 + x / 5.5e6 < p.time + (p.split > 1 ? 5.0 : 0.0);
+    return pays ? n : 1;
 }
 
 template <bool kDense>
@@ -1573,8 +1575,11 @@ void launch_linear_rows(const GroupedArgs& g0, const Epilogue& e, int64_t ws_byt
 {
     GroupedArgs g = g0;
     const Plan p = plan_grouped<0>(g);
-    if constexpr (kDense)
-        if (wide_pays(g, p)) return launch_linear_thin_rows<kDense, true>(g, e, p.m, out_fp32, s);
+    if constexpr (kDense) {
+        const int n = wide_columns(g, p);
+        if (n == 4) return launch_linear_thin_rows<kDense, 4>(g, e, p.m, out_fp32, s);
+        if (n == 2) return launch_linear_thin_rows<kDense, 2>(g, e, p.m, out_fp32, s);
+    }
     const int64_t grid = grouped_grid<0>(g, 128, 128);
     if (p.split > 1 && g.ws && ws_bytes >= plan_bytes<0>(g)) {
         g.split = p.split;
@@ -1586,7 +1591,7 @@ void launch_linear_rows(const GroupedArgs& g0, const Epilogue& e, int64_t ws_byt
             hipLaunchKernelGGL((k_linear_join<false, kDense>), join, dim3(256), 0, s, g, e);
         return;
     }
-    if (p.tiles == Tiles::kThin) return launch_linear_thin_rows<kDense, false>(g, e, p.m, out_fp32, s);
+    if (p.tiles == Tiles::kThin) return launch_linear_thin_rows<kDense, kThinN>(g, e, p.m, out_fp32, s);
     if (p.tiles == Tiles::kBig)
         launch_linear_tiles<true, kDense>(g, e, out_fp32, s);
     else

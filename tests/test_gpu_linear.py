@@ -82,7 +82,8 @@ def check(T, N, K, ends, act, bias_dtype, residual, pre, out, more=0, seed=0, **
 
 DENSE = [(1, 8, 8), (1, 2048, 1024), (3, 136, 264), (16, 512, 5120), (37, 1296, 520), (64, 1024, 2048), (100, 72, 4096), (130, 264, 1032),
          (300, 1280, 1288), (777, 1024, 512), (1000, 2056, 776), (2048, 2560, 640),
-         (9, 4104, 264), (16, 5120, 1032), (20, 4120, 2048), (33, 4224, 72), (37, 6152, 1288), (64, 5128, 640)]
+         (9, 4104, 264), (16, 5120, 1032), (20, 4120, 2048), (33, 4224, 72), (37, 6152, 1288), (64, 5128, 640),
+         (16, 8200, 520), (20, 8192, 1032), (64, 10248, 264)]
 
 
 @pytest.mark.parametrize("T,N,K", DENSE)

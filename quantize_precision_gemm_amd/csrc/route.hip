@@ -13,7 +13,8 @@
 // choose differently when two values lie close.  Here every choice is the one
 // that 64-bit arithmetic makes: what is compared is held as whole numbers of a
 // bounded error, and a token for which two values that a decision compares lie
-// within that bound is done again in 64 bits by the whole wave.  Ordinary
+// within that bound is done again in 64 bits by the whole wave, unless they are made of equal
+// logits and biases, as all others within the bound of theirs are.  Ordinary
 // logits have a few such tokens in a thousand; if all are such, 16384 x 256 take 14
 // us (softmax; sigmoid with a bias 43, with groups 57) instead of 11 to 21.
 //
@@ -172,6 +173,7 @@ __device__ __forceinline__ void load_values(const void* p, bool f32, bool vec, i
                 const float4 v = *reinterpret_cast<const float4*>(src + e0 + i);
                 l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
             }
+            asm volatile("");  // (without it both branches may become the other one's single loads)
             return;
         }
 #pragma unroll
@@ -365,7 +367,9 @@ __device__ __forceinline__ uint32_t key_below(const uint32_t (&key)[P], uint32_t
 // a value of 0: never.  Lane j of the row gets the j-th one's index (-1: there
 // is none left), `last` the last one's key.  Returns (in every lane of the
 // row) whether values no further apart than `near` decided, other than those of equal
-// logits (the row's, in LDS) and biases.
+// logits (the row's, in LDS) and biases: among the candidates each with the next one, since
+// values that lie between two near ones are near to both; and where the k-th and the
+// next one are equal, the k-th with all that are left.
 template <int L, int P>
 __device__ __forceinline__ bool pick(const RouteArgs& a, const float* logits, const uint32_t (&key)[P], uint32_t near,
                                      int& mine, uint32_t& last)
@@ -387,6 +391,19 @@ __device__ __forceinline__ bool pick(const RouteArgs& a, const float* logits, co
     if (sub < a.k && next > kMask && (own >> kBits) - (next >> kBits) <= near)  // equal logits and biases make equal values
         close = logits[e] != logits[after] || (a.bias && a.bias[e] != a.bias[after]);
     mine = own > kMask ? e : -1;
+    const bool border = sub == a.k - 1 && !close && next > kMask && (own >> kBits) - (next >> kBits) <= near;
+    if (__ballot(border)) {  // (rare but for rows of few values)
+        const uint32_t edge = (uint32_t)__shfl((int)own, a.k - 1, L);
+        const int at = (int)(kMask - (edge & kMask)), e0 = sub * P;
+        uint32_t left = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            left |= key[i] < last && key[i] > kMask && (edge >> kBits) - (key[i] >> kBits) <= near ? 1u << i : 0u;
+        for (; left && !close; left &= left - 1) {
+            const int i = e0 + __builtin_ctz(left);
+            close |= logits[i] != logits[at] || (a.bias && a.bias[i] != a.bias[at]);
+        }
+    }
     return own_bits<L>(__ballot(close)) != 0;
 }
 

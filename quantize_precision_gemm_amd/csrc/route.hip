@@ -248,8 +248,12 @@ __device__ __forceinline__ float sum_of(const float (&l)[P], float top)
     return over_lanes<L>(s, Add());
 }
 
-// Sum of the two largest values of a group, as far as there are two.
-__device__ __forceinline__ float pair_sum(float one, float two) { return two > -INFINITY ? one + two : one; }
+// Sum of the two largest values of a group, as far as there are two; in fp32 half of it, which does not overflow.
+__device__ __forceinline__ float pair_sum(float one, float two)
+{
+    one *= 0.5f;
+    return two > -INFINITY ? __builtin_fmaf(two, 0.5f, one) : one;
+}
 __device__ __forceinline__ double pair_sum(double one, double two) { return two > -INFINITY ? one + two : one; }
 
 // v among the two largest so far (one >= two): the new second is the middle of the three.
@@ -342,7 +346,8 @@ __device__ __forceinline__ bool drop_groups(const RouteArgs& a, float (&c)[P], f
         }
     }
     __builtin_amdgcn_wave_barrier();  // buf is written again for the next row
-    return least - most <= 6 * error;  // (infinity where nothing is dropped; the sums round, too)
+    // (half a sum is off by as much as a c, and rounds by no more; infinity where nothing is dropped)
+    return least - most <= 4 * error;
 }
 
 // A float as a whole number, truncated, what is below 0 (and NaN) as 0: the instruction's rule.

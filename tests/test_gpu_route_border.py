@@ -1,7 +1,8 @@
 """Routing where values that the fast comparison cannot tell apart lie on both
 sides of the border between the chosen and the others, more than two of them: equal ones
-among the chosen and the next, and a larger one beyond.  Against the definition in 64
-bits, as test_gpu_route.py has it (experts and places equal, weights within its tolerance)."""
+among the chosen and the next, and a larger one beyond.  And groups whose sums
+of two pass fp32's range.  Against the definition in 64 bits, as
+test_gpu_route.py has it (experts and places equal, weights within its tolerance)."""
 import pytest
 import torch
 
@@ -96,3 +97,26 @@ def test_few_values(E, biased, score):
         check(logits, k, score, bias)
         if E % 8 == 0:
             check(logits, min(k, E // 8 * 3), score, bias, 8, 3)
+
+
+@SCORES
+@pytest.mark.parametrize("E,groups", [(16, 8), (32, 8), (60, 6), (64, 8), (128, 8), (256, 8), (320, 8), (512, 16), (1024, 64)])
+def test_groups_whose_sums_overflow(E, groups, score):
+    """A group counts the sum of two: with biases of the type's lowest or largest values it passes fp32."""
+    per = E // groups
+    k = min(16, per + 1)
+    for equal in (False, True):
+        logits = torch.zeros(66, E, device=DEV) if equal else randn(E, 66, E)
+        bias = torch.full((groups, per), LOWEST, device=DEV)
+        bias[3] = 0.0  # all groups but one masked, two kept
+        check(logits, k, score, bias.flatten(), groups, 2)
+        bias[1] = -3e38  # better than the lowest
+        check(logits, k, score, bias.flatten(), groups, 2)
+        check(logits, k, score, bias.flatten(), groups, 3)
+        bias[:] = 0.1
+        bias[2], bias[4] = 3e38, 3.3e38
+        check(logits, min(per, 16), score, bias.flatten(), groups, 1)
+        bias[0, 0], bias[0, 1] = -LOWEST, LOWEST
+        check(logits, k, score, bias.flatten(), groups, 2)
+        bias[5] = -LOWEST
+        check(logits, k, score, bias.flatten(), groups, 3)

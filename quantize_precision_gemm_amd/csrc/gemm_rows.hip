@@ -1565,6 +1565,7 @@ int wide_columns(const GroupedArgs& g, const Plan& p)
 {
     if (g.T <= 8 || g.T > 64 || 2 * ceil_div(g.N, (int64_t)32) < g.cus) return 1;
     const int n = 2 * ceil_div(g.N, (int64_t)64) < g.cus ? 2 : 4;
+    if (grouped_grid<0>(g, 16 * p.m, 16 * n) >= int64_t(1) << 23) return 1;  // (a grid holds fewer than 2^32 threads)
     const double w = 2.0 * g.N * g.K, x = 2.0 * ceil_div(g.N, (int64_t)(16 * n)) * g.T * g.K;
     const bool pays = p.tiles == Tiles::kThin || 3.5 + w / 5.0e6 + x / 5.5e6 < p.time + (p.split > 1 ? 5.0 : 0.0);
     return pays ? n : 1;

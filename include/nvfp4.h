@@ -687,7 +687,8 @@ int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int
 
 /*
  * nvfp4_route -- routing of T tokens to k of E experts each, and the order of
- * the rows by expert that nvfp4_bf16_grouped_gemm takes.
+ * the rows by expert that nvfp4_bf16_grouped_gemm takes.  (From here on: outputs and
+ * workspaces share no memory with each other or with inputs, but where it says that they may.)
  *   s = softmax(l) or 1 / (1 + e^-l) of a token's logits l;  c = s + bias.
  *   groups > groups_kept: groups of E / groups neighbours; a group counts the
  *   sum of its two largest c (of its only one), and the experts outside of the
@@ -703,7 +704,9 @@ int nvfp4_i8_gemm(const int8_t* a, int64_t lda, const float* a_scales, const int
  * infinity has weights NaN.
  *   logits    device fp32 or bf16 (l_dtype), T rows of E, ld apart (any ld >= E;
  *             16-byte aligned rows are read faster).
- *   bias      device float, E values, or NULL; it enters the choice alone.
+ *   bias      device float, E values, or NULL; it enters the choice alone.  Minus infinity
+ *             leaves an expert out; a large finite value costs time for all tokens (the more the larger:
+ *             choices that fp32 cannot make are made again in 64 bits).
  *   T         0 to 2^27; E 1 to 1024; k 1 to min(16, E / groups * groups_kept);
  *             T k below 2^31; groups 1 to 64, a divisor of E.
  *   experts, weights  device, T x k.
@@ -782,8 +785,9 @@ int nvfp4_combine_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, cons
  *             may be NULL, and may be residual or x itself (same type and pitch); residual may be NULL.
  *   weight    fp32 or bf16, cols values, or NULL: 1.
  *   cols      a multiple of 8 (with codes: 16); eps finite, >= 0 (with 0 a row of zeros gives NaN).
- *             The squares are summed in fp32: a row with values beyond 2^56, where they
- *             may overflow, or with eps 0 below 2^-60, where they vanish, is not normalised.
+ *             The squares are summed in fp32: a row with values beyond 2^56 (of more than 2^15
+ *             columns: 2^48), where they may overflow, or with eps 0 below 2^-60, where they vanish, is not
+ *             normalised.
  *   Bases 16-byte aligned; pitches multiples of 8 (bf16), 4 (fp32), 16 (codes).
  */
 int nvfp4_rmsnorm(const void* x, int32_t x_dtype, int64_t ld_x, const void* residual, int64_t ld_r, int32_t s_dtype,

@@ -1560,7 +1560,9 @@ void launch_linear_thin_rows(const GroupedArgs& g, const Epilogue& e, int m, boo
 // 5120 x 5120, 16 rows 22.2, 22.1, 19.3, 30; 32 23.8, 31, 24.5, 35; 64 26.2, 49, 33, 44;
 // 10240 x 2560, 16 rows 26.6, 18.2, 19.8, 19.0; 32 27.8, 24.8, 24.5, 21.4; 64 30.8, 39, 37, 26.9;
 // 5120 x 2048, 16 rows 10.3, 10.2, 8.6, 12.4; 32 13.9, 13.9, 10.7, 14.6; 64 16.9, 20.9, 14.5, 18.8;
-// 2048 x 8192, 16 rows 17.7, 17.7, 25, 41; one row of 10240 x 2560 14.1, 14.1, 16.5, 17.6.)
+// 2048 x 8192, 16 rows 17.7, 17.7, 25, 41; one row of 10240 x 2560 14.1, 14.1, 16.5, 17.6.
+// Only `p` and one width are compared: 16 rows of 10240 x 2560 take 64 columns, 19.0, in place of
+// parts, 26.6, where tiles of 16 would take 18.2.)
 int wide_columns(const GroupedArgs& g, const Plan& p)
 {
     if (g.T <= 8 || g.T > 64 || 2 * ceil_div(g.N, (int64_t)32) < g.cus) return 1;

@@ -15,8 +15,10 @@
 // bounded error, and a token for which two values that a decision compares lie
 // within that bound is done again in 64 bits by the whole wave, unless they are made of equal
 // logits and biases, as all others within the bound of theirs are.  Ordinary
-// logits have a few such tokens in a thousand; if all are such, 16384 x 256 take 14
-// us (softmax; sigmoid with a bias 43, with groups 57) instead of 11 to 21.
+// logits have a few such tokens in a thousand; if all are such, 16384 x 256 take 33
+// us (softmax; sigmoid with a bias 43, with groups 60) instead of 15 to 16.  The bound
+// grows with the largest finite bias, of whatever sign: one of -100 16 us (groups 22), -1e4 38
+// (51), -1e9 all of them; one of minus infinity costs nothing.
 //
 // The whole numbers carry the expert's index in their low bits, so no two of a
 // token are equal and the k largest come out in order, ties by the lowest
@@ -29,9 +31,9 @@
 // with factors of 1 / (1 + e^-|l|)), scaled by the largest, so that no sum of
 // them vanishes.
 //
-// Bound by instructions, not bytes: 16384 x 128 softmax 6.8 us for the choice (8.4
-// MB of logits are 1.6) and 5.1 for the places, each 2.5 us of starting and
-// ending; 16384 x 256 with groups and a bias 16 and 5.
+// Bound by instructions, not bytes: 16384 x 128 softmax 6.4 us for the choice (8.4
+// MB of logits are 1.6) and 5.2 for the places, each 2.5 us of starting and
+// ending; 16384 x 256 with groups and a bias 13 and 5.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -573,7 +575,7 @@ __device__ __forceinline__ int group_scan(int v, int* waves, int& all)
 // order could show.  One chunk: the places are written here; otherwise its
 // counts, one byte each, and k_route_place writes them.
 // 16 lanes a token up to 256 experts: four tokens share a lane move or a scalar step
-// (4096 x 256: 12.9 us, a wave a token 19.4; 65536 x 256: 49 and 75).
+// (4096 x 256: 11.7 us, a wave a token 18.5; 65536 x 256: 46 and 71).
 template <int L, int P, int kMode>
 __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a)
 {
@@ -1000,9 +1002,9 @@ void launch_route_back_rows(const RouteBackArgs& a, hipStream_t s)
     hipLaunchKernelGGL((k_route_backward<L, P>), dim3((uint32_t)(blocks < most ? blocks : most)), dim3(256), 0, s, a);
 }
 
-// From 256 chunks on one more launch adds up the counts, which each workgroup does
-// for itself below.  (16384 x 256: 14.2 us, by the launch 16.4; 32768 x 256: 27.7
-// without it, 27.3 by it, 65536 x 64: 28.6 and 27.6, and each doubling costs more.)
+// Beyond 256 chunks one more launch adds up the counts, which each workgroup does
+// for itself up to there.  (16384 x 256, 256 chunks: 15.6 us, by the launch 17.7; 32768 x 256: 26.0
+// without it, 25.8 by it; 65536 x 64: 30.2 and 27.1; 65536 x 256: 57 and 46.)
 bool sums_apart(int64_t chunks) { return chunks > 256; }
 
 // Bytes of a chunk's counts: 16 experts a lane, a power of two of lanes.
